@@ -79,6 +79,16 @@ __all__ = [
     "linear_nvfp4_quantize",
     "linear_nvfp4_gemm",
     "linear_nvfp4_noalloc",
+    "QuantizedActivation",
+    "rms_norm_quant",
+    "rms_norm_operand",
+    "quant_operand",
+    "linear_fused",
+    "interleave_gate_up",
+    "KVCache8",
+    "kv_append",
+    "attention_kv8",
+    "attention_kv8_plan",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -92,6 +102,22 @@ FMT_FP8_BLOCK = 5
 
 _c_int, _c_i64, _c_f32, _c_vp, _c_sz = (ctypes.c_int, ctypes.c_int64, ctypes.c_float,
                                          ctypes.c_void_p, ctypes.c_size_t)
+
+class KvCacheStruct(ctypes.Structure):
+    """fql_kv_cache."""
+    _fields_ = [("k", _c_vp), ("v", _c_vp), ("k_scale", _c_vp), ("v_scale", _c_vp),
+                ("num_blocks", _c_i64), ("kv_heads", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
+
+
+class KvBatchStruct(ctypes.Structure):
+    """fql_kv_batch."""
+    _fields_ = [("block_table", _c_vp), ("ld_table", _c_i64), ("lens", _c_vp), ("cu_seqlens", _c_vp),
+                ("tokens", _c_i64), ("table_cols", ctypes.c_int32), ("batch", ctypes.c_int32),
+                ("max_new", ctypes.c_int32)]
+
+
+_c_cache, _c_batch = ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvBatchStruct)
 
 # name -> (restype, argtypes); must match include/fql.h
 SIGNATURES = {
@@ -170,6 +196,25 @@ SIGNATURES = {
     "fql_set_plan_override": (_c_int, [_c_int, ctypes.c_char_p]),
     "fql_linear_nvfp4_noalloc": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_f32, _c_int, _c_vp,
                                           _c_i64, _c_f32, _c_vp, _c_vp, _c_i64, _c_vp]),
+    "fql_rms_norm_quant": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp,
+                                    _c_f32, _c_f32, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp]),
+    "fql_operand_bytes": (_c_int, [_c_int, _c_i64, _c_i64, ctypes.POINTER(_c_sz)]),
+    "fql_rms_norm_operand": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp,
+                                      _c_f32, _c_f32, _c_vp, _c_sz, _c_vp, _c_i64, _c_vp]),
+    "fql_quant_operand": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_f32, _c_vp, _c_sz,
+                                   _c_vp]),
+    "fql_linear_fused": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_f32, _c_vp, _c_vp,
+                                  _c_i64, _c_f32, _c_vp, _c_vp, _c_int, _c_vp, _c_i64, _c_vp,
+                                  _c_i64, _c_vp, _c_sz, _c_vp]),
+    "fql_kv_append": (_c_int, [_c_cache, _c_batch, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64,
+                               _c_vp]),
+    "fql_attention_kv8_workspace_bytes": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_i64, _c_i64,
+                                                   _c_int, ctypes.POINTER(_c_sz)]),
+    "fql_attention_kv8_describe": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_i64, _c_i64, _c_int,
+                                            ctypes.c_char_p, _c_sz]),
+    "fql_attention_kv8": (_c_int, [_c_cache, _c_batch, _c_vp, _c_i64, _c_i64, _c_int, _c_f32,
+                                   _c_int, _c_int, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp,
+                                   _c_sz, _c_vp]),
 }
 
 PLAN_OVERRIDES = {"nvfp4": 0, "sc_gemm": 1, "sc_gemv": 2}  # FQL_PLAN_NVFP4, _SC_GEMM, _SC_GEMV
@@ -982,3 +1027,8 @@ def warmup(layers, token_counts, device=None):
             fn(x, w)
             calls += 1
     return calls
+
+
+from .serving import (KVCache8, QuantizedActivation, attention_kv8, attention_kv8_plan,  # noqa: E402
+                      interleave_gate_up, kv_append, linear_fused, quant_operand, rms_norm_operand,
+                      rms_norm_quant)

@@ -33,7 +33,7 @@ CALIB_LIB = os.path.join(HERE, "libfql_calib.so")
 CALIB_SOURCES = ["calib.hip"]
 
 SOURCES = ["fql_api.hip", "quant_nvfp4.hip", "pack_nvfp4.hip", "gemm_nvfp4.hip", "sc_quant.hip",
-           "sc_gemm.hip", "transform_nvfp4.hip"]
+           "sc_gemm.hip", "transform_nvfp4.hip", "norm_quant.hip", "kv_cache.hip", "attn_kv8.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

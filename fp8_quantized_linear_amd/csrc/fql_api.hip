@@ -16,6 +16,7 @@
 
 #include "../../include/fql.h"
 #include "fql_internal.h"
+#include "fql_serving.h"
 
 // ---- launch-plan overrides and per-thread plan caches ------------------------
 
@@ -987,6 +988,293 @@ int fql_linear_nvfp4_noalloc(const void* x, int64_t M, int64_t K, int64_t ldx,
       static_cast<const uint8_t*>(w_packed), N, alpha, static_cast<const uint16_t*>(bias),
       static_cast<uint16_t*>(y), ldy, ws, st);
   return hip_status(e, "linear launch");
+}
+
+}  // extern "C"
+
+// ---- 8-bit serving operators --------------------------------------------------
+
+namespace {
+
+// Runs an entry point's body; a C++ exception (out of host memory) becomes a status.
+template <typename Body>
+int guarded(Body body) {
+  try {
+    return body();
+  } catch (...) {
+    return fail(FQL_ERR_UNSUPPORTED, "out of host memory");
+  }
+}
+
+// FQL_FMT_* -> ScFmt, or -1.
+int sc_format(int format, bool fp4) {
+  switch (format) {
+    case FQL_FMT_MXFP4: return fp4 ? fql::SC_MXFP4 : -1;
+    case FQL_FMT_MXFP8: return fql::SC_MXFP8;
+    case FQL_FMT_FP8: return fql::SC_FP8;
+    case FQL_FMT_FP8_BLOCK: return fql::SC_FP8_BLOCK;
+    default: return -1;
+  }
+}
+
+int inverse_scale(int fmt, float scale, const char* name, float* inv) {
+  *inv = 0.0f;
+  if (fmt != fql::SC_FP8) return FQL_OK;
+  if (int r = check_scale(scale, name)) return r;
+  *inv = std::fmin(1.0f / scale, 3.4028234663852886e38f);  // fl32(1/s), finite
+  return FQL_OK;
+}
+
+int check_operand(int fmt, int64_t M, int64_t K, const void* operand, size_t bytes) {
+  if (!operand) return fail(FQL_ERR_INVALID, "null pointer");
+  if (reinterpret_cast<uintptr_t>(operand) % 256 != 0)
+    return fail(FQL_ERR_INVALID, "operand must be 256-byte aligned");
+  const size_t need = (size_t)fql::operand_dims(fmt, M, K).total_bytes();
+  if (bytes < need) return fail(FQL_ERR_INVALID, "operand holds %zu bytes, %zu needed", bytes, need);
+  return FQL_OK;
+}
+
+int rms_norm(int format, bool to_operand, const void* x, int64_t M, int64_t K, int64_t ldx, const void* residual,
+             int64_t ldr, const void* weight, float eps, float scale, uint8_t* codes, void* scales,
+             size_t operand_bytes, void* h_out, int64_t ldh, void* stream) {
+  const int fmt = sc_format(format, false);
+  if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no 8-bit norm output (MXFP8, FP8, block FP8 have)", format);
+  if (int r = check_sc_shape(fmt, M, K, ldx, "M", false)) return r;
+  if (!x || !weight || !codes || (!to_operand && fmt != fql::SC_FP8 && !scales))
+    return fail(FQL_ERR_INVALID, "null pointer");
+  if (residual && ldr < K) return fail(FQL_ERR_INVALID, "residual row stride %lld is smaller than K", (long long)ldr);
+  if (h_out && !residual) return fail(FQL_ERR_INVALID, "h_out needs a residual");
+  if (h_out && ldh < K) return fail(FQL_ERR_INVALID, "h_out row stride %lld is smaller than K", (long long)ldh);
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(FQL_ERR_INVALID, "eps must be finite and >= 0");
+  fql::NormArgs a{};
+  if (int r = inverse_scale(fmt, scale, "scale", &a.inv_scale)) return r;
+  if (to_operand) {
+    if (int r = check_operand(fmt, M, K, codes, operand_bytes)) return r;
+    scales = codes + fql::operand_dims(fmt, M, K).code_bytes;
+  } else if (reinterpret_cast<uintptr_t>(codes) % 8 != 0 ||
+             (fmt == fql::SC_FP8_BLOCK && reinterpret_cast<uintptr_t>(scales) % 4 != 0)) {
+    return fail(FQL_ERR_INVALID, "codes must be 8-byte and float scales 4-byte aligned");
+  }
+  a.x = static_cast<const uint16_t*>(x);
+  a.M = M;
+  a.K = K;
+  a.ldx = ldx;
+  a.residual = static_cast<const uint16_t*>(residual);
+  a.ldr = ldr;
+  a.weight = static_cast<const uint16_t*>(weight);
+  a.eps = eps;
+  a.codes = codes;
+  a.scales = scales;
+  a.h = static_cast<uint16_t*>(h_out);
+  a.ldh = ldh;
+  return hip_status(fql::launch_rms_norm_quant(fmt, to_operand, a, static_cast<hipStream_t>(stream)),
+                    "norm launch");
+}
+
+int check_cache(const fql_kv_cache* c, const fql_kv_batch* b, fql::PagedCache* pc, fql::PagedBatch* pb) {
+  if (!c || !b) return fail(FQL_ERR_INVALID, "null pointer");
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale) return fail(FQL_ERR_INVALID, "null cache pointer");
+  if (reinterpret_cast<uintptr_t>(c->k) % 16 != 0 || reinterpret_cast<uintptr_t>(c->v) % 16 != 0)
+    return fail(FQL_ERR_INVALID, "cache codes must be 16-byte aligned");
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(FQL_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", c->head_dim);
+  const int bs = c->block_size;
+  if (bs < 16 || bs > 256 || (bs & (bs - 1)) != 0)
+    return fail(FQL_ERR_UNSUPPORTED, "block_size must be 16, 32, 64, 128 or 256 (got %d)", bs);
+  if (c->kv_heads < 1 || c->kv_heads > 4096) return fail(FQL_ERR_INVALID, "kv_heads must be in 1 .. 4096");
+  if (c->num_blocks < 1 || c->num_blocks > INT32_MAX) return fail(FQL_ERR_INVALID, "num_blocks out of range");
+  if (b->batch < 1 || b->batch > 65535) return fail(FQL_ERR_INVALID, "batch must be in 1 .. 65535 (got %d)", b->batch);
+  if (!b->block_table || !b->lens || !b->cu_seqlens) return fail(FQL_ERR_INVALID, "null batch pointer");
+  if (b->table_cols < 1 || b->ld_table < b->table_cols)
+    return fail(FQL_ERR_INVALID, "block_table needs 1 <= table_cols <= ld_table");
+  if ((int64_t)b->table_cols * bs > (int64_t)1 << 30) return fail(FQL_ERR_INVALID, "more than 2^30 tokens a sequence");
+  if (b->tokens < 0 || b->tokens > (int64_t)1 << 30) return fail(FQL_ERR_INVALID, "tokens out of range");
+  if (b->max_new < 0 || b->max_new > 1 << 24) return fail(FQL_ERR_INVALID, "max_new must be in 0 .. 2^24");
+  *pc = fql::PagedCache{c->k, c->v, c->k_scale, c->v_scale, c->num_blocks, c->kv_heads, bs, c->head_dim};
+  *pb = fql::PagedBatch{b->block_table, b->ld_table, b->table_cols, b->lens, b->cu_seqlens, b->batch, b->tokens, b->max_new};
+  return FQL_OK;
+}
+
+int check_attention(int batch, int Hq, int Hkv, int D, int64_t max_new, int64_t max_len, int window) {
+  if (batch < 1 || Hkv < 1 || Hkv > 4096 || Hq < Hkv || Hq % Hkv != 0 || Hq > 1 << 20)
+    return fail(FQL_ERR_INVALID, "q_heads must be a positive multiple of kv_heads (got %d, %d)", Hq, Hkv);
+  if (D != 64 && D != 128 && D != 256) return fail(FQL_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", D);
+  if (batch > 65535) return fail(FQL_ERR_INVALID, "batch must be in 1 .. 65535 (got %d)", batch);
+  if (max_new < 0 || max_new > 1 << 24) return fail(FQL_ERR_INVALID, "max_new must be in 0 .. 2^24");
+  if (max_len < 1 || max_len > (int64_t)1 << 30) return fail(FQL_ERR_INVALID, "max_len must be in 1 .. 2^30");
+  if (window < 0) return fail(FQL_ERR_INVALID, "window must be >= 0");
+  const fql::AttnPlan p = fql::plan_attention(batch, Hq, Hkv, D, max_new, max_len, window);
+  if (max_new * (Hq / Hkv) > (int64_t)1 << 30 || (int64_t)p.row_tiles * p.splits > 65535)
+    return fail(FQL_ERR_UNSUPPORTED, "too many query rows in one call");
+  return FQL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fql_rms_norm_quant(int format, const void* x, int64_t M, int64_t K, int64_t ldx, const void* residual,
+                       int64_t ldr, const void* weight, float eps, float scale, uint8_t* codes, void* scales,
+                       void* h_out, int64_t ldh, void* stream) {
+  return guarded([&] {
+    return rms_norm(format, false, x, M, K, ldx, residual, ldr, weight, eps, scale, codes, scales, 0, h_out, ldh, stream);
+  });
+}
+
+int fql_operand_bytes(int format, int64_t M, int64_t K, size_t* bytes) {
+  return guarded([&] {
+    const int fmt = sc_format(format, true);
+    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no operand", format);
+    if (!bytes) return fail(FQL_ERR_INVALID, "null pointer");
+    if (int r = check_sc_shape(fmt, M, K, K, "M", false)) return r;
+    *bytes = (size_t)fql::operand_dims(fmt, M, K).total_bytes();
+    return ok();
+  });
+}
+
+int fql_rms_norm_operand(int format, const void* x, int64_t M, int64_t K, int64_t ldx, const void* residual,
+                         int64_t ldr, const void* weight, float eps, float scale, void* operand,
+                         size_t operand_bytes, void* h_out, int64_t ldh, void* stream) {
+  return guarded([&] {
+    return rms_norm(format, true, x, M, K, ldx, residual, ldr, weight, eps, scale, static_cast<uint8_t*>(operand),
+                    nullptr, operand_bytes, h_out, ldh, stream);
+  });
+}
+
+int fql_quant_operand(int format, const void* x, int64_t M, int64_t K, int64_t ldx, float scale, void* operand,
+                      size_t operand_bytes, void* stream) {
+  return guarded([&] {
+    const int fmt = sc_format(format, true);
+    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no operand", format);
+    if (int r = check_sc_shape(fmt, M, K, ldx, "M", false)) return r;
+    if (!x) return fail(FQL_ERR_INVALID, "null pointer");
+    float inv = 0.0f;
+    if (int r = inverse_scale(fmt, scale, "scale", &inv)) return r;
+    if (int r = check_operand(fmt, M, K, operand, operand_bytes)) return r;
+    uint8_t* codes = static_cast<uint8_t*>(operand);
+    return hip_status(
+        fql::launch_sc_quant_operand(fmt, static_cast<const uint16_t*>(x), M, K, ldx, aligned16(x, ldx, 2), inv,
+                                     fql::round_up(M, 16), codes, codes + fql::operand_dims(fmt, M, K).code_bytes,
+                                     static_cast<hipStream_t>(stream)),
+        "quant launch");
+  });
+}
+
+int fql_linear_fused(int format, const void* x, int64_t M, int64_t K, int64_t ldx, float input_scale,
+                     const void* x_operand, const void* w_packed, int64_t N, float alpha, const float* alpha_dev,
+                     const void* bias, int activation, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    const int fmt = sc_format(format, true);
+    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no fused epilogue (MXFP4, MXFP8, FP8, block FP8 have)", format);
+    if (int r = check_sc_shape(fmt, M, K, x ? ldx : K, "M", false)) return r;
+    if (int r = check_sc_shape(fmt, N, K, K, "N", true)) return r;
+    if (activation < FQL_ACT_NONE || activation > FQL_ACT_SWIGLU) return fail(FQL_ERR_INVALID, "unknown activation %d", activation);
+    if (activation == FQL_ACT_SWIGLU && N % 32 != 0)
+      return fail(FQL_ERR_INVALID, "a gated layer needs N a multiple of 32 (got %lld)", (long long)N);
+    if (!alpha_dev && !std::isfinite(alpha)) return fail(FQL_ERR_INVALID, "alpha must be finite");
+    const int64_t Nout = activation == FQL_ACT_SWIGLU ? N / 2 : N;
+    if (ldy < Nout) return fail(FQL_ERR_INVALID, "ldy %lld is smaller than the %lld output columns", (long long)ldy, (long long)Nout);
+    if (residual && ldr < Nout)
+      return fail(FQL_ERR_INVALID, "residual row stride %lld is smaller than the %lld output columns", (long long)ldr, (long long)Nout);
+    if ((x == nullptr) == (x_operand == nullptr)) return fail(FQL_ERR_INVALID, "give either x or x_operand");
+    if (!w_packed || !y || !workspace) return fail(FQL_ERR_INVALID, "null pointer");
+    if (reinterpret_cast<uintptr_t>(w_packed) % 16 != 0 || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+      return fail(FQL_ERR_INVALID, "packed weight must be 16-byte and workspace 256-byte aligned");
+    if (reinterpret_cast<uintptr_t>(x_operand) % 256 != 0) return fail(FQL_ERR_INVALID, "operand must be 256-byte aligned");
+    float inv = 0.0f;
+    if (x) {
+      if (int r = inverse_scale(fmt, input_scale, "input_scale", &inv)) return r;
+    }
+    const fql::ScPlan plan = fql::cached_plan_sc_gemm(fmt, M, N, K);
+    if (workspace_bytes < (size_t)plan.total_bytes)
+      return fail(FQL_ERR_WORKSPACE, "workspace holds %zu bytes, %lld needed", workspace_bytes, (long long)plan.total_bytes);
+    if (plan.splits > 1 && plan.groups > plan.counter_bytes / 4)
+      return fail(FQL_ERR_INVALID, "too many output tiles for the arrival counters");
+    if (plan.Mp * (plan.groups > 0 ? fql::round_up(K, 128) / 32 : 0) > ((int64_t)1 << 31) - 4096)
+      return fail(FQL_ERR_INVALID, "activation too large");
+    const fql::ScEpilogue epi = {activation, static_cast<const uint16_t*>(residual), ldr};
+    return hip_status(
+        fql::launch_sc_linear_fused(plan, static_cast<const uint16_t*>(x), M, K, ldx, x && aligned16(x, ldx, 2), inv,
+                                    static_cast<const uint8_t*>(x_operand), static_cast<const uint8_t*>(w_packed), N,
+                                    alpha, alpha_dev, static_cast<const uint16_t*>(bias), epi, static_cast<uint16_t*>(y),
+                                    ldy, static_cast<uint8_t*>(workspace), static_cast<hipStream_t>(stream)),
+        "linear launch");
+  });
+}
+
+int fql_kv_append(const fql_kv_cache* cache, const fql_kv_batch* batch, const void* k, int64_t k_ld_token,
+                  int64_t k_ld_head, const void* v, int64_t v_ld_token, int64_t v_ld_head, void* stream) {
+  return guarded([&] {
+    fql::PagedCache c;
+    fql::PagedBatch b;
+    if (int r = check_cache(cache, batch, &c, &b)) return r;
+    if (!k || !v) return fail(FQL_ERR_INVALID, "null pointer");
+    if (k_ld_token < 0 || k_ld_head < 0 || v_ld_token < 0 || v_ld_head < 0) return fail(FQL_ERR_INVALID, "negative stride");
+    if (b.T == 0 || b.max_new == 0) return ok();
+    const bool al = aligned16(k, k_ld_token, 2) && aligned16(v, v_ld_token, 2) && (k_ld_head | v_ld_head) % 8 == 0;
+    return hip_status(fql::launch_kv_append(c, b, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v),
+                                            k_ld_token, k_ld_head, v_ld_token, v_ld_head, al,
+                                            static_cast<hipStream_t>(stream)),
+                      "append launch");
+  });
+}
+
+int fql_attention_kv8_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim, int64_t max_new,
+                                      int64_t max_len, int window, size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) return fail(FQL_ERR_INVALID, "null pointer");
+    if (int r = check_attention(batch, q_heads, kv_heads, head_dim, max_new, max_len, window)) return r;
+    *bytes = (size_t)fql::plan_attention(batch, q_heads, kv_heads, head_dim, max_new, max_len, window).total_bytes;
+    return ok();
+  });
+}
+
+int fql_attention_kv8_describe(int batch, int q_heads, int kv_heads, int head_dim, int64_t max_new, int64_t max_len,
+                               int window, char* buf, size_t buf_len) {
+  return guarded([&] {
+    if (int r = check_attention(batch, q_heads, kv_heads, head_dim, max_new, max_len, window)) return r;
+    write_reason(buf, buf_len,
+                 fql::describe_attention(
+                     fql::plan_attention(batch, q_heads, kv_heads, head_dim, max_new, max_len, window), head_dim));
+    return ok();
+  });
+}
+
+int fql_attention_kv8(const fql_kv_cache* cache, const fql_kv_batch* batch, const void* q, int64_t q_ld_token,
+                      int64_t q_ld_head, int q_heads, float scale, int causal, int window, int64_t max_len, void* out,
+                      int64_t o_ld_token, int64_t o_ld_head, float* lse, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  return guarded([&] {
+    fql::PagedCache c;
+    fql::PagedBatch b;
+    if (int r = check_cache(cache, batch, &c, &b)) return r;
+    if (int r = check_attention(b.B, q_heads, c.heads, c.D, b.max_new, max_len, window)) return r;
+    if (!q || !out || !workspace) return fail(FQL_ERR_INVALID, "null pointer");
+    if (q_ld_token < 0 || q_ld_head < 0 || o_ld_token < 0 || o_ld_head < 0) return fail(FQL_ERR_INVALID, "negative stride");
+    if (!std::isfinite(scale)) return fail(FQL_ERR_INVALID, "scale must be finite");
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return fail(FQL_ERR_INVALID, "workspace must be 256-byte aligned");
+    if (b.T == 0 || b.max_new == 0) return ok();
+    const fql::AttnPlan plan = fql::plan_attention(b.B, q_heads, c.heads, c.D, b.max_new, max_len, window);
+    if (workspace_bytes < (size_t)plan.total_bytes)
+      return fail(FQL_ERR_WORKSPACE, "workspace holds %zu bytes, %lld needed", workspace_bytes, (long long)plan.total_bytes);
+    fql::AttnArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.q_ld_token = q_ld_token;
+    a.q_ld_head = q_ld_head;
+    a.out = static_cast<uint16_t*>(out);
+    a.o_ld_token = o_ld_token;
+    a.o_ld_head = o_ld_head;
+    a.lse = lse;
+    a.Hq = q_heads;
+    a.scale = scale;
+    a.causal = causal != 0;
+    a.window = window;
+    a.aligned = aligned16(q, q_ld_token, 2) && q_ld_head % 8 == 0;
+    return hip_status(fql::launch_attention(plan, a, c, b, static_cast<uint8_t*>(workspace),
+                                            static_cast<hipStream_t>(stream)),
+                      "attention launch");
+  });
 }
 
 }  // extern "C"

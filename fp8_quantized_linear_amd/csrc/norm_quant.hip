@@ -1,0 +1,249 @@
+// Residual addition + root-mean-square norm + 8-bit quantizer, one pass
+// (gfx950): the input of an 8-bit linear layer straight from the residual
+// stream.
+//
+//   h = x + residual                       (float32; written back as bf16)
+//   y = h * (1 / sqrt(mean(h^2) + eps)) * w
+//   codes, scales = the linear layers' quantizer on y (per-tensor FP8, block
+//   FP8 or MXFP8; quant_block8 below)
+//
+// Roundings: h is rounded to bf16 only where it is stored; the norm and the
+// quantizer take the unrounded float32 sum, so a code carries one rounding.
+// The sum of squares is float32: per thread in element order, then a tree.
+#include "fql_device.h"
+#include "fql_serving.h"
+#include "sc_quant.h"
+
+namespace fql {
+
+namespace {
+
+// Eight consecutive values of a row.
+struct Vec8 {
+  float v[8];
+};
+__device__ __forceinline__ Vec8 load8(const uint16_t* p, bool aligned) {
+  Vec8 r;
+  if (aligned) {
+    const uint4v u = *reinterpret_cast<const uint4v*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r.v[2 * j] = __uint_as_float(w[j] << 16);
+      r.v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.v[j] = bf16_bits_to_f32(p[j]);
+  }
+  return r;
+}
+__device__ __forceinline__ void store8(uint16_t* p, const Vec8& r, bool aligned) {
+  if (aligned) {
+    uint4v u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      u[j] = f32_to_bf16_bits(r.v[2 * j]) | (f32_to_bf16_bits(r.v[2 * j + 1]) << 16);
+    *reinterpret_cast<uint4v*>(p) = u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = (uint16_t)f32_to_bf16_bits(r.v[j]);
+  }
+}
+
+// Codes of eight consecutive values (two words) and the scale of their block.
+// A block of 32 (MXFP8) or 128 (block FP8) values is held by 4 or 16
+// neighbouring lanes, all of which must call this.
+template <int F>
+__device__ __forceinline__ void quant_block8(const Vec8& y, float inv_scale, uint32_t w[2], uint32_t& sbyte,
+                                             float& gscale) {
+#pragma clang fp contract(off)
+  float f = inv_scale;
+  if (F != SC_FP8) {
+    float a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = __builtin_fmaxf(a, __builtin_fabsf(y.v[j]));
+    a = __builtin_fmaxf(a, __shfl_xor(a, 1));
+    a = __builtin_fmaxf(a, __shfl_xor(a, 2));
+    if (F == SC_FP8_BLOCK) {
+      a = __builtin_fmaxf(a, __shfl_xor(a, 4));
+      a = __builtin_fmaxf(a, __shfl_xor(a, 8));
+      gscale = a / 448.0f;
+      f = safe_reciprocal(gscale);
+    } else {
+      const int e = mx_exponent(a, 8);
+      sbyte = (uint32_t)(e + 127);
+      f = pow2_neg(e);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    w[j] = fp8x4(y.v[4 * j] * f, y.v[4 * j + 1] * f, y.v[4 * j + 2] * f, y.v[4 * j + 3] * f);
+}
+
+// Row-independent addressing of one workgroup's row.
+struct NormFlags {
+  bool x, r, w, h;  // 16-byte aligned rows
+};
+
+// Where the eight codes of columns 8v .. 8v+7 of row m go, with their scale.
+template <int F, bool OP>
+__device__ __forceinline__ void store_codes(const NormArgs& a, int64_t m, int64_t v, const uint32_t w[2],
+                                            uint32_t sbyte, float gscale) {
+  const int64_t k = 8 * v;
+  uint64_t word = (uint64_t)w[0] | ((uint64_t)w[1] << 32);
+  if (!OP) {
+    *reinterpret_cast<uint64_t*>(a.codes + m * a.K + k) = word;
+    if (F == SC_MXFP8 && (v & 3) == 0) static_cast<uint8_t*>(a.scales)[m * (a.K / 32) + k / 32] = (uint8_t)sbyte;
+    if (F == SC_FP8_BLOCK && (v & 15) == 0) static_cast<float*>(a.scales)[m * (a.K / 128) + k / 128] = gscale;
+  } else {
+    // 16-element piece h16 of chunk c: half h16 / 4, lane (h16 % 4) * 16 + m % 16
+    const int64_t KC = (a.K + 127) / 128, c = k / 128, tile = m / 16, quad = m / 64;
+    const int r = (int)(m % 16), h16 = (int)(k % 128) / 16;
+    uint8_t* dst = a.codes + (tile * KC + c) * 2048 + (h16 / 4) * 1024 + ((h16 % 4) * 16 + r) * 16 + k % 16;
+    *reinterpret_cast<uint64_t*>(dst) = word;
+    if (F == SC_MXFP8 && (v & 3) == 0)
+      static_cast<uint8_t*>(a.scales)[((quad * KC + c) * 64 + (h16 / 2) * 16 + r) * 4 + (int)(m / 16) % 4] =
+          (uint8_t)sbyte;
+    if (F == SC_FP8_BLOCK && (v & 15) == 0) static_cast<float*>(a.scales)[(quad * KC + c) * 64 + m % 64] = gscale;
+  }
+}
+
+// h = x + residual of one vector, stored back where there is a residual.
+__device__ __forceinline__ Vec8 load_h(const NormArgs& a, const NormFlags& f, int64_t m, int64_t v, bool store) {
+  Vec8 h = load8(a.x + m * a.ldx + 8 * v, f.x);
+  if (a.residual != nullptr) {
+    const Vec8 r = load8(a.residual + m * a.ldr + 8 * v, f.r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h.v[j] += r.v[j];
+    if (store && a.h != nullptr) store8(a.h + m * a.ldh + 8 * v, h, f.h);
+  }
+  return h;
+}
+
+template <int F, bool OP>
+__device__ __forceinline__ void finish_vec(const NormArgs& a, const NormFlags& f, int64_t m, int64_t v, int64_t nv,
+                                           int64_t nvp, const Vec8& h, float rinv) {
+#pragma clang fp contract(off)
+  Vec8 y;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y.v[j] = 0.0f;
+  if (v < nv) {
+    const Vec8 w = load8(a.weight + 8 * v, f.w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y.v[j] = h.v[j] * rinv * w.v[j];
+  }
+  uint32_t q[2], sb = 0;
+  float gs = 0.0f;
+  quant_block8<F>(y, a.inv_scale, q, sb, gs);
+  if (OP && v >= nv) sb = 0;  // padding up to the chunk: zero codes, zero scale bytes
+  if (v < (OP ? nvp : nv)) store_codes<F, OP>(a, m, v, q, sb, gs);
+}
+
+// One row per workgroup (WAVE: per wave, four rows a workgroup), its values in
+// registers: vector v = t + T * i of thread t (T threads a row, I vectors a
+// thread). STREAM: rows too long for that read x and the residual twice.
+template <int F, bool OP, int I, bool WAVE, bool STREAM>
+__global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, const NormFlags f) {
+  __shared__ float red[16];
+  int64_t m;
+  int t, T;
+  if (WAVE) {
+    m = (int64_t)blockIdx.x * (blockDim.x / 64) + threadIdx.x / 64;
+    t = threadIdx.x & 63;
+    T = 64;
+    if (m >= a.M) return;
+  } else {
+    m = blockIdx.x;
+    // The operand interleaves 16 rows in every 256-byte run, so a row's stores
+    // are 16-byte pieces. The workgroups of one 16-row tile are placed on one
+    // XCD (workgroups go to the eight XCDs in turn), whose L2 then joins the
+    // pieces into whole lines.
+    if (OP) m = ((m / 128) * 8 + m % 8) * 16 + (m / 8) % 16;
+    t = threadIdx.x;
+    T = blockDim.x;
+    if (m >= a.M) return;
+  }
+  const int64_t nv = a.K / 8, nvp = OP ? (a.K + 127) / 128 * 16 : nv;
+  Vec8 h[I];
+  float ss = 0.0f;
+  if (!STREAM) {
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int64_t v = t + (int64_t)T * i;
+      if (v < nv) h[i] = load_h(a, f, m, v, true);
+      else
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i].v[j] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += h[i].v[j] * h[i].v[j];
+    }
+  } else {
+    for (int64_t v = t; v < nv; v += T) {
+      const Vec8 u = load_h(a, f, m, v, false);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += u.v[j] * u.v[j];
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) ss += __shfl_xor(ss, o);
+  if (!WAVE) {
+    if ((t & 63) == 0) red[t >> 6] = ss;
+    __syncthreads();
+    ss = 0.0f;
+    for (int i = 0; i < T / 64; ++i) ss += red[i];
+  }
+  const float rinv = 1.0f / __builtin_sqrtf(ss / (float)a.K + a.eps);
+  if (!STREAM) {
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      // whole groups of T vectors, so that every lane of a block takes part
+      if ((int64_t)T * i < nvp) finish_vec<F, OP>(a, f, m, t + (int64_t)T * i, nv, nvp, h[i], rinv);
+    }
+  } else {
+    for (int64_t v0 = 0; v0 < nvp; v0 += T) {
+      const int64_t v = v0 + t;
+      Vec8 u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u.v[j] = 0.0f;
+      if (v < nv) u = load_h(a, f, m, v, true);
+      finish_vec<F, OP>(a, f, m, v, nv, nvp, u, rinv);
+    }
+  }
+}
+
+bool row_aligned(const void* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+
+template <int F, bool OP>
+hipError_t launch_t(const NormArgs& a, hipStream_t st) {
+  const NormFlags f = {row_aligned(a.x, a.ldx), row_aligned(a.residual, a.ldr), row_aligned(a.weight, 0),
+                       row_aligned(a.h, a.ldh)};
+  const int64_t nv = OP ? (a.K + 127) / 128 * 16 : a.K / 8;
+#define FQL_LAUNCH(I, W, S, grid, threads) \
+  rms_norm_quant_kernel<F, OP, I, W, S><<<(unsigned)(grid), (unsigned)(threads), 0, st>>>(a, f)
+  if (nv <= 128 && a.M > 1) {
+    FQL_LAUNCH(2, true, false, (a.M + 3) / 4, 256);
+    return hipGetLastError();
+  }
+  const int64_t rows = OP ? round_up(a.M, 128) : a.M;
+  const int64_t per = nv <= 1024 ? 2 : nv <= 2048 ? 4 : 8;  // vectors a thread
+  const int64_t threads = round_up((nv + per - 1) / per, 64);
+  if (nv > 8192) FQL_LAUNCH(1, false, true, rows, 1024);
+  else if (per == 2) FQL_LAUNCH(2, false, false, rows, threads);
+  else if (per == 4) FQL_LAUNCH(4, false, false, rows, threads);
+  else FQL_LAUNCH(8, false, false, rows, threads);
+#undef FQL_LAUNCH
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm_quant(int fmt, bool operand, const NormArgs& a, hipStream_t st) {
+#define FQL_F(F) \
+  if (fmt == F) return operand ? launch_t<F, true>(a, st) : launch_t<F, false>(a, st);
+  FQL_F(SC_FP8) FQL_F(SC_FP8_BLOCK) FQL_F(SC_MXFP8)
+#undef FQL_F
+  return hipErrorInvalidValue;
+}
+
+}  // namespace fql

@@ -26,6 +26,8 @@
 #include "fql_device.h"
 #include "fql_gemm.h"
 #include "fql_internal.h"
+#include "fql_serving.h"
+#include "sc_epilogue.h"
 #include "sc_quant.h"
 
 namespace fql {
@@ -93,14 +95,16 @@ __device__ __forceinline__ float4v mfma_scale_sel(const int8v& a, const int8v& b
   }
 }
 
-template <int F, int WM, int WN, int MTW, int NTW, int ST>
+// EX: the fused epilogue of sc_epilogue.h (activation, residual) in place of
+// alpha * acc + bias; the products and their order are the same.
+template <int F, int WM, int WN, int MTW, int NTW, int ST, bool EX = false>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_sc_kernel(
     const uint8_t* __restrict__ xcodes, const uint8_t* __restrict__ xscales,
     const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, int M, int N,
     int64_t KC, int ntiles_w, int64_t quads_w, int ngroups, int kc_per_split, int dp, int splits,
     float alpha, const float* __restrict__ alpha_dev, const uint16_t* __restrict__ bias,
-    uint16_t* __restrict__ y, int64_t ldy, float4v* __restrict__ partial,
-    uint32_t* __restrict__ counters) {
+    uint16_t* y, int64_t ldy, float4v* __restrict__ partial, uint32_t* __restrict__ counters,
+    const ScEpilogue epi) {
   if (alpha_dev != nullptr) alpha = *alpha_dev;  // output scale kept in device memory
   typedef ScTraits<F> T;
   typedef ScStage<F, WM, WN, MTW, NTW> Stage;
@@ -441,7 +445,30 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_sc_kernel(
   // (and its 16-byte pieces divide evenly among the threads)
   constexpr bool kStaged = sizeof(stage) >= (size_t)TA * 16 * StagedPitch<TB * 16>::P * 2 &&
                            (TA * 16 * TB * 16 / 8) % (64 * NW) == 0;
-  if constexpr (kStaged) {
+  if constexpr (EX) {
+    const EpiOut o = {M, N, alpha, bias, epi, y, ldy};
+    // the gated tile's half as many pieces have to divide evenly too
+    if constexpr (kStaged && (TA * 16 * TB * 16 / 16) % (64 * NW) == 0) {
+      if (nsplit == 1) {
+        __syncthreads();  // every wave's loads have landed: the ring is free
+        uint16_t* lds = reinterpret_cast<uint16_t*>(&stage[0]);
+        if (o.gated()) write_tile16_staged_fused<MTW, NTW, WM, WN, true>(acc, m0, n0, wm, wn, o, lds);
+        else write_tile16_staged_fused<MTW, NTW, WM, WN, false>(acc, m0, n0, wm, wn, o, lds);
+        return;
+      }
+    }
+    float4v frag[P];
+#pragma unroll
+    for (int mt = 0; mt < MTW; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NTW; ++nt) frag[mt * NTW + nt] = acc[mt][nt];
+    auto row_of = [&](int f, int i) { return (wm * MTW + f / NTW) * 16 + 4 * (lane >> 4) + i; };
+    auto col_of = [&](int f) { return (wn * NTW + f % NTW) * 16 + (lane & 15); };
+    float4v* slab = partial + (int64_t)sslot * splits * (NW * P * 64);
+    finish_frags_fused<P, decltype(row_of), decltype(col_of), NW>(frag, row_of, col_of, m0, n0, split, nsplit, o,
+                                                                  slab, counters + sslot, &s_flag);
+    return;
+  } else if constexpr (kStaged) {
     if (nsplit == 1) {
       __syncthreads();  // every wave's loads have landed: the ring is free
       write_tile16_staged<MTW, NTW, WM, WN>(acc, M, N, m0, n0, wm, wn, alpha, bias, y, ldy,
@@ -512,13 +539,13 @@ struct ScvStage<F, MT, NT, 1> {
 // of rows >= M read row 0 (an output row depends only on its own activation
 // row and rows >= M are never stored). The ring then carries only the
 // weight. This removes the separate quantizer launch for decode sizes.
-template <int F, int W, int MT, int NT, int D, int FQ>
+template <int F, int W, int MT, int NT, int D, int FQ, bool EX = false>
 __global__ __launch_bounds__(64 * W) void gemv_sc_kernel(
     const uint8_t* __restrict__ xcodes, const uint8_t* __restrict__ xscales,
     const uint8_t* __restrict__ wcodes, const uint8_t* __restrict__ wscales, int M, int N,
     int64_t KC, int ntiles_w, int64_t quads_w, float alpha, const float* __restrict__ alpha_dev,
-    const uint16_t* __restrict__ bias, uint16_t* __restrict__ y, int64_t ldy,
-    const uint16_t* __restrict__ x, int64_t ldx, int aligned, float inv_scale, int64_t K) {
+    const uint16_t* __restrict__ bias, uint16_t* y, int64_t ldy, const uint16_t* __restrict__ x,
+    int64_t ldx, int aligned, float inv_scale, int64_t K, const ScEpilogue epi) {
   if (alpha_dev != nullptr) alpha = *alpha_dev;  // output scale kept in device memory
   typedef ScTraits<F> T;
   typedef ScvStage<F, MT, NT, FQ> Stage;
@@ -727,6 +754,23 @@ __global__ __launch_bounds__(64 * W) void gemv_sc_kernel(
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) red[wave][mt * NT + nt][lane] = acc[mt][nt];
   __syncthreads();
+  if constexpr (EX) {
+    // pairs of neighbouring column tiles, for the gated activation
+    static_assert(NT % 2 == 0, "column tile pairs");
+    const EpiOut o = {M, N, alpha, bias, epi, y, ldy};
+#pragma unroll
+    for (int f = 0; f < MT * NT; f += 2) {
+      if ((f / 2) % W != wave) continue;
+      float4v a = red[0][f][lane], b = red[0][f + 1][lane];
+#pragma unroll
+      for (int w = 1; w < W; ++w) {
+        a += red[w][f][lane];
+        b += red[w][f + 1][lane];
+      }
+      o.emit_pair(a, b, (f / NT) * 16 + 4 * (lane >> 4), (int)((tile0 + f % NT) * 16) + (lane & 15));
+    }
+    return;
+  }
 #pragma unroll
   for (int f = 0; f < MT * NT; ++f) {
     if (f % W != wave) continue;
@@ -951,88 +995,128 @@ std::string describe_sc_plan(const ScPlan& p) {
   return std::string(b);
 }
 
+// The rest of one call: output scale, bias, output and the fused epilogue
+// (null: the plain kernels).
+struct ScOut {
+  float alpha;
+  const float* alpha_dev;
+  const uint16_t* bias;
+  uint16_t* y;
+  int64_t ldy;
+  const ScEpilogue* epi;
+};
+
 template <int F, int WM, int WN, int MTW, int NTW, int ST>
-static hipError_t launch_sc_t(const ScPlan& p, const uint8_t* xc, const uint8_t* xs,
-                              const uint8_t* packed, const ScDims& w, int64_t M, int64_t N,
-                              float alpha, const float* alpha_dev, const uint16_t* bias, uint16_t* y,
-                              int64_t ldy, float4v* partial, uint32_t* counters, hipStream_t st) {
+static hipError_t launch_sc_t(const ScPlan& p, const uint8_t* xc, const uint8_t* xs, const uint8_t* packed,
+                              const ScDims& w, int64_t M, int64_t N, const ScOut& o, float4v* partial,
+                              uint32_t* counters, hipStream_t st) {
   if constexpr (!sc_config_fits<F, WM, WN, MTW, NTW, ST>()) {
     return hipErrorInvalidValue;
   } else {
     const int64_t grid = p.dp_groups + (p.groups - p.dp_groups) * p.splits;
-    gemm_sc_kernel<F, WM, WN, MTW, NTW, ST><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(
-        xc, xs, packed, packed + w.code_bytes, (int)M, (int)N, w.KC, (int)(w.rows_p / 16), w.quads,
-        (int)p.ngroups, p.kc_per_split, (int)p.dp_groups, p.splits, alpha, alpha_dev, bias, y, ldy,
-        partial, counters);
+#define FQL_GEMM(EX, E)                                                                              \
+  gemm_sc_kernel<F, WM, WN, MTW, NTW, ST, EX><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(              \
+      xc, xs, packed, packed + w.code_bytes, (int)M, (int)N, w.KC, (int)(w.rows_p / 16), w.quads,    \
+      (int)p.ngroups, p.kc_per_split, (int)p.dp_groups, p.splits, o.alpha, o.alpha_dev, o.bias, o.y, \
+      o.ldy, partial, counters, E)
+    if (o.epi != nullptr) FQL_GEMM(true, *o.epi);
+    else FQL_GEMM(false, ScEpilogue{});
+#undef FQL_GEMM
     return hipGetLastError();
   }
 }
 
 template <int F, int W, int MT, int NT, int D>
-static hipError_t launch_scv_t(const ScPlan& p, const uint8_t* xc, const uint8_t* xs,
-                               const uint8_t* packed, const ScDims& w, int64_t M, int64_t N,
-                               float alpha, const float* alpha_dev, const uint16_t* bias,
-                               uint16_t* y, int64_t ldy, hipStream_t st) {
+static hipError_t launch_scv_t(const ScPlan& p, const uint8_t* xc, const uint8_t* xs, const uint8_t* packed,
+                               const ScDims& w, int64_t M, int64_t N, const ScOut& o, hipStream_t st) {
   if constexpr (!scv_config_fits<F, W, MT, NT, D>()) {
     return hipErrorInvalidValue;
   } else {
-    gemv_sc_kernel<F, W, MT, NT, D, 0><<<(unsigned)p.groups, 64 * W, 0, st>>>(
-        xc, xs, packed, packed + w.code_bytes, (int)M, (int)N, w.KC, (int)(w.rows_p / 16), w.quads,
-        alpha, alpha_dev, bias, y, ldy, nullptr, 0, 0, 0.0f, 0);
+#define FQL_GEMV(EX, E)                                                                            \
+  gemv_sc_kernel<F, W, MT, NT, D, 0, EX><<<(unsigned)p.groups, 64 * W, 0, st>>>(                   \
+      xc, xs, packed, packed + w.code_bytes, (int)M, (int)N, w.KC, (int)(w.rows_p / 16), w.quads,  \
+      o.alpha, o.alpha_dev, o.bias, o.y, o.ldy, nullptr, 0, 0, 0.0f, 0, E)
+    if (o.epi != nullptr) FQL_GEMV(true, *o.epi);
+    else FQL_GEMV(false, ScEpilogue{});
+#undef FQL_GEMV
     return hipGetLastError();
   }
 }
 
 template <int F, int W, int MT, int NT, int D>
-static hipError_t launch_scv_fused_t(const ScPlan& p, const uint16_t* x, int64_t ldx, bool aligned,
-                                     float inv_scale, int64_t K, const uint8_t* packed,
-                                     const ScDims& w, int64_t M, int64_t N, float alpha,
-                                     const float* alpha_dev, const uint16_t* bias, uint16_t* y,
-                                     int64_t ldy, hipStream_t st) {
+static hipError_t launch_scv_fused_t(const ScPlan& p, const uint16_t* x, int64_t ldx, bool aligned, float inv_scale,
+                                     int64_t K, const uint8_t* packed, const ScDims& w, int64_t M, int64_t N,
+                                     const ScOut& o, hipStream_t st) {
   if (p.dyn_lds <= 0 || M > 16 * MT) return hipErrorInvalidValue;
-  gemv_sc_kernel<F, W, MT, NT, D, 1><<<(unsigned)p.groups, 64 * W, (size_t)p.dyn_lds, st>>>(
-      nullptr, nullptr, packed, packed + w.code_bytes, (int)M, (int)N, w.KC, (int)(w.rows_p / 16),
-      w.quads, alpha, alpha_dev, bias, y, ldy, x, ldx, aligned ? 1 : 0, inv_scale, K);
+#define FQL_GEMV(EX, E)                                                                            \
+  gemv_sc_kernel<F, W, MT, NT, D, 1, EX><<<(unsigned)p.groups, 64 * W, (size_t)p.dyn_lds, st>>>(   \
+      nullptr, nullptr, packed, packed + w.code_bytes, (int)M, (int)N, w.KC, (int)(w.rows_p / 16), \
+      w.quads, o.alpha, o.alpha_dev, o.bias, o.y, o.ldy, x, ldx, aligned ? 1 : 0, inv_scale, K, E)
+  if (o.epi != nullptr) FQL_GEMV(true, *o.epi);
+  else FQL_GEMV(false, ScEpilogue{});
+#undef FQL_GEMV
   return hipGetLastError();
+}
+
+// x_operand (nullable): the activation already in operand form.
+static hipError_t launch_sc_any(const ScPlan& p, const uint16_t* x, int64_t M, int64_t K, int64_t ldx, bool aligned,
+                                float inv_scale, const uint8_t* x_operand, const uint8_t* packed, int64_t N,
+                                const ScOut& o, uint8_t* workspace, hipStream_t st) {
+  const ScDims w = sc_dims(p.fmt, N, K, true);
+  uint32_t* counters = reinterpret_cast<uint32_t*>(workspace);
+  uint8_t* const xc_ws = workspace + p.counter_bytes;
+  uint8_t* const xs_ws = xc_ws + p.xcode_bytes;
+  float4v* partial = reinterpret_cast<float4v*>(xs_ws + p.xscale_bytes);
+  if (p.splits > 1 && p.groups - p.dp_groups > p.counter_bytes / 4) return hipErrorInvalidValue;  // counter per split tile
+  const uint8_t* xc = xc_ws;
+  const uint8_t* xs = xs_ws;
+  if (x_operand != nullptr) {
+    xc = x_operand;
+    xs = x_operand + operand_dims(p.fmt, M, K).code_bytes;
+  } else if (p.kind == 1 && p.fq) {
+#define FQL_X(F0, A, B, C, E)                                                                            \
+  if (p.fmt == F0 && p.wn == A && p.mtw == B && p.ntw == C && p.st == E)                                 \
+    return launch_scv_fused_t<F0, A, B, C, E>(p, x, ldx, aligned, inv_scale, K, packed, w, M, N, o, st);
+    FQL_SCV_FUSED_CONFIGS_ALL(FQL_X)
+#undef FQL_X
+    return hipErrorInvalidValue;
+  } else {
+    const hipError_t e = launch_sc_quant_operand(p.fmt, x, M, K, ldx, aligned, inv_scale, p.Mp, xc_ws, xs_ws, st);
+    if (e != hipSuccess) return e;
+  }
+  if (p.kind == 1) {
+#define FQL_X(F0, A, B, C, E)                                            \
+  if (p.fmt == F0 && p.wn == A && p.mtw == B && p.ntw == C && p.st == E) \
+    return launch_scv_t<F0, A, B, C, E>(p, xc, xs, packed, w, M, N, o, st);
+    FQL_SCV_CONFIGS_ALL(FQL_X)
+#undef FQL_X
+    return hipErrorInvalidValue;
+  }
+#define FQL_X(F0, A, B, C, D, E)                                                       \
+  if (p.fmt == F0 && p.wm == A && p.wn == B && p.mtw == C && p.ntw == D && p.st == E)  \
+    return launch_sc_t<F0, A, B, C, D, E>(p, xc, xs, packed, w, M, N, o, partial, counters, st);
+  FQL_SC_CONFIGS_ALL(FQL_X)
+#undef FQL_X
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_sc_linear(const ScPlan& p, const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
                             bool aligned, float inv_scale, const uint8_t* packed, int64_t N,
                             float alpha, const float* alpha_dev, const uint16_t* bias, uint16_t* y,
                             int64_t ldy, uint8_t* workspace, hipStream_t st) {
-  const ScDims w = sc_dims(p.fmt, N, K, true);
-  uint32_t* counters = reinterpret_cast<uint32_t*>(workspace);
-  uint8_t* xc = workspace + p.counter_bytes;
-  uint8_t* xs = xc + p.xcode_bytes;
-  float4v* partial = reinterpret_cast<float4v*>(xs + p.xscale_bytes);
-  if (p.splits > 1 && p.groups - p.dp_groups > p.counter_bytes / 4) return hipErrorInvalidValue;  // counter per split tile
-  if (p.kind == 1 && p.fq) {
-#define FQL_X(F0, A, B, C, E)                                                                      \
-  if (p.fmt == F0 && p.wn == A && p.mtw == B && p.ntw == C && p.st == E)                           \
-    return launch_scv_fused_t<F0, A, B, C, E>(p, x, ldx, aligned, inv_scale, K, packed, w, M, N,    \
-                                              alpha, alpha_dev, bias, y, ldy, st);
-    FQL_SCV_FUSED_CONFIGS_ALL(FQL_X)
-#undef FQL_X
-    return hipErrorInvalidValue;
-  }
-  hipError_t e = launch_sc_quant_operand(p.fmt, x, M, K, ldx, aligned, inv_scale, p.Mp, xc, xs, st);
-  if (e != hipSuccess) return e;
-  if (p.kind == 1) {
-#define FQL_X(F0, A, B, C, E)                                                                      \
-  if (p.fmt == F0 && p.wn == A && p.mtw == B && p.ntw == C && p.st == E)                           \
-    return launch_scv_t<F0, A, B, C, E>(p, xc, xs, packed, w, M, N, alpha, alpha_dev, bias, y, ldy, \
-                                        st);
-    FQL_SCV_CONFIGS_ALL(FQL_X)
-#undef FQL_X
-    return hipErrorInvalidValue;
-  }
-#define FQL_X(F0, A, B, C, D, E)                                                                  \
-  if (p.fmt == F0 && p.wm == A && p.wn == B && p.mtw == C && p.ntw == D && p.st == E)             \
-    return launch_sc_t<F0, A, B, C, D, E>(p, xc, xs, packed, w, M, N, alpha, alpha_dev, bias, y, ldy, \
-                                          partial, counters, st);
-  FQL_SC_CONFIGS_ALL(FQL_X)
-#undef FQL_X
-  return hipErrorInvalidValue;
+  return launch_sc_any(p, x, M, K, ldx, aligned, inv_scale, nullptr, packed, N,
+                       ScOut{alpha, alpha_dev, bias, y, ldy, nullptr}, workspace, st);
+}
+
+hipError_t launch_sc_linear_fused(const ScPlan& p, const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
+                                  bool aligned, float inv_scale, const uint8_t* x_operand,
+                                  const uint8_t* packed, int64_t N, float alpha, const float* alpha_dev,
+                                  const uint16_t* bias, const ScEpilogue& epi, uint16_t* y, int64_t ldy,
+                                  uint8_t* workspace, hipStream_t st) {
+  // no activation and no residual: the plain kernels' epilogue
+  const bool plain = epi.act == kActNone && epi.residual == nullptr;
+  return launch_sc_any(p, x, M, K, ldx, aligned, inv_scale, x_operand, packed, N,
+                       ScOut{alpha, alpha_dev, bias, y, ldy, plain ? nullptr : &epi}, workspace, st);
 }
 
 }  // namespace fql

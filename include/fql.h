@@ -478,6 +478,155 @@ int fql_linear_fp8_block(const void* x, int64_t M, int64_t K, int64_t ldx, const
                          int64_t N, float alpha, const void* bias, void* y, int64_t ldy,
                          void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit serving operators: what stands between the 8-bit linear layers of a
+ * decoder. `format` is FQL_FMT_FP8, FQL_FMT_FP8_BLOCK or FQL_FMT_MXFP8 (the
+ * fused linear call also takes FQL_FMT_MXFP4).
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Residual addition, root-mean-square norm and 8-bit quantizer in one pass:
+ *   h = x + residual (float32; x alone when residual is NULL),
+ *   y = h * (1 / sqrt(mean_k(h^2) + eps)) * weight, in float32,
+ *   codes, scales = the format's quantizer (fql_quant_fp8 with `scale`,
+ *   fql_quant_fp8_block, fql_quant_mxfp8) applied to the float32 y.
+ *   x, residual [M][ld] bf16; weight [K] bf16; eps finite, >= 0.
+ *   scale   per-tensor FP8's static scale (ignored otherwise).
+ *   codes   [M][K], 8-byte aligned; scales as the format's quantizer writes
+ *           them (NULL for per-tensor FP8).
+ *   h_out   [M][ldh] bf16 = h rounded once, or NULL; only with a residual. It
+ *           may be x or residual itself (same pointer and stride).
+ */
+int fql_rms_norm_quant(int format, const void* x, int64_t M, int64_t K, int64_t ldx,
+                       const void* residual, int64_t ldr, const void* weight, float eps, float scale,
+                       uint8_t* codes, void* scales, void* h_out, int64_t ldh, void* stream);
+
+/* Bytes of an 8-bit (or MXFP4) activation operand: the quantized activation
+ * in the order the linear kernels read it, which fql_linear_fused takes in
+ * place of a bf16 activation (host-side). */
+int fql_operand_bytes(int format, int64_t M, int64_t K, size_t* bytes);
+
+/* fql_rms_norm_quant with the codes and scales written as an operand
+ * (256-byte aligned, at least fql_operand_bytes). */
+int fql_rms_norm_operand(int format, const void* x, int64_t M, int64_t K, int64_t ldx,
+                         const void* residual, int64_t ldr, const void* weight, float eps,
+                         float scale, void* operand, size_t operand_bytes, void* h_out, int64_t ldh,
+                         void* stream);
+
+/* The format's activation quantizer written as an operand (several linear
+ * layers that share an input quantize it once). */
+int fql_quant_operand(int format, const void* x, int64_t M, int64_t K, int64_t ldx, float scale,
+                      void* operand, size_t operand_bytes, void* stream);
+
+#define FQL_ACT_NONE 0
+#define FQL_ACT_RELU 1
+#define FQL_ACT_GELU 2      /* z/2 (1 + erf(z / sqrt 2)) */
+#define FQL_ACT_GELU_TANH 3 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+#define FQL_ACT_SILU 4      /* z / (1 + e^-z) */
+#define FQL_ACT_SWIGLU 5    /* silu(gate) * up */
+
+/*
+ * An 8-bit (or MXFP4) linear layer with activation and residual in its
+ * epilogue: y = bf16(act(alpha * (x_q @ w_q^T) + bias) + residual), one
+ * rounding.
+ *   x          [M][ldx] bf16, quantized in the call as fql_linear_<format>
+ *              does; or NULL with
+ *   x_operand  an operand of this format, M and K (256-byte aligned).
+ *   alpha      as in fql_linear_<format>; alpha_dev (device float) replaces it
+ *              when not NULL.
+ *   activation FQL_ACT_*. FQL_ACT_SWIGLU: the weight's N rows (and bias) come
+ *              in groups of 16 gate rows followed by their 16 up rows, N is a
+ *              multiple of 32, and y and residual have N / 2 columns.
+ *   residual   [M][ldr] bf16 or NULL; may be y itself (same pointer, stride).
+ *   workspace  as fql_linear_<format> (fql_linear_<format>_workspace_bytes).
+ */
+int fql_linear_fused(int format, const void* x, int64_t M, int64_t K, int64_t ldx, float input_scale,
+                     const void* x_operand, const void* w_packed, int64_t N, float alpha,
+                     const float* alpha_dev, const void* bias, int activation, const void* residual,
+                     int64_t ldr, void* y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/*
+ * A paged key/value cache of E4M3 codes with one E8M0 scale per (block of
+ * tokens, head) for keys and one for values: value = code * 2^(scale - 127).
+ *   k  [num_blocks][kv_heads][block_size][head_dim]
+ *   v  [num_blocks][kv_heads][block_size / 16][head_dim][16]
+ *   k_scale, v_scale  [num_blocks][kv_heads] bytes
+ * k and v 16-byte aligned; block_size 16, 32, 64, 128 or 256; head_dim 64,
+ * 128 or 256. Needs no initialisation.
+ */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int64_t num_blocks;
+  int32_t kv_heads, block_size, head_dim;
+} fql_kv_cache;
+
+/*
+ * Where a batch's tokens lie. The new tokens of all B sequences lie one after
+ * another in tensors of `tokens` rows: sequence b's are rows cu_seqlens[b] ..
+ * cu_seqlens[b + 1] - 1, its last ones of lens[b] (new ones included), so the
+ * first of n new tokens has position lens[b] - n. Row b of block_table names
+ * the blocks of the sequence in order. The arrays are device memory that the
+ * host does not read: row ranges are clamped to `tokens`, lengths to the
+ * table's capacity, tokens at negative positions are ignored, and a block
+ * number outside the cache is never followed (its tokens are not written, and
+ * attention takes them as absent).
+ */
+typedef struct {
+  const int32_t* block_table; /* [batch][ld_table], table_cols <= ld_table columns used */
+  int64_t ld_table;
+  const int32_t* lens;        /* [batch] */
+  const int32_t* cu_seqlens;  /* [batch + 1] */
+  int64_t tokens;
+  int32_t table_cols, batch;
+  int32_t max_new;            /* upper bound of a sequence's new tokens; more are not looked at */
+} fql_kv_batch;
+
+/*
+ * Writes new keys and values into the cache. Per block, head and tensor: a =
+ * the largest finite |v| of its new tokens, e = the smallest integer in
+ * [-127, 127] with a <= 448 * 2^e (a = 0: -127); the scale's exponent becomes
+ * E = e where the new tokens start the block, else max(E_old, e); codes =
+ * E4M3_RNE_satfinite(v * 2^-E), NaN kept. Where E grew, the codes already in
+ * the block are multiplied by 2^(E_old - E) and rounded again. Two sequences
+ * must not add to one block in the same call.
+ *   k, v  bf16 [tokens][kv_heads][head_dim] with strides (in elements) between
+ *         tokens and heads; head_dim elements are contiguous.
+ */
+int fql_kv_append(const fql_kv_cache* cache, const fql_kv_batch* batch, const void* k,
+                  int64_t k_ld_token, int64_t k_ld_head, const void* v, int64_t v_ld_token,
+                  int64_t v_ld_head, void* stream);
+
+/* Workspace bytes fql_attention_kv8 needs (host-side): arrival counters (first
+ * 64 KiB, zero before first use and left zero by every call; a linear call's
+ * workspace serves) and the partial results of a split call. max_len: an upper
+ * bound of lens (the table's capacity always is one). */
+int fql_attention_kv8_workspace_bytes(int batch, int q_heads, int kv_heads, int head_dim,
+                                      int64_t max_new, int64_t max_len, int window, size_t* bytes);
+/* One-line description of the launch plan (host-side). */
+int fql_attention_kv8_describe(int batch, int q_heads, int kv_heads, int head_dim, int64_t max_new,
+                               int64_t max_len, int window, char* buf, size_t buf_len);
+
+/*
+ * Softmax attention of the batch's new tokens over the cache (which holds
+ * them): out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q . k_j - max).
+ * Query head i reads kv head i / (q_heads / kv_heads).
+ *   q, out   bf16 [tokens][q_heads][head_dim] with token and head strides.
+ *            Rows that no sequence names are not written.
+ *   lse      float32 [tokens][q_heads] or NULL: log sum_j exp(scale q . k_j).
+ *   causal   nonzero: position p sees keys 0 .. p; zero: all lens[b] keys.
+ *   window   > 0: of those only keys above position p - window; 0: no limit.
+ * A token that sees no key gets zeros (lse -inf). NaN or anything else in
+ * cache places that a token does not see never reaches it.
+ */
+int fql_attention_kv8(const fql_kv_cache* cache, const fql_kv_batch* batch, const void* q,
+                      int64_t q_ld_token, int64_t q_ld_head, int q_heads, float scale, int causal,
+                      int window, int64_t max_len, void* out, int64_t o_ld_token, int64_t o_ld_head,
+                      float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
