@@ -90,43 +90,19 @@ __device__ __forceinline__ void mask_values(uint4v (&vw)[VT], int have, int skip
 }
 // 0x80 in every byte that is E4M3's NaN (all seven magnitude bits set)
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+// Zeros in the place of NaN values; whether there were any.
 template <int VT>
-__device__ __forceinline__ bool has_nan(const uint4v (&vw)[VT]) {
+__device__ __forceinline__ bool drop_nan(uint4v (&vw)[VT]) {
   uint32_t any = 0u;
 #pragma unroll
   for (int i = 0; i < VT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) any |= nan_bytes(vw[i][j]);
-  return any != 0u;
-}
-// Replaces NaN values by zeros and makes NaN of every output whose row sees
-// one in its channel: a product of 0/1 matrices counts them.
-template <int NC, int VT>
-__device__ __forceinline__ void nan_rows(uint4v (&vw)[VT], const uint32_t (&seen)[NC], float4v (&o)[NC][VT]) {
-  bf16x8 p[NC][2];
-#pragma unroll
-  for (int t = 0; t < NC; ++t)
-#pragma unroll
-    for (int j = 0; j < 16; ++j) p[t][j / 8][j % 8] = (seen[t] >> j) & 1u ? (__bf16)1.0f : (__bf16)0.0f;
-#pragma unroll
-  for (int i = 0; i < VT; ++i) {
-    uint32_t one[4];
-#pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t n = nan_bytes(vw[i][j]) >> 7;  // 1 in each such byte
-      vw[i][j] &= ~(n * 0xFFu);
-      one[j] = n * 0x38u;  // E4M3's code of 1
+      const uint32_t n = nan_bytes(vw[i][j]);
+      any |= n;
+      vw[i][j] &= ~((n >> 7) * 0xFFu);
     }
-    const bf16x8 v0 = widen8(one[0], one[1]), v1 = widen8(one[2], one[3]);
-#pragma unroll
-    for (int t = 0; t < NC; ++t) {
-      float4v n = float4v{0.f, 0.f, 0.f, 0.f};
-      n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, p[t][0], n, 0, 0, 0);
-      n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[t][1], n, 0, 0, 0);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) o[t][i][r] = n[r] > 0.0f ? __builtin_nanf("") : o[t][i][r];
-    }
-  }
+  return any != 0u;
 }
 
 // Float32 partial results cross XCDs (each with its own L2) like the GEMMs'
@@ -180,12 +156,12 @@ __device__ __forceinline__ int64_t partial_floats(int rows) {
 }
 
 // The last workgroup of a row tile to arrive adds the ranges' results in
-// order: every thread (thread tid of 256) takes items of four channels.
+// order; an item is four channels of one row.
 template <int D>
 __device__ __forceinline__ void join_ranges(const AttnArgs& a, const SeqSpan& s, int kv_head, int G, int row0,
                                             int rows_in_tile, int tile_rows, int ns, const float* slab) {
   const int64_t stride = partial_floats<D>(tile_rows);
-  for (int item = threadIdx.x; item < rows_in_tile * (D / 4); item += 256) {
+  for (int item = threadIdx.x; item < rows_in_tile * (D / 4); item += blockDim.x) {
     const int row = item / (D / 4), d = (item % (D / 4)) * 4;
     const float* ml = slab + (int64_t)tile_rows * D + row * 2;
     const float* po = slab + (int64_t)row * D + d;
@@ -235,6 +211,39 @@ __device__ __forceinline__ bool last_to_arrive(uint32_t* counter, int ns, uint32
   return *s_flag != 0u;
 }
 
+// A NaN value of a token that some rows of a row tile see and others do not
+// would reach all of them through the matrix product (0 * NaN). The kernels
+// leave NaN values of such tiles of 64 tokens out of the product and, where
+// one was there (s_nan), make NaN of the outputs that see it here, after they
+// were written: straight (part null) or in the partial results.
+template <int D>
+__device__ void put_nan_rows(const AttnArgs& a, const PagedCache& c, const PagedBatch& pb, const SeqSpan& s, int b,
+                             int h, int G, int bs_shift, int row0, int nrows, int k0, int k1, const Visible& first,
+                             const Visible& last, float* part) {
+  __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's outputs are written
+  __syncthreads();
+  for (int t0 = k0; t0 < k1; t0 += 64) {
+    if (t0 + 64 <= first.hi && t0 >= last.lo) continue;  // every row sees these
+    for (int t = t0; t < t0 + 64 && t < k1; ++t) {
+      const int64_t blk = pb.table[(int64_t)b * pb.ld_table + (t >> bs_shift)];
+      if (blk < 0 || blk >= c.num_blocks) continue;
+      const int off = t & (c.block_size - 1);
+      const uint8_t* v = c.v + ((blk * c.heads + h) * (c.block_size / 16) + off / 16) * (D * 16) + off % 16;
+      for (int d = threadIdx.x; d < D; d += blockDim.x) {
+        if ((v[d * 16] & 0x7F) != 0x7F) continue;
+        for (int r = 0; r < nrows; ++r) {
+          const Visible w = visible_of(s, (row0 + r) / G, a.causal, a.window);
+          if (t < w.lo || t >= w.hi) continue;
+          if (part != nullptr)
+            __hip_atomic_store(part + (int64_t)r * D + d, __builtin_nanf(""), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          else
+            a.out[(s.row0 + (row0 + r) / G) * a.o_ld_token + (h * G + (row0 + r) % G) * a.o_ld_head + d] = 0x7FC0;
+        }
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // few rows: every wave its own keys
 // ---------------------------------------------------------------------------
@@ -264,7 +273,7 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
   constexpr int KI = D / 64, VT = D / 16, SK = D / 32;
   __shared__ float4v so[4][NC * VT][64];
   __shared__ float2v sml[4][NC][16];
-  __shared__ uint32_t s_flag;
+  __shared__ uint32_t s_flag, s_nan;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
@@ -275,13 +284,18 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
   const int rows = s.n * G, row0 = rt * 16 * NC;
   if (row0 >= rows) return;
   const int last_row = row0 + 16 * NC < rows ? row0 + 16 * NC - 1 : rows - 1;
-  const int kmin = visible_of(s, row0 / G, a.causal, a.window).lo & ~63;
-  const int kmax = visible_of(s, last_row / G, a.causal, a.window).hi;
+  // every row sees [last.lo, first.hi), some row each of [first.lo, last.hi)
+  const Visible first = visible_of(s, row0 / G, a.causal, a.window);
+  const Visible last = visible_of(s, last_row / G, a.causal, a.window);
+  const int kmin = first.lo & ~63, kmax = last.hi;
   int ns = kmax > kmin ? (kmax - kmin + chunk - 1) / chunk : 1;
   ns = ns < splits ? ns : splits;
   if (z >= ns) return;
   const int k0 = kmin + z * chunk;
   const int k1 = z == ns - 1 || k0 + chunk > kmax ? kmax : k0 + chunk;
+
+  if (tid == 0) s_nan = 0u;
+  __syncthreads();
 
   // this lane's columns (query rows)
   bf16x8 q[NC][SK];
@@ -303,12 +317,6 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
         for (int j = 0; j < 8; ++j) q[t][i][j] = (__bf16)0.0f;
     }
   }
-  // keys below all_lo or from all_hi on are hidden from some row, keys below
-  // any_lo from every row (as those from kmax on)
-  const int all_lo = visible_of(s, last_row / G, a.causal, a.window).lo;
-  const int all_hi = visible_of(s, row0 / G, a.causal, a.window).hi;
-  const int any_lo = visible_of(s, row0 / G, a.causal, a.window).lo;
-
   const float sl2 = a.scale * kLog2e;
   float m[NC], l[NC];
   float4v o[NC][VT];
@@ -390,24 +398,21 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
     // Masked in edge tiles only: keys hidden from some row, past this range
     // (the ranges meet at multiples of 64, so only past kmax) or of a block
     // that is not there.
-    const bool edge = t0 < all_lo || t0 + 64 > all_hi || t0 + 64 > k1 || __any(blk < 0);
+    const bool edge = t0 < last.lo || t0 + 64 > first.hi || t0 + 64 > k1 || __any(blk < 0);
     if (edge) {
-      const int have = blk < 0 ? 0 : clamp16(k1 - tg), skip = clamp16(any_lo - tg);
-      uint32_t seen[NC];  // bit i: this lane's row sees its token i
+      const int have = blk < 0 ? 0 : clamp16(k1 - tg), skip = clamp16(first.lo - tg);
 #pragma unroll
       for (int t = 0; t < NC; ++t) {
         const int lo = clamp16(vlo[t] - tg), hi = clamp16(vhi[t] - tg);
         const int top = hi < have ? hi : have;
-        seen[t] = ((1u << top) - 1u) & ~((1u << lo) - 1u);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[t][i] = (seen[t] >> i) & 1u ? x[t][i] * ks : neg_inf();
+        for (int i = 0; i < 16; ++i) x[t][i] = i >= lo && i < top ? x[t][i] * ks : neg_inf();
       }
       // Values of tokens that no row sees may hold anything, and 0 * NaN is
       // not 0: they are zeroed.
       mask_values<VT>(vw, have, skip);
-      // NaN values of tokens that some rows see and others do not: taken out
-      // of the product, and put back into the rows that see them.
-      if ((all_lo > any_lo || all_hi < kmax) && __any(has_nan<VT>(vw))) nan_rows<NC, VT>(vw, seen, o);
+      // NaN where rows differ in what they see: see put_nan_rows
+      if ((t0 < last.lo || t0 + 64 > first.hi) && drop_nan<VT>(vw)) s_nan = 1u;
     } else {
 #pragma unroll
       for (int t = 0; t < NC; ++t)
@@ -496,9 +501,290 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
       if (d == 0) put_f2(mine + (int64_t)16 * NC * D + row * 2, M, L);
     }
   }
+  if (s_nan != 0u)
+    put_nan_rows<D>(a, c, pb, s, b, h, G, bs_shift, row0, last_row - row0 + 1, k0, k1, first, last,
+                    ns == 1 ? nullptr : mine);
   if (ns == 1) return;
   if (last_to_arrive(counters + tile, ns, &s_flag))
     join_ranges<D>(a, s, h, G, row0, last_row - row0 + 1, 16 * NC, ns, slab);
+}
+
+// ---------------------------------------------------------------------------
+// many rows: keys and values shared through LDS
+// ---------------------------------------------------------------------------
+//
+// 32 rows a wave, NW waves a workgroup. Tiles of 64 tokens are widened to
+// bf16 once per workgroup, on their way into LDS (two buffers; the next tile's
+// codes are loaded at the start of a tile's work and written to the other
+// buffer at its end, one barrier a tile).
+//
+// v_mfma_f32_32x32x16_bf16: A lane l holds row l % 32, k = 8 (l / 32) + j; B
+// column l % 32, the same k; result register r: column l % 32, row
+// 8 (r / 4) + 4 (l / 32) + r % 4.
+//   S^T: row rho of 32 tokens is token 16 ((rho / 4) % 2) + 4 (rho / 8) + rho % 4,
+//     so register r of lane half hf is token 16 hf + r.
+//   O^T step s (0, 1): k = 8 hf + j is token 16 hf + 8 s + j.
+// LDS: keys [64 rows in S^T order][D], values [D][64 tokens], in 16-byte
+// chunks; a row's chunks are exchanged by an XOR with its number so that the
+// 16 rows a quarter-wave reads at one chunk lie in 16 different bank groups.
+//
+// The running maximum moves only when a tile exceeds it by more than 2^8 (the
+// weights then stay below 2^8, which costs no precision): the accumulators
+// are rescaled a few times a row instead of at every tile.
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kernel(
+    const AttnArgs a, const PagedCache c, const PagedBatch pb, int bs_shift, int row_tiles, int splits, int chunk,
+    float* partial, uint32_t* counters) {
+  constexpr int T = 64 * NW, ROWS = 32 * NW;
+  constexpr int KP = 4 * D / T;                  // 16-byte pieces of keys (and of values) a thread stages
+  constexpr int KC = D / 8;                      // 16-byte chunks of a key row in LDS
+  constexpr int SK = D / 16, VT = D / 32;
+  static_assert(KP >= 1 && 4 * D % T == 0, "whole pieces");
+  __shared__ uint4v sk[2][64 * KC];
+  __shared__ uint4v sv[2][D * 8];
+  __shared__ uint32_t s_flag, s_nan;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 31, hf = lane >> 5;
+  const int bh = blockIdx.x, H = c.heads, h = bh % H, b = bh / H;
+  // the last row tiles see the most keys under a causal mask: they start first
+  const int rt = row_tiles - 1 - (int)blockIdx.y % row_tiles, z = blockIdx.y / row_tiles;
+  const int G = a.Hq / H, bs = c.block_size;
+  const SeqSpan s = seq_span(pb, b, bs);
+  const int rows = s.n * G, row0 = rt * ROWS;
+  if (row0 >= rows) return;
+  const int last_row = row0 + ROWS < rows ? row0 + ROWS - 1 : rows - 1;
+  const Visible first = visible_of(s, row0 / G, a.causal, a.window);
+  const Visible last = visible_of(s, last_row / G, a.causal, a.window);
+  const int kmin = first.lo & ~63, kmax = last.hi;
+  int ns = kmax > kmin ? (kmax - kmin + chunk - 1) / chunk : 1;
+  ns = ns < splits ? ns : splits;
+  if (z >= ns) return;
+  const int k0 = kmin + z * chunk;
+  const int k1 = z == ns - 1 || k0 + chunk > kmax ? kmax : k0 + chunk;
+  if (tid == 0) s_nan = 0u;
+  __syncthreads();
+
+  // this lane's query row, and the keys that all (some) rows of the wave see
+  const int row = row0 + 32 * wave + col;
+  const bool ok = row < rows;
+  const Visible mine = visible_of(s, ok ? row / G : 0, a.causal, a.window);
+  const int vlo = mine.lo, vhi = ok ? mine.hi : 0;
+  const int wfirst = row0 + 32 * wave < rows ? row0 + 32 * wave : rows - 1;
+  const int wlast = row0 + 32 * wave + 31 < rows ? row0 + 32 * wave + 31 : rows - 1;
+  const int wave_all_lo = visible_of(s, wlast / G, a.causal, a.window).lo;
+  const int wave_all_hi = visible_of(s, wfirst / G, a.causal, a.window).hi;
+  const int wave_any_hi = row0 + 32 * wave < rows ? visible_of(s, wlast / G, a.causal, a.window).hi : 0;
+  bf16x8 q[SK];
+  {
+    const uint16_t* qp = a.q + (s.row0 + (ok ? row / G : 0)) * a.q_ld_token +
+                         (int64_t)(h * G + (ok ? row % G : 0)) * a.q_ld_head + 8 * hf;
+#pragma unroll
+    for (int i = 0; i < SK; ++i) {
+      q[i] = load_q8(qp + 16 * i, a.aligned);
+      if (!ok)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[i][j] = (__bf16)0.0f;
+    }
+  }
+
+  const float sl2 = a.scale * kLog2e;
+  float m = neg_inf(), l = 0.0f;
+  float16v o[VT];
+#pragma unroll
+  for (int i = 0; i < VT; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
+
+  const int64_t page_bytes = (int64_t)H * bs * D;
+  const int32_t* table = pb.table + (int64_t)b * pb.ld_table;
+  auto block_of = [&](int t) -> int {
+    if (t >= kmax) return -1;  // kmax <= len <= the table's capacity
+    const int p = table[t >> bs_shift];
+    return p >= 0 && p < c.num_blocks ? p : -1;
+  };
+  // staging: piece i of this thread is (token, 16 channels) of the keys and
+  // (16 tokens, channel) of the values
+  uint4v kw[KP], vw[KP];
+  int kb[KP], vb[KP];          // their blocks
+  int sb[2];                   // blocks of this lane's tokens 16 hf .. of the tile's two halves
+  uint32_t ksb[2], vsb[2];
+  auto k_token = [&](int i) { return (tid + T * i) / (D / 16); };
+  auto v_group = [&](int i) { return (tid + T * i) / D; };
+  auto find_blocks = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < KP; ++i) {
+      kb[i] = block_of(t0 + (k_token(i) & ~15));
+      vb[i] = block_of(t0 + 16 * v_group(i));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sb[i] = block_of(t0 + 32 * i + 16 * hf);
+  };
+  auto load_tile = [&](int t0) {
+#pragma unroll
+    for (int i = 0; i < KP; ++i) {
+      const int kt = t0 + k_token(i), vt = t0 + 16 * v_group(i);
+      const int kc = (tid + T * i) % (D / 16), vd = (tid + T * i) % D;
+      kw[i] = *reinterpret_cast<const uint4v*>(c.k + (kb[i] < 0 ? 0 : kb[i]) * page_bytes +
+                                               ((int64_t)h * bs + (kt & (bs - 1))) * D + 16 * kc);
+      vw[i] = *reinterpret_cast<const uint4v*>(c.v + (vb[i] < 0 ? 0 : vb[i]) * page_bytes +
+                                               ((int64_t)h * bs + (vt & (bs - 1))) * D + 16 * vd);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t at = (int64_t)(sb[i] < 0 ? 0 : sb[i]) * H + h;
+      ksb[i] = c.k_scale[at];
+      vsb[i] = sb[i] < 0 ? 0u : c.v_scale[at];
+    }
+  };
+  auto stage_tile = [&](int t0, int buf) {
+    // tokens that no row sees may hold anything: their values are zeroed; NaN
+    // where rows differ in what they see: see put_nan_rows
+    const bool some = t0 + 64 > first.hi || t0 < last.lo;
+#pragma unroll
+    for (int i = 0; i < KP; ++i) {
+      const int tok = k_token(i), kc = (tid + T * i) % (D / 16);
+      const int w = tok & 31, r = w & 15;
+      const int lrow = (tok & 32) + 8 * (r >> 2) + 4 * (w >> 4) + (r & 3);
+      const int key = D == 64 ? (lrow >> 1) & 7 : lrow & 15;
+      uint4v* kd = &sk[buf][lrow * KC];
+      kd[(2 * kc) ^ key] = __builtin_bit_cast(uint4v, widen8(kw[i][0], kw[i][1]));
+      kd[(2 * kc + 1) ^ key] = __builtin_bit_cast(uint4v, widen8(kw[i][2], kw[i][3]));
+      const int g = v_group(i), d = (tid + T * i) % D;
+      uint4v u[1] = {vw[i]};
+      if (some || vb[i] < 0 || t0 + 64 > kmax) {
+        mask_values<1>(u, vb[i] < 0 ? 0 : clamp16(kmax - (t0 + 16 * g)), clamp16(first.lo - (t0 + 16 * g)));
+        if (some && drop_nan<1>(u)) s_nan = 1u;
+      }
+      uint4v* vd = &sv[buf][d * 8];
+      vd[(2 * g) ^ ((d >> 1) & 7)] = __builtin_bit_cast(uint4v, widen8(u[0][0], u[0][1]));
+      vd[(2 * g + 1) ^ ((d >> 1) & 7)] = __builtin_bit_cast(uint4v, widen8(u[0][2], u[0][3]));
+    }
+  };
+
+  if (k0 < k1) {
+    find_blocks(k0);
+    load_tile(k0);
+    stage_tile(k0, 0);
+  }
+  int buf = 0;
+  for (int t0 = k0; t0 < k1; t0 += 64, buf ^= 1) {
+    const float kk0 = e8m0(ksb[0]) * sl2, kk1 = e8m0(ksb[1]) * sl2;
+    const uint32_t ve[2] = {vsb[0], vsb[1]};
+    const bool absent0 = sb[0] < 0, absent1 = sb[1] < 0;
+    const bool more = t0 + 64 < k1;
+    if (more) {
+      find_blocks(t0 + 64);
+      load_tile(t0 + 64);
+    }
+    __syncthreads();
+    if (t0 < wave_any_hi) {
+      float x[2][16];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float16v acc;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
+        const int lrow = 32 * half + col;
+        const int key = D == 64 ? (lrow >> 1) & 7 : lrow & 15;
+#pragma unroll
+        for (int i = 0; i < SK; ++i) {
+          const bf16x8 kf = __builtin_bit_cast(bf16x8, sk[buf][lrow * KC + ((2 * i + hf) ^ key)]);
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[i], acc, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[half][r] = acc[r];
+      }
+      float kk[2] = {kk0, kk1};
+      if (t0 < wave_all_lo || t0 + 64 > wave_all_hi || t0 + 64 > k1 || __any(absent0 || absent1)) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int tg = t0 + 32 * half + 16 * hf;
+          const int have = (half ? absent1 : absent0) ? 0 : clamp16(k1 - tg);
+          const int lo = clamp16(vlo - tg), hi = clamp16(vhi - tg);
+          const int upto = hi < have ? hi : have;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[half][r] = r >= lo && r < upto ? x[half][r] * kk[half] : neg_inf();
+          kk[half] = 1.0f;
+        }
+      }
+      float top = neg_inf();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float t = x[half][0];
+#pragma unroll
+        for (int r = 1; r < 16; ++r) t = __builtin_fmaxf(t, x[half][r]);
+        top = __builtin_fmaxf(top, t * kk[half]);  // kk >= 0
+      }
+      {
+        const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+        top = __builtin_fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+      }
+      if (__any(top > m + 8.0f)) {
+        top = __builtin_fmaxf(top, m);
+        const float back = exp2_fast(m - (top == neg_inf() ? 0.0f : top));
+        l *= back;
+#pragma unroll
+        for (int i = 0; i < VT; ++i) o[i] *= back;
+        m = top;
+      }
+      const float safe = m == neg_inf() ? 0.0f : m;
+      bf16x8 p[2][2];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float vs = e8m0(ve[half]);
+        float w[16], sum = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          w[r] = exp2_fast(__builtin_fmaf(x[half][r], kk[half], -safe));
+          sum += w[r];
+          w[r] *= vs;
+        }
+        l += sum;
+        p[half][0] = round8(w);
+        p[half][1] = round8(w + 8);
+      }
+#pragma unroll
+      for (int i = 0; i < VT; ++i) {
+        const int d = 32 * i + col;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bf16x8 vf = __builtin_bit_cast(bf16x8, sv[buf][d * 8 + ((4 * (j / 2) + 2 * hf + j % 2) ^ ((d >> 1) & 7))]);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[j / 2][j % 2], o[i], 0, 0, 0);
+        }
+      }
+    }
+    // the other buffer was last read before this tile's barrier
+    if (more) stage_tile(t0 + 64, buf ^ 1);
+  }
+
+  {
+    const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
+    l = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
+  }
+  const int tile = bh * row_tiles + rt;
+  float* slab = partial + (int64_t)tile * splits * partial_floats<D>(ROWS);
+  float* mine_p = slab + z * partial_floats<D>(ROWS);
+  if (ok) {
+    const int lr = 32 * wave + col;
+#pragma unroll
+    for (int i = 0; i < VT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float4v v = float4v{o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]};
+        const int d = 32 * i + 8 * r + 4 * hf;
+        if (ns == 1) write_out4(a, s, h, G, row, d, v, m, l);
+        else put_f4(mine_p + (int64_t)lr * D + d, v);
+      }
+    if (ns > 1 && hf == 0) put_f2(mine_p + (int64_t)ROWS * D + lr * 2, m, l);
+  }
+  __syncthreads();  // s_nan
+  if (s_nan != 0u)
+    put_nan_rows<D>(a, c, pb, s, b, h, G, bs_shift, row0, last_row - row0 + 1, k0, k1, first, last,
+                    ns == 1 ? nullptr : mine_p);
+  if (ns == 1) return;
+  if (last_to_arrive(counters + tile, ns, &s_flag))
+    join_ranges<D>(a, s, h, G, row0, last_row - row0 + 1, ROWS, ns, slab);
 }
 
 }  // namespace
@@ -507,12 +793,14 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
 // plan, launcher
 // ---------------------------------------------------------------------------
 
+static int rows_of(const AttnPlan& p) { return p.kind == 0 ? 16 * p.cols : 32 * p.cols; }
+
 AttnPlan plan_attention(int B, int Hq, int Hkv, int D, int64_t max_new, int64_t max_len, int window) {
   AttnPlan p{};
   const int64_t rows = std::max<int64_t>(1, max_new) * (Hq / Hkv);
-  p.kind = 0;
-  p.cols = rows <= 16 ? 1 : 2;
-  p.row_tiles = (int)((rows + 16 * p.cols - 1) / (16 * p.cols));
+  p.kind = rows <= 32 ? 0 : 1;
+  p.cols = p.kind == 1 ? 4 : rows <= 16 || D == 256 ? 1 : 2;
+  p.row_tiles = (int)((rows + rows_of(p) - 1) / rows_of(p));
   const int64_t tiles = (int64_t)B * Hkv * p.row_tiles;
   // keys one row tile goes through; with a window it starts at a multiple of
   // 64 below its first visible key
@@ -520,6 +808,8 @@ AttnPlan plan_attention(int B, int Hq, int Hkv, int D, int64_t max_new, int64_t 
   if (window > 0) span = std::min<int64_t>(span, (int64_t)window + max_new - 1 + 63);
   // ranges: about 2048 workgroups, at least 256 keys each
   int64_t splits = std::max<int64_t>(1, std::min<int64_t>((2048 + tiles - 1) / tiles, (span + 255) / 256));
+  // many rows: only where the tiles leave half of the card idle
+  if (p.kind == 1) splits = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, (span + 511) / 512));
   // one arrival counter a tile, below the words a linear call keeps its device scalars in
   if (tiles > kWorkspaceScalarOffset / 4) splits = 1;
   int64_t chunk = round_up((span + splits - 1) / splits, 64);
@@ -527,14 +817,15 @@ AttnPlan plan_attention(int B, int Hq, int Hkv, int D, int64_t max_new, int64_t 
   p.splits = (int)splits;
   p.chunk = (int)chunk;
   p.counter_bytes = kWorkspaceCounterBytes;
-  p.partial_bytes = splits > 1 ? round_up(tiles * splits * (16 * p.cols) * (D + 2) * 4, 256) : 0;
+  p.partial_bytes = splits > 1 ? round_up(tiles * splits * rows_of(p) * (D + 2) * 4, 256) : 0;
   p.total_bytes = p.counter_bytes + p.partial_bytes;
   return p;
 }
 
 std::string describe_attention(const AttnPlan& p, int D) {
   char b[160];
-  std::snprintf(b, sizeof(b), "attn_kv8_stream_kernel<D=%d,NC=%d> row_tiles=%d splits=%d chunk=%d", D, p.cols,
+  std::snprintf(b, sizeof(b), "%s<D=%d,%s=%d> row_tiles=%d splits=%d chunk=%d",
+                p.kind == 0 ? "attn_kv8_stream_kernel" : "attn_kv8_tile_kernel", D, p.kind == 0 ? "NC" : "NW", p.cols,
                 p.row_tiles, p.splits, p.chunk);
   return std::string(b);
 }
@@ -546,13 +837,20 @@ hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, const PagedCac
   uint32_t* counters = reinterpret_cast<uint32_t*>(workspace);
   float* partial = reinterpret_cast<float*>(workspace + p.counter_bytes);
   const dim3 grid((unsigned)(pb.B * c.heads), (unsigned)(p.row_tiles * p.splits), 1);
-#define FQL_A(DD, NC)                                                                                    \
-  if (c.D == DD && p.cols == NC) {                                                                       \
-    attn_kv8_stream_kernel<DD, NC><<<grid, 256, 0, st>>>(a, c, pb, shift, p.row_tiles, p.splits, p.chunk, \
-                                                         partial, counters);                             \
-    return hipGetLastError();                                                                            \
+#define FQL_A(KIND, KERNEL, DD, N, THREADS)                                                               \
+  if (p.kind == KIND && c.D == DD && p.cols == N) {                                                       \
+    KERNEL<DD, N><<<grid, THREADS, 0, st>>>(a, c, pb, shift, p.row_tiles, p.splits, p.chunk, partial,     \
+                                            counters);                                                    \
+    return hipGetLastError();                                                                             \
   }
-  FQL_A(64, 1) FQL_A(64, 2) FQL_A(128, 1) FQL_A(128, 2) FQL_A(256, 1) FQL_A(256, 2)
+  FQL_A(0, attn_kv8_stream_kernel, 64, 1, 256)
+  FQL_A(0, attn_kv8_stream_kernel, 64, 2, 256)
+  FQL_A(0, attn_kv8_stream_kernel, 128, 1, 256)
+  FQL_A(0, attn_kv8_stream_kernel, 128, 2, 256)
+  FQL_A(0, attn_kv8_stream_kernel, 256, 1, 256)
+  FQL_A(1, attn_kv8_tile_kernel, 64, 4, 256)
+  FQL_A(1, attn_kv8_tile_kernel, 128, 4, 256)
+  FQL_A(1, attn_kv8_tile_kernel, 256, 4, 256)
 #undef FQL_A
   return hipErrorInvalidValue;
 }

@@ -116,8 +116,8 @@ hipError_t launch_kv_append(const PagedCache& c, const PagedBatch& pb, const uin
 // ---- attention over the paged cache ------------------------------------------
 struct AttnPlan {
   int kind;        // 0: 16 * cols query rows per workgroup, every wave its own keys;
-                   // 1: 128 query rows per workgroup, 32 per wave, keys shared through LDS
-  int cols;        // kind 0: 16-row tiles (1 or 2)
+                   // 1: 32 query rows per wave, cols waves, keys shared through LDS
+  int cols;
   int row_tiles;   // row tiles of one (sequence, kv head)
   int splits;      // ranges of keys (1: written directly)
   int chunk;       // keys of one range (a multiple of 64)
