@@ -539,9 +539,10 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
   constexpr int KP = 4 * D / T;                  // 16-byte pieces of keys (and of values) a thread stages
   constexpr int KC = D / 8;                      // 16-byte chunks of a key row in LDS
   constexpr int SK = D / 16, VT = D / 32;
-  static_assert(KP >= 1 && 4 * D % T == 0, "whole pieces");
+  static_assert(KP >= 1 && 4 * D % T == 0 && T % D == 0 && D % 64 == 0, "a wave's pieces in one group");
   __shared__ uint4v sk[2][64 * KC];
   __shared__ uint4v sv[2][D * 8];
+  __shared__ float4v ss[2][4];  // per group of 16 tokens: score factor (-1: no block), see stage_tile
   __shared__ uint32_t s_flag, s_nan;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -596,111 +597,105 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
 #pragma unroll
     for (int r = 0; r < 16; ++r) o[i][r] = 0.0f;
 
-  const int64_t page_bytes = (int64_t)H * bs * D;
+  // Staging. A tile's four groups of 16 tokens are 16 D contiguous bytes each,
+  // of keys as of values, in one block: a thread takes the 16-byte piece pd of
+  // one group in every pass, so a wave's group, its block and its scales are
+  // scalars. Blocks are looked up one tile ahead of the loads.
+  const int pd = tid % D, g0 = __builtin_amdgcn_readfirstlane(tid / D);
+  constexpr int GS = T / D;  // groups a pass
   const int32_t* table = pb.table + (int64_t)b * pb.ld_table;
-  auto block_of = [&](int t) -> int {
-    if (t >= kmax) return -1;  // kmax <= len <= the table's capacity
-    const int p = table[t >> bs_shift];
-    return p >= 0 && p < c.num_blocks ? p : -1;
-  };
-  // staging: piece i of this thread is (token, 16 channels) of the keys and
-  // (16 tokens, channel) of the values
+  const int64_t head_bytes = (int64_t)bs * D;
   uint4v kw[KP], vw[KP];
-  int kb[KP], vb[KP];          // their blocks
-  int sb[2];                   // blocks of this lane's tokens 16 hf .. of the tile's two halves
-  uint32_t ksb[2], vsb[2];
-  auto k_token = [&](int i) { return (tid + T * i) / (D / 16); };
-  auto v_group = [&](int i) { return (tid + T * i) / D; };
-  auto find_blocks = [&](int t0) {
+  int blk[KP], entry[KP];  // blocks of the tile loaded last, table entries of the one after it
+  uint32_t ksb[KP], vsb[KP];
+  auto look_up = [&](int t0) {  // past the last key the last entry: see load_tile
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
-      kb[i] = block_of(t0 + (k_token(i) & ~15));
-      vb[i] = block_of(t0 + 16 * v_group(i));
+      const int t = t0 + 16 * (g0 + GS * i);
+      entry[i] = table[(t < kmax ? t : kmax - 1) >> bs_shift];
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) sb[i] = block_of(t0 + 32 * i + 16 * hf);
   };
   auto load_tile = [&](int t0) {
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
-      const int kt = t0 + k_token(i), vt = t0 + 16 * v_group(i);
-      const int kc = (tid + T * i) % (D / 16), vd = (tid + T * i) % D;
-      kw[i] = *reinterpret_cast<const uint4v*>(c.k + (kb[i] < 0 ? 0 : kb[i]) * page_bytes +
-                                               ((int64_t)h * bs + (kt & (bs - 1))) * D + 16 * kc);
-      vw[i] = *reinterpret_cast<const uint4v*>(c.v + (vb[i] < 0 ? 0 : vb[i]) * page_bytes +
-                                               ((int64_t)h * bs + (vt & (bs - 1))) * D + 16 * vd);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t at = (int64_t)(sb[i] < 0 ? 0 : sb[i]) * H + h;
+      const int e = __builtin_amdgcn_readfirstlane(entry[i]);
+      blk[i] = t0 + 16 * (g0 + GS * i) < kmax && e >= 0 && e < c.num_blocks ? e : -1;
+      const int off = (t0 + 16 * (g0 + GS * i)) & (bs - 1);
+      const int64_t at = (int64_t)(blk[i] < 0 ? 0 : blk[i]) * H + h;
+      const int64_t base = at * head_bytes + off * D;
+      kw[i] = *reinterpret_cast<const uint4v*>(c.k + base + 16 * pd);
+      vw[i] = *reinterpret_cast<const uint4v*>(c.v + base + 16 * pd);
       ksb[i] = c.k_scale[at];
-      vsb[i] = sb[i] < 0 ? 0u : c.v_scale[at];
+      vsb[i] = c.v_scale[at];
     }
   };
   auto stage_tile = [&](int t0, int buf) {
     // tokens that no row sees may hold anything: their values are zeroed; NaN
     // where rows differ in what they see: see put_nan_rows
-    const bool some = t0 + 64 > first.hi || t0 < last.lo;
+    const bool some = t0 + 64 > first.hi || t0 < last.lo || t0 + 64 > kmax;
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
-      const int tok = k_token(i), kc = (tid + T * i) % (D / 16);
-      const int w = tok & 31, r = w & 15;
-      const int lrow = (tok & 32) + 8 * (r >> 2) + 4 * (w >> 4) + (r & 3);
+      const int g = g0 + GS * i;
+      const int tok = pd / (D / 16), kc = pd % (D / 16);
+      const int lrow = 32 * (g >> 1) + 8 * (tok >> 2) + 4 * (g & 1) + (tok & 3);
       const int key = D == 64 ? (lrow >> 1) & 7 : lrow & 15;
       uint4v* kd = &sk[buf][lrow * KC];
       kd[(2 * kc) ^ key] = __builtin_bit_cast(uint4v, widen8(kw[i][0], kw[i][1]));
       kd[(2 * kc + 1) ^ key] = __builtin_bit_cast(uint4v, widen8(kw[i][2], kw[i][3]));
-      const int g = v_group(i), d = (tid + T * i) % D;
       uint4v u[1] = {vw[i]};
-      if (some || vb[i] < 0 || t0 + 64 > kmax) {
-        mask_values<1>(u, vb[i] < 0 ? 0 : clamp16(kmax - (t0 + 16 * g)), clamp16(first.lo - (t0 + 16 * g)));
-        if (some && drop_nan<1>(u)) s_nan = 1u;
+      if (some || blk[i] < 0) {
+        const int t = t0 + 16 * g;
+        mask_values<1>(u, blk[i] < 0 ? 0 : clamp16(kmax - t), clamp16(first.lo - t));
+        if (drop_nan<1>(u)) s_nan = 1u;
       }
-      uint4v* vd = &sv[buf][d * 8];
-      vd[(2 * g) ^ ((d >> 1) & 7)] = __builtin_bit_cast(uint4v, widen8(u[0][0], u[0][1]));
-      vd[(2 * g + 1) ^ ((d >> 1) & 7)] = __builtin_bit_cast(uint4v, widen8(u[0][2], u[0][3]));
+      const int vkey = (pd >> 1) & 7;
+      uint4v* vd = &sv[buf][pd * 8];
+      vd[(2 * g) ^ vkey] = __builtin_bit_cast(uint4v, widen8(u[0][0], u[0][1]));
+      vd[(2 * g + 1) ^ vkey] = __builtin_bit_cast(uint4v, widen8(u[0][2], u[0][3]));
+      if (pd == 0) {
+        // the weights take the value scale 2^ev in their exponent; what lies
+        // outside +-100 (no exponent's bits are lost there) is a factor of its own
+        const int ev = blk[i] < 0 ? 0 : (int)vsb[i] - 127;
+        const int e = ev < -100 ? -100 : (ev > 100 ? 100 : ev);
+        ss[buf][g] = float4v{blk[i] < 0 ? -1.0f : e8m0(ksb[i]) * sl2, (float)e,
+                             __uint_as_float((uint32_t)(127 - e) << 23), __uint_as_float((uint32_t)(127 + ev - e) << 23)};
+      }
     }
   };
 
   if (k0 < k1) {
-    find_blocks(k0);
+    look_up(k0);
     load_tile(k0);
+    look_up(k0 + 64);
     stage_tile(k0, 0);
   }
   int buf = 0;
   for (int t0 = k0; t0 < k1; t0 += 64, buf ^= 1) {
-    const float kk0 = e8m0(ksb[0]) * sl2, kk1 = e8m0(ksb[1]) * sl2;
-    const uint32_t ve[2] = {vsb[0], vsb[1]};
-    const bool absent0 = sb[0] < 0, absent1 = sb[1] < 0;
     const bool more = t0 + 64 < k1;
     if (more) {
-      find_blocks(t0 + 64);
       load_tile(t0 + 64);
+      look_up(t0 + 128);
     }
     __syncthreads();
     if (t0 < wave_any_hi) {
-      float x[2][16];
+      float16v x[2];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        float16v acc;
+      for (int r = 0; r < 16; ++r) x[0][r] = x[1][r] = 0.0f;
+      const int key = D == 64 ? (col >> 1) & 7 : col & 15;  // of rows col and 32 + col alike
 #pragma unroll
-        for (int r = 0; r < 16; ++r) acc[r] = 0.0f;
-        const int lrow = 32 * half + col;
-        const int key = D == 64 ? (lrow >> 1) & 7 : lrow & 15;
+      for (int i = 0; i < SK; ++i)
 #pragma unroll
-        for (int i = 0; i < SK; ++i) {
-          const bf16x8 kf = __builtin_bit_cast(bf16x8, sk[buf][lrow * KC + ((2 * i + hf) ^ key)]);
-          acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[i], acc, 0, 0, 0);
+        for (int half = 0; half < 2; ++half) {
+          const bf16x8 kf = __builtin_bit_cast(bf16x8, sk[buf][(32 * half + col) * KC + ((2 * i + hf) ^ key)]);
+          x[half] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[i], x[half], 0, 0, 0);
         }
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[half][r] = acc[r];
-      }
-      float kk[2] = {kk0, kk1};
-      if (t0 < wave_all_lo || t0 + 64 > wave_all_hi || t0 + 64 > k1 || __any(absent0 || absent1)) {
+      const float4v sc[2] = {ss[buf][hf], ss[buf][2 + hf]};
+      float kk[2] = {sc[0][0], sc[1][0]};
+      if (t0 < wave_all_lo || t0 + 64 > wave_all_hi || t0 + 64 > k1 || __any(__builtin_fminf(kk[0], kk[1]) < 0.0f)) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int tg = t0 + 32 * half + 16 * hf;
-          const int have = (half ? absent1 : absent0) ? 0 : clamp16(k1 - tg);
+          const int have = kk[half] < 0.0f ? 0 : clamp16(k1 - tg);
           const int lo = clamp16(vlo - tg), hi = clamp16(vhi - tg);
           const int upto = hi < have ? hi : have;
 #pragma unroll
@@ -729,30 +724,32 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
         m = top;
       }
       const float safe = m == neg_inf() ? 0.0f : m;
+      const bool factor = __any(sc[0][3] != 1.0f || sc[1][3] != 1.0f);
       bf16x8 p[2][2];
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const float vs = e8m0(ve[half]);
+        const float shift = sc[half][1] - safe;
         float w[16], sum = 0.0f;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          w[r] = exp2_fast(__builtin_fmaf(x[half][r], kk[half], -safe));
+          w[r] = exp2_fast(__builtin_fmaf(x[half][r], kk[half], shift));
           sum += w[r];
-          w[r] *= vs;
         }
-        l += sum;
+        l += sum * sc[half][2];
+        if (factor)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) w[r] *= sc[half][3];
         p[half][0] = round8(w);
         p[half][1] = round8(w + 8);
       }
 #pragma unroll
-      for (int i = 0; i < VT; ++i) {
-        const int d = 32 * i + col;
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int i = 0; i < VT; ++i) {
+          const int d = 32 * i + col;
           const bf16x8 vf = __builtin_bit_cast(bf16x8, sv[buf][d * 8 + ((4 * (j / 2) + 2 * hf + j % 2) ^ ((d >> 1) & 7))]);
           o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[j / 2][j % 2], o[i], 0, 0, 0);
         }
-      }
     }
     // the other buffer was last read before this tile's barrier
     if (more) stage_tile(t0 + 64, buf ^ 1);
@@ -806,10 +803,10 @@ AttnPlan plan_attention(int B, int Hq, int Hkv, int D, int64_t max_new, int64_t 
   // 64 below its first visible key
   int64_t span = max_len < 1 ? 1 : max_len;
   if (window > 0) span = std::min<int64_t>(span, (int64_t)window + max_new - 1 + 63);
-  // ranges: about 2048 workgroups, at least 256 keys each
+  // ranges of keys: about 2048 workgroups, of at least 256 keys each (many
+  // rows: 1024)
   int64_t splits = std::max<int64_t>(1, std::min<int64_t>((2048 + tiles - 1) / tiles, (span + 255) / 256));
-  // many rows: only where the tiles leave half of the card idle
-  if (p.kind == 1) splits = std::max<int64_t>(1, std::min<int64_t>(512 / tiles, (span + 511) / 512));
+  if (p.kind == 1) splits = std::max<int64_t>(1, std::min<int64_t>(2048 / tiles, span / 1024));
   // one arrival counter a tile, below the words a linear call keeps its device scalars in
   if (tiles > kWorkspaceScalarOffset / 4) splits = 1;
   int64_t chunk = round_up((span + splits - 1) / splits, 64);
