@@ -61,7 +61,17 @@ __device__ __forceinline__ bf16x8 load_q8(const uint16_t* p, bool aligned) {
   return __builtin_bit_cast(bf16x8, u);
 }
 
-// The keys row `r` of a sequence's rows sees: [lo, hi).
+// The new token of a row and its head within the group: rows of one kv head
+// are (token, head) with the head running fastest.
+struct Row {
+  int token, head;
+};
+__device__ __forceinline__ Row row_of(const AttnArgs& a, int row) {
+  const int t = (int)(((uint64_t)(uint32_t)row * a.group_mul) >> a.group_shift);
+  return Row{t, row - t * a.group};
+}
+
+// The keys the rows of a new token see: [lo, hi).
 struct Visible {
   int lo, hi;
 };
@@ -105,37 +115,55 @@ __device__ __forceinline__ bool drop_nan(uint4v (&vw)[VT]) {
   return any != 0u;
 }
 
-// Float32 partial results cross XCDs (each with its own L2) like the GEMMs'
-// split-K slabs: agent-scope relaxed stores and loads.
-__device__ __forceinline__ void put_f4(float* p, const float4v& v) {
-  uint64_t* q = reinterpret_cast<uint64_t*>(p);
-  __hip_atomic_store(q, __builtin_bit_cast(uint64_t, float2v{v[0], v[1]}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __hip_atomic_store(q + 1, __builtin_bit_cast(uint64_t, float2v{v[2], v[3]}), __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float4v get_f4(const float* p) {
-  uint64_t* q = const_cast<uint64_t*>(reinterpret_cast<const uint64_t*>(p));
-  const float2v a = __builtin_bit_cast(float2v, __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-  const float2v b = __builtin_bit_cast(float2v, __hip_atomic_load(q + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-  return float4v{a[0], a[1], b[0], b[1]};
-}
-__device__ __forceinline__ void put_f2(float* p, float a, float b) {
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, float2v{a, b}), __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float2v get_f2(const float* p) {
-  uint64_t* q = const_cast<uint64_t*>(reinterpret_cast<const uint64_t*>(p));
-  return __builtin_bit_cast(float2v, __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-}
+// Partial results of one range of keys, float32: for `rows` rows the sums, as
+// [channel pair of four: 0, 1 / 2, 3][D / 4][rows] pairs, then [rows] pairs
+// (maximum, sum of weights). Rows are neighbours in both kernels' lanes, so
+// every store and load of 8 bytes a lane covers whole lines. They cross XCDs
+// (each with its own L2) like the GEMMs' split-K slabs: agent-scope relaxed
+// stores and loads.
+template <int D>
+struct Partial {
+  uint64_t* p;
+  int rows;
+  static __device__ __forceinline__ int64_t floats(int rows) { return (int64_t)rows * (D + 2); }
+  __device__ __forceinline__ Partial(float* slab, int z, int rows)
+      : p(reinterpret_cast<uint64_t*>(slab + z * floats(rows))), rows(rows) {}
+  static __device__ __forceinline__ void put(uint64_t* q, float a, float b) {
+    __hip_atomic_store(q, __builtin_bit_cast(uint64_t, float2v{a, b}), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  static __device__ __forceinline__ float2v get(uint64_t* q) {
+    return __builtin_bit_cast(float2v, __hip_atomic_load(q, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
+  }
+  __device__ __forceinline__ void put4(int row, int d4, const float4v& v) const {
+    put(p + d4 * rows + row, v[0], v[1]);
+    put(p + (D / 4 + d4) * rows + row, v[2], v[3]);
+  }
+  __device__ __forceinline__ float4v get4(int row, int d4) const {
+    const float2v a = get(p + d4 * rows + row), b = get(p + (D / 4 + d4) * rows + row);
+    return float4v{a[0], a[1], b[0], b[1]};
+  }
+  __device__ __forceinline__ void put_ml(int row, float m, float l) const { put(p + (D / 2) * rows + row, m, l); }
+  __device__ __forceinline__ float2v get_ml(int row) const { return get(p + (D / 2) * rows + row); }
+  __device__ __forceinline__ void put_nan(int row, int d) const {
+    float* f = reinterpret_cast<float*>(p + ((d % 4 / 2) * (D / 4) + d / 4) * rows + row) + d % 2;
+    __hip_atomic_store(f, __builtin_nanf(""), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+};
 
 // Four consecutive channels of one output row (sum / l; a row that sees no key
 // gives zeros), and the row's log-sum-exp once.
-__device__ __forceinline__ void write_out4(const AttnArgs& a, const SeqSpan& s, int kv_head, int G, int row, int d,
-                                           const float4v& o, float m, float l) {
-  const int64_t t = s.row0 + row / G;
-  const int head = kv_head * G + row % G;
-  uint16_t* dst = a.out + t * a.o_ld_token + head * a.o_ld_head + d;
-  const float r = l == 0.0f ? 0.0f : 1.0f / l;
+struct OutRow {
+  uint16_t* p;
+  float* lse;
+};
+__device__ __forceinline__ OutRow out_row(const AttnArgs& a, const SeqSpan& s, int kv_head, int row) {
+  const Row r = row_of(a, row);
+  const int64_t t = s.row0 + r.token;
+  const int head = kv_head * a.group + r.head;
+  return OutRow{a.out + t * a.o_ld_token + head * a.o_ld_head, a.lse == nullptr ? nullptr : a.lse + t * a.Hq + head};
+}
+__device__ __forceinline__ void put_out4(const OutRow& q, int d, const float4v& o, float l, float r) {
+  uint16_t* dst = q.p + d;
   uint32_t b[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) b[i] = l == 0.0f ? 0u : f32_to_bf16_bits(o[i] * r);
@@ -145,56 +173,103 @@ __device__ __forceinline__ void write_out4(const AttnArgs& a, const SeqSpan& s, 
 #pragma unroll
     for (int i = 0; i < 4; ++i) dst[i] = (uint16_t)b[i];
   }
-  if (a.lse != nullptr && d == 0) a.lse[t * a.Hq + head] = l == 0.0f ? neg_inf() : kLn2 * m + __logf(l);
+}
+__device__ __forceinline__ void put_lse(const OutRow& q, float m, float l) {
+  if (q.lse != nullptr) *q.lse = l == 0.0f ? neg_inf() : kLn2 * m + __logf(l);
+}
+__device__ __forceinline__ void write_out4(const AttnArgs& a, const SeqSpan& s, int kv_head, int row, int d,
+                                           const float4v& o, float m, float l) {
+  const OutRow q = out_row(a, s, kv_head, row);
+  put_out4(q, d, o, l, l == 0.0f ? 0.0f : 1.0f / l);
+  if (d == 0) put_lse(q, m, l);
 }
 
-// Partial results of one range of keys: float32 [rows][D] sums, then [rows]
-// (maximum, sum) pairs.
-template <int D>
-__device__ __forceinline__ int64_t partial_floats(int rows) {
-  return (int64_t)rows * (D + 2);
-}
-
-// The last workgroup of a row tile to arrive adds the ranges' results in
-// order; an item is four channels of one row.
-template <int D>
-__device__ __forceinline__ void join_ranges(const AttnArgs& a, const SeqSpan& s, int kv_head, int G, int row0,
-                                            int rows_in_tile, int tile_rows, int ns, const float* slab) {
-  const int64_t stride = partial_floats<D>(tile_rows);
-  for (int item = threadIdx.x; item < rows_in_tile * (D / 4); item += blockDim.x) {
-    const int row = item / (D / 4), d = (item % (D / 4)) * 4;
-    const float* ml = slab + (int64_t)tile_rows * D + row * 2;
-    const float* po = slab + (int64_t)row * D + d;
-    float M = neg_inf(), L = 0.0f;
-    float4v o = float4v{0.f, 0.f, 0.f, 0.f};
-    // eight ranges a round, all loads issued before any is used
-    for (int z0 = 0; z0 < ns; z0 += 8) {
-      float2v p[8];
-      float4v v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int z = z0 + j < ns ? z0 + j : ns - 1;
-        p[j] = get_f2(ml + z * stride);
-        v[j] = get_f4(po + z * stride);
-      }
-      float top = M;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = __builtin_fmaxf(top, p[j][0]);
-      const float safe = top == neg_inf() ? 0.0f : top;
-      const float back = exp2_fast(M - safe);
-      M = top;
-      L *= back;
-      o *= back;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (z0 + j < ns) {
-          const float w = exp2_fast(p[j][0] - safe);
-          L += w * p[j][1];
-          o += w * v[j];
-        }
-    }
-    write_out4(a, s, kv_head, G, row0 + row, d, o, M, L);
+// A running softmax-weighted sum of four channels of one row.
+struct Joined {
+  float m, l;
+  float4v o;
+  __device__ __forceinline__ void add(float m2, float l2, const float4v& o2) {
+    const float top = __builtin_fmaxf(m, m2);
+    const float safe = top == neg_inf() ? 0.0f : top;
+    const float a = exp2_fast(m - safe), b = exp2_fast(m2 - safe);
+    l = l * a + l2 * b;
+    o = o * a + o2 * b;
+    m = top;
   }
+};
+
+// The last workgroup of a row tile to arrive joins the ranges' results. An
+// item is four channels of one row. NT threads; where there are fewer items
+// than threads, PT threads share an item (ranges p, p + PT, ...) and join
+// through LDS (`lds`: NT * 24 bytes), else a thread takes items in turn. Loads
+// are issued in rounds of 8 to 16 before any is used; every sum has a fixed
+// order.
+template <int D, int NT>
+__device__ __forceinline__ void join_ranges(const AttnArgs& a, const SeqSpan& s, int kv_head, int row0, int rows,
+                                            int ns, float* slab, float* lds) {
+  const int items = rows * (D / 4), tid = threadIdx.x;
+  if (items >= NT || ns <= 8) {
+    constexpr int U = 2, Z = 4;  // items, ranges a round
+    for (int i0 = tid; i0 < items; i0 += NT * U) {
+      Joined acc[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) acc[u] = Joined{neg_inf(), 0.0f, float4v{0.f, 0.f, 0.f, 0.f}};
+      for (int z0 = 0; z0 < ns; z0 += Z) {
+        float2v ml[U][Z];
+        float4v o[U][Z];
+#pragma unroll
+        for (int z = 0; z < Z; ++z)
+          if (z0 + z < ns) {
+            const Partial<D> p(slab, z0 + z, rows);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int i = i0 + NT * u < items ? i0 + NT * u : i0;
+              ml[u][z] = p.get_ml(i % rows);
+              o[u][z] = p.get4(i % rows, i / rows);
+            }
+          }
+#pragma unroll
+        for (int z = 0; z < Z; ++z)
+          if (z0 + z < ns)
+#pragma unroll
+            for (int u = 0; u < U; ++u) acc[u].add(ml[u][z][0], ml[u][z][1], o[u][z]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + NT * u;
+        if (i < items) write_out4(a, s, kv_head, row0 + i % rows, i / rows * 4, acc[u].o, acc[u].m, acc[u].l);
+      }
+    }
+    return;
+  }
+  const int PT = NT / items, part = tid / items, i = tid % items;
+  Joined acc = {neg_inf(), 0.0f, float4v{0.f, 0.f, 0.f, 0.f}};
+  if (part < PT) {
+    constexpr int Z = 8;
+    for (int z0 = part; z0 < ns; z0 += PT * Z) {
+      float2v ml[Z];
+      float4v o[Z];
+#pragma unroll
+      for (int z = 0; z < Z; ++z) {
+        const int zz = z0 + PT * z < ns ? z0 + PT * z : z0;
+        const Partial<D> p(slab, zz, rows);
+        ml[z] = p.get_ml(i % rows);
+        o[z] = p.get4(i % rows, i / rows);
+      }
+#pragma unroll
+      for (int z = 0; z < Z; ++z)
+        if (z0 + PT * z < ns) acc.add(ml[z][0], ml[z][1], o[z]);
+    }
+    float* q = lds + tid * 6;
+    q[0] = acc.m; q[1] = acc.l; q[2] = acc.o[0]; q[3] = acc.o[1]; q[4] = acc.o[2]; q[5] = acc.o[3];
+  }
+  __syncthreads();
+  if (part != 0) return;
+  for (int t = 1; t < PT; ++t) {
+    const float* q = lds + (t * items + i) * 6;
+    acc.add(q[0], q[1], float4v{q[2], q[3], q[4], q[5]});
+  }
+  write_out4(a, s, kv_head, row0 + i % rows, i / rows * 4, acc.o, acc.m, acc.l);
 }
 
 // Whether this workgroup is the last of `ns` to arrive (its partial results
@@ -218,8 +293,8 @@ __device__ __forceinline__ bool last_to_arrive(uint32_t* counter, int ns, uint32
 // were written: straight (part null) or in the partial results.
 template <int D>
 __device__ void put_nan_rows(const AttnArgs& a, const PagedCache& c, const PagedBatch& pb, const SeqSpan& s, int b,
-                             int h, int G, int bs_shift, int row0, int nrows, int k0, int k1, const Visible& first,
-                             const Visible& last, float* part) {
+                             int h, int bs_shift, int row0, int nrows, int k0, int k1, const Visible& first,
+                             const Visible& last, const Partial<D>* part) {
   __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's outputs are written
   __syncthreads();
   for (int t0 = k0; t0 < k1; t0 += 64) {
@@ -232,12 +307,10 @@ __device__ void put_nan_rows(const AttnArgs& a, const PagedCache& c, const Paged
       for (int d = threadIdx.x; d < D; d += blockDim.x) {
         if ((v[d * 16] & 0x7F) != 0x7F) continue;
         for (int r = 0; r < nrows; ++r) {
-          const Visible w = visible_of(s, (row0 + r) / G, a.causal, a.window);
+          const Visible w = visible_of(s, row_of(a, row0 + r).token, a.causal, a.window);
           if (t < w.lo || t >= w.hi) continue;
-          if (part != nullptr)
-            __hip_atomic_store(part + (int64_t)r * D + d, __builtin_nanf(""), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          else
-            a.out[(s.row0 + (row0 + r) / G) * a.o_ld_token + (h * G + (row0 + r) % G) * a.o_ld_head + d] = 0x7FC0;
+          if (part != nullptr) part->put_nan(r, d);
+          else out_row(a, s, h, row0 + r).p[d] = 0x7FC0;
         }
       }
     }
@@ -248,8 +321,9 @@ __device__ void put_nan_rows(const AttnArgs& a, const PagedCache& c, const Paged
 // few rows: every wave its own keys
 // ---------------------------------------------------------------------------
 //
-// NC tiles of 16 rows; the four waves of a workgroup take 64-token tiles in
-// turn and keep their own running maximum, sum and output, joined through LDS
+// NC tiles of 16 rows; the W waves of a workgroup (eight where their registers
+// allow it: the more, the fewer ranges have to be joined across workgroups)
+// take 64-token tiles in turn and keep their own running maximum, sum and output, joined through LDS
 // at the end. The call is a stream over the cache: codes go straight from
 // memory into registers (16-byte loads; keys: a lane's 16 bytes of 4
 // neighbouring lanes make 64 bytes of a row, values: 256-byte runs), the next
@@ -265,31 +339,36 @@ __device__ void put_nan_rows(const AttnArgs& a, const PagedCache& c, const Paged
 //     64 (s / 2) + 16 g + 8 (s % 2) + j (keys and queries alike).
 //   O^T step s (0, 1): k = 8 g + j is token 16 g + 8 s + j, byte 8 s + j of the
 //     lane's 16-byte piece of channel l % 16.
+constexpr int stream_waves(int D, int NC) { return D * NC <= 128 ? 8 : 4; }
+
 template <int D, int NC>
-__global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, const PagedCache c,
+__global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kernel(const AttnArgs a, const PagedCache c,
                                                               const PagedBatch pb, int bs_shift, int row_tiles,
                                                               int splits, int chunk, float* partial,
                                                               uint32_t* counters) {
-  constexpr int KI = D / 64, VT = D / 16, SK = D / 32;
-  __shared__ float4v so[4][NC * VT][64];
-  __shared__ float2v sml[4][NC][16];
+  constexpr int KI = D / 64, VT = D / 16, SK = D / 32, W = stream_waves(D, NC), STEP = 64 * W;
+  __shared__ float4v so[W][NC * VT][64];
+  __shared__ float2v sml[W][NC][16];
   __shared__ uint32_t s_flag, s_nan;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, g = lane >> 4;
-  const int bh = blockIdx.x, H = c.heads, h = bh % H, b = bh / H;
-  const int rt = blockIdx.y % row_tiles, z = blockIdx.y / row_tiles;
-  const int G = a.Hq / H, bs = c.block_size;
+  const int h = blockIdx.x, b = blockIdx.y, H = c.heads, bs = c.block_size;
+  const int z = splits == 1 ? 0 : (int)blockIdx.z / row_tiles;
+  const int rt = (int)blockIdx.z - z * row_tiles;
   const SeqSpan s = seq_span(pb, b, bs);
-  const int rows = s.n * G, row0 = rt * 16 * NC;
+  const int rows = s.n * a.group, row0 = rt * 16 * NC;
   if (row0 >= rows) return;
   const int last_row = row0 + 16 * NC < rows ? row0 + 16 * NC - 1 : rows - 1;
   // every row sees [last.lo, first.hi), some row each of [first.lo, last.hi)
-  const Visible first = visible_of(s, row0 / G, a.causal, a.window);
-  const Visible last = visible_of(s, last_row / G, a.causal, a.window);
+  const Visible first = visible_of(s, row_of(a, row0).token, a.causal, a.window);
+  const Visible last = visible_of(s, row_of(a, last_row).token, a.causal, a.window);
   const int kmin = first.lo & ~63, kmax = last.hi;
-  int ns = kmax > kmin ? (kmax - kmin + chunk - 1) / chunk : 1;
-  ns = ns < splits ? ns : splits;
+  int ns = 1;
+  if (splits > 1) {
+    ns = kmax > kmin ? (kmax - kmin + chunk - 1) / chunk : 1;
+    ns = ns < splits ? ns : splits;
+  }
   if (z >= ns) return;
   const int k0 = kmin + z * chunk;
   const int k1 = z == ns - 1 || k0 + chunk > kmax ? kmax : k0 + chunk;
@@ -304,11 +383,11 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
   for (int t = 0; t < NC; ++t) {
     const int row = row0 + 16 * t + col;
     const bool ok = row < rows;
-    const int token = ok ? row / G : 0;
-    const Visible v = visible_of(s, token, a.causal, a.window);
+    const Row rw = row_of(a, ok ? row : 0);
+    const Visible v = visible_of(s, rw.token, a.causal, a.window);
     vlo[t] = v.lo;
     vhi[t] = ok ? v.hi : 0;
-    const uint16_t* qp = a.q + (s.row0 + token) * a.q_ld_token + (int64_t)(h * G + (ok ? row % G : 0)) * a.q_ld_head;
+    const uint16_t* qp = a.q + (s.row0 + rw.token) * a.q_ld_token + (int64_t)(h * a.group + rw.head) * a.q_ld_head;
 #pragma unroll
     for (int i = 0; i < SK; ++i) {
       q[t][i] = load_q8(qp + 64 * (i / 2) + 16 * g + 8 * (i % 2), a.aligned);
@@ -371,9 +450,9 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
     load_scales(blk);
     load_v(t0, blk);
   }
-  for (; t0 < k1; t0 += 256) {
-    const int64_t blk_next = block_of(t0 + 256 + 16 * g), blk_k_next = block_of(t0 + 256 + 16 * (col >> 2));
-    const bool more = t0 + 256 < k1;
+  for (; t0 < k1; t0 += STEP) {
+    const int64_t blk_next = block_of(t0 + STEP + 16 * g), blk_k_next = block_of(t0 + STEP + 16 * (col >> 2));
+    const bool more = t0 + STEP < k1;
     float x[NC][16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -393,7 +472,7 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
         for (int r = 0; r < 4; ++r) x[t][4 * i + r] = acc[t][r];
     }
     const float ks = e8m0(ksb) * sl2, vs = e8m0(vsb);
-    if (more) load_k(t0 + 256, blk_k_next);
+    if (more) load_k(t0 + STEP, blk_k_next);
     const int tg = t0 + 16 * g;  // this lane's 16 tokens start here
     // Masked in edge tiles only: keys hidden from some row, past this range
     // (the ranges meet at multiples of 64, so only past kmax) or of a block
@@ -460,11 +539,11 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
     blk = blk_next;
     if (more) {
       load_scales(blk);
-      load_v(t0 + 256, blk);
+      load_v(t0 + STEP, blk);
     }
   }
 
-  // join the four waves
+  // join the waves
 #pragma unroll
   for (int t = 0; t < NC; ++t) {
     l[t] += __shfl_xor(l[t], 16);
@@ -474,19 +553,20 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
     for (int i = 0; i < VT; ++i) so[wave][t * VT + i][lane] = o[t][i];
   }
   __syncthreads();
-  const int tile = (bh * row_tiles + rt);
-  float* slab = partial + (int64_t)tile * splits * partial_floats<D>(16 * NC);
-  float* mine = slab + z * partial_floats<D>(16 * NC);
-  for (int f = wave; f < NC * VT; f += 4) {
+  const int tile = (b * H + h) * row_tiles + rt;
+  const int nrows = last_row - row0 + 1;
+  float* slab = partial + (int64_t)tile * splits * Partial<D>::floats(16 * NC);
+  const Partial<D> mine(slab, z, nrows);
+  for (int f = wave; f < NC * VT; f += W) {
     const int t = f / VT, i = f % VT;
     float M = neg_inf();
 #pragma unroll
-    for (int w = 0; w < 4; ++w) M = __builtin_fmaxf(M, sml[w][t][col][0]);
+    for (int w = 0; w < W; ++w) M = __builtin_fmaxf(M, sml[w][t][col][0]);
     const float safe = M == neg_inf() ? 0.0f : M;
     float L = 0.0f;
     float4v sum = float4v{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float2v ml = sml[w][t][col];
       const float f2 = exp2_fast(ml[0] - safe);
       L += f2 * ml[1];
@@ -495,18 +575,18 @@ __global__ __launch_bounds__(256) void attn_kv8_stream_kernel(const AttnArgs a, 
     const int row = 16 * t + col, d = 16 * i + 4 * g;
     if (row0 + row >= rows) continue;
     if (ns == 1) {
-      write_out4(a, s, h, G, row0 + row, d, sum, M, L);
+      write_out4(a, s, h, row0 + row, d, sum, M, L);
     } else {
-      put_f4(mine + (int64_t)row * D + d, sum);
-      if (d == 0) put_f2(mine + (int64_t)16 * NC * D + row * 2, M, L);
+      mine.put4(row, d / 4, sum);
+      if (d == 0) mine.put_ml(row, M, L);
     }
   }
   if (s_nan != 0u)
-    put_nan_rows<D>(a, c, pb, s, b, h, G, bs_shift, row0, last_row - row0 + 1, k0, k1, first, last,
-                    ns == 1 ? nullptr : mine);
+    put_nan_rows<D>(a, c, pb, s, b, h, bs_shift, row0, nrows, k0, k1, first, last,
+                    ns == 1 ? nullptr : &mine);
   if (ns == 1) return;
   if (last_to_arrive(counters + tile, ns, &s_flag))
-    join_ranges<D>(a, s, h, G, row0, last_row - row0 + 1, 16 * NC, ns, slab);
+    join_ranges<D, 64 * W>(a, s, h, row0, nrows, ns, slab, reinterpret_cast<float*>(&so[0][0][0]));
 }
 
 // ---------------------------------------------------------------------------
@@ -547,19 +627,22 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hf = lane >> 5;
-  const int bh = blockIdx.x, H = c.heads, h = bh % H, b = bh / H;
+  const int h = blockIdx.x, b = blockIdx.y, H = c.heads, bs = c.block_size;
+  const int z = splits == 1 ? 0 : (int)blockIdx.z / row_tiles;
   // the last row tiles see the most keys under a causal mask: they start first
-  const int rt = row_tiles - 1 - (int)blockIdx.y % row_tiles, z = blockIdx.y / row_tiles;
-  const int G = a.Hq / H, bs = c.block_size;
+  const int rt = row_tiles - 1 - ((int)blockIdx.z - z * row_tiles);
   const SeqSpan s = seq_span(pb, b, bs);
-  const int rows = s.n * G, row0 = rt * ROWS;
+  const int rows = s.n * a.group, row0 = rt * ROWS;
   if (row0 >= rows) return;
   const int last_row = row0 + ROWS < rows ? row0 + ROWS - 1 : rows - 1;
-  const Visible first = visible_of(s, row0 / G, a.causal, a.window);
-  const Visible last = visible_of(s, last_row / G, a.causal, a.window);
+  const Visible first = visible_of(s, row_of(a, row0).token, a.causal, a.window);
+  const Visible last = visible_of(s, row_of(a, last_row).token, a.causal, a.window);
   const int kmin = first.lo & ~63, kmax = last.hi;
-  int ns = kmax > kmin ? (kmax - kmin + chunk - 1) / chunk : 1;
-  ns = ns < splits ? ns : splits;
+  int ns = 1;
+  if (splits > 1) {
+    ns = kmax > kmin ? (kmax - kmin + chunk - 1) / chunk : 1;
+    ns = ns < splits ? ns : splits;
+  }
   if (z >= ns) return;
   const int k0 = kmin + z * chunk;
   const int k1 = z == ns - 1 || k0 + chunk > kmax ? kmax : k0 + chunk;
@@ -567,19 +650,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
   __syncthreads();
 
   // this lane's query row, and the keys that all (some) rows of the wave see
-  const int row = row0 + 32 * wave + col;
+  const int wrow = row0 + 32 * wave, row = wrow + col;
   const bool ok = row < rows;
-  const Visible mine = visible_of(s, ok ? row / G : 0, a.causal, a.window);
+  const Row rw = row_of(a, ok ? row : 0);
+  const Visible mine = visible_of(s, rw.token, a.causal, a.window);
   const int vlo = mine.lo, vhi = ok ? mine.hi : 0;
-  const int wfirst = row0 + 32 * wave < rows ? row0 + 32 * wave : rows - 1;
-  const int wlast = row0 + 32 * wave + 31 < rows ? row0 + 32 * wave + 31 : rows - 1;
-  const int wave_all_lo = visible_of(s, wlast / G, a.causal, a.window).lo;
-  const int wave_all_hi = visible_of(s, wfirst / G, a.causal, a.window).hi;
-  const int wave_any_hi = row0 + 32 * wave < rows ? visible_of(s, wlast / G, a.causal, a.window).hi : 0;
+  const Visible wave_last = visible_of(s, row_of(a, wrow + 31 < rows ? wrow + 31 : rows - 1).token, a.causal, a.window);
+  const int wave_all_lo = wave_last.lo;
+  const int wave_all_hi = visible_of(s, row_of(a, wrow < rows ? wrow : rows - 1).token, a.causal, a.window).hi;
+  const int wave_any_hi = wrow < rows ? wave_last.hi : 0;
   bf16x8 q[SK];
   {
-    const uint16_t* qp = a.q + (s.row0 + (ok ? row / G : 0)) * a.q_ld_token +
-                         (int64_t)(h * G + (ok ? row % G : 0)) * a.q_ld_head + 8 * hf;
+    const uint16_t* qp = a.q + (s.row0 + rw.token) * a.q_ld_token + (int64_t)(h * a.group + rw.head) * a.q_ld_head + 8 * hf;
 #pragma unroll
     for (int i = 0; i < SK; ++i) {
       q[i] = load_q8(qp + 16 * i, a.aligned);
@@ -604,11 +686,13 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
   const int pd = tid % D, g0 = __builtin_amdgcn_readfirstlane(tid / D);
   constexpr int GS = T / D;  // groups a pass
   const int32_t* table = pb.table + (int64_t)b * pb.ld_table;
-  const int64_t head_bytes = (int64_t)bs * D;
+  const uint32_t head_bytes = (uint32_t)(bs * D);
   uint4v kw[KP], vw[KP];
   int blk[KP], entry[KP];  // blocks of the tile loaded last, table entries of the one after it
   uint32_t ksb[KP], vsb[KP];
-  auto look_up = [&](int t0) {  // past the last key the last entry: see load_tile
+  // Past the last key the last entry is looked up, and its block (or block 0
+  // where it is none) is read and masked.
+  auto look_up = [&](int t0) {
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
       const int t = t0 + 16 * (g0 + GS * i);
@@ -619,46 +703,60 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
       const int e = __builtin_amdgcn_readfirstlane(entry[i]);
-      blk[i] = t0 + 16 * (g0 + GS * i) < kmax && e >= 0 && e < c.num_blocks ? e : -1;
+      const bool in = (uint32_t)e < (uint32_t)c.num_blocks;
+      blk[i] = in && t0 + 16 * (g0 + GS * i) < kmax ? e : -1;
+      const uint32_t at = (uint32_t)(in ? e : 0) * (uint32_t)H + (uint32_t)h;  // num_blocks * heads < 2^31
       const int off = (t0 + 16 * (g0 + GS * i)) & (bs - 1);
-      const int64_t at = (int64_t)(blk[i] < 0 ? 0 : blk[i]) * H + h;
-      const int64_t base = at * head_bytes + off * D;
+      const uint64_t base = (uint64_t)at * head_bytes + (uint32_t)(off * D);
       kw[i] = *reinterpret_cast<const uint4v*>(c.k + base + 16 * pd);
       vw[i] = *reinterpret_cast<const uint4v*>(c.v + base + 16 * pd);
       ksb[i] = c.k_scale[at];
       vsb[i] = c.v_scale[at];
     }
   };
-  auto stage_tile = [&](int t0, int buf) {
-    // tokens that no row sees may hold anything: their values are zeroed; NaN
-    // where rows differ in what they see: see put_nan_rows
-    const bool some = t0 + 64 > first.hi || t0 < last.lo || t0 + 64 > kmax;
+  // Edges of the values loaded: tokens that no row sees may hold anything, they
+  // become zeros; NaN where rows differ in what they see: see put_nan_rows.
+  auto trim_values = [&](int t0) {
+    bool absent = false;
+#pragma unroll
+    for (int i = 0; i < KP; ++i) absent |= blk[i] < 0;
+    if (t0 + 64 > first.hi || t0 < last.lo || absent) {
+#pragma unroll
+      for (int i = 0; i < KP; ++i) {
+        uint4v u[1] = {vw[i]};
+        const int t = t0 + 16 * (g0 + GS * i);
+        mask_values<1>(u, blk[i] < 0 ? 0 : clamp16(kmax - t), clamp16(first.lo - t));
+        if (drop_nan<1>(u)) s_nan = 1u;
+        vw[i] = u[0];
+      }
+    }
+  };
+  auto widen_tile = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < KP; ++i) {
       const int g = g0 + GS * i;
       const int tok = pd / (D / 16), kc = pd % (D / 16);
       const int lrow = 32 * (g >> 1) + 8 * (tok >> 2) + 4 * (g & 1) + (tok & 3);
-      const int key = D == 64 ? (lrow >> 1) & 7 : lrow & 15;
+      const int key = D == 64 ? (lrow >> 1) & 7 : lrow & 15, vkey = (pd >> 1) & 7;
       uint4v* kd = &sk[buf][lrow * KC];
       kd[(2 * kc) ^ key] = __builtin_bit_cast(uint4v, widen8(kw[i][0], kw[i][1]));
       kd[(2 * kc + 1) ^ key] = __builtin_bit_cast(uint4v, widen8(kw[i][2], kw[i][3]));
-      uint4v u[1] = {vw[i]};
-      if (some || blk[i] < 0) {
-        const int t = t0 + 16 * g;
-        mask_values<1>(u, blk[i] < 0 ? 0 : clamp16(kmax - t), clamp16(first.lo - t));
-        if (drop_nan<1>(u)) s_nan = 1u;
-      }
-      const int vkey = (pd >> 1) & 7;
       uint4v* vd = &sv[buf][pd * 8];
-      vd[(2 * g) ^ vkey] = __builtin_bit_cast(uint4v, widen8(u[0][0], u[0][1]));
-      vd[(2 * g + 1) ^ vkey] = __builtin_bit_cast(uint4v, widen8(u[0][2], u[0][3]));
-      if (pd == 0) {
+      vd[(2 * g) ^ vkey] = __builtin_bit_cast(uint4v, widen8(vw[i][0], vw[i][1]));
+      vd[(2 * g + 1) ^ vkey] = __builtin_bit_cast(uint4v, widen8(vw[i][2], vw[i][3]));
+    }
+  };
+  auto stage_scales = [&](int buf) {
+    if (pd == 0) {
+#pragma unroll
+      for (int i = 0; i < KP; ++i) {
         // the weights take the value scale 2^ev in their exponent; what lies
         // outside +-100 (no exponent's bits are lost there) is a factor of its own
         const int ev = blk[i] < 0 ? 0 : (int)vsb[i] - 127;
         const int e = ev < -100 ? -100 : (ev > 100 ? 100 : ev);
-        ss[buf][g] = float4v{blk[i] < 0 ? -1.0f : e8m0(ksb[i]) * sl2, (float)e,
-                             __uint_as_float((uint32_t)(127 - e) << 23), __uint_as_float((uint32_t)(127 + ev - e) << 23)};
+        ss[buf][g0 + GS * i] =
+            float4v{blk[i] < 0 ? -1.0f : e8m0(ksb[i]) * sl2, (float)e, __uint_as_float((uint32_t)(127 - e) << 23),
+                    __uint_as_float((uint32_t)(127 + ev - e) << 23)};
       }
     }
   };
@@ -667,121 +765,152 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
     look_up(k0);
     load_tile(k0);
     look_up(k0 + 64);
-    stage_tile(k0, 0);
+    trim_values(k0);
+    widen_tile(0);
+    stage_scales(0);
   }
   int buf = 0;
   for (int t0 = k0; t0 < k1; t0 += 64, buf ^= 1) {
-    const bool more = t0 + 64 < k1;
-    if (more) {
-      load_tile(t0 + 64);
-      look_up(t0 + 128);
-    }
     __syncthreads();
-    if (t0 < wave_any_hi) {
-      float16v x[2];
+    load_tile(t0 + 64);  // after the last tile: masked, and never read
+    look_up(t0 + 128);
+    if (t0 >= wave_any_hi) {  // no row of this wave sees the tile
+      trim_values(t0 + 64);
+      widen_tile(buf ^ 1);
+      stage_scales(buf ^ 1);
+      continue;
+    }
+    float16v x[2];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) x[0][r] = x[1][r] = 0.0f;
-      const int key = D == 64 ? (col >> 1) & 7 : col & 15;  // of rows col and 32 + col alike
+    for (int r = 0; r < 16; ++r) x[0][r] = x[1][r] = 0.0f;
+    const int key = D == 64 ? (col >> 1) & 7 : col & 15;  // of rows col and 32 + col alike
+    // Fragments are read in batches ahead of the products: left to itself the
+    // compiler reads each just before its use, and every pair of products then
+    // waits out an LDS access.
+    constexpr int KB = 8, VB = 4;
 #pragma unroll
-      for (int i = 0; i < SK; ++i)
+    for (int f0 = 0; f0 < 2 * SK; f0 += KB) {
+      uint4v kf[KB];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const bf16x8 kf = __builtin_bit_cast(bf16x8, sk[buf][(32 * half + col) * KC + ((2 * i + hf) ^ key)]);
-          x[half] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, q[i], x[half], 0, 0, 0);
-        }
-      const float4v sc[2] = {ss[buf][hf], ss[buf][2 + hf]};
-      float kk[2] = {sc[0][0], sc[1][0]};
-      if (t0 < wave_all_lo || t0 + 64 > wave_all_hi || t0 + 64 > k1 || __any(__builtin_fminf(kk[0], kk[1]) < 0.0f)) {
+      for (int f = 0; f < KB; ++f) kf[f] = sk[buf][(32 * (f % 2) + col) * KC + ((2 * ((f0 + f) / 2) + hf) ^ key)];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int tg = t0 + 32 * half + 16 * hf;
-          const int have = kk[half] < 0.0f ? 0 : clamp16(k1 - tg);
-          const int lo = clamp16(vlo - tg), hi = clamp16(vhi - tg);
-          const int upto = hi < have ? hi : have;
+      for (int f = 0; f < KB; ++f)
+        x[f % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[f]), q[(f0 + f) / 2], x[f % 2], 0, 0, 0);
+    }
+    // the first values arrive during the softmax
+    uint4v vf[2][VB];
+    auto read_v = [&](int f0, uint4v (&dst)[VB]) {
 #pragma unroll
-          for (int r = 0; r < 16; ++r) x[half][r] = r >= lo && r < upto ? x[half][r] * kk[half] : neg_inf();
-          kk[half] = 1.0f;
-        }
+      for (int f = 0; f < VB; ++f) {
+        const int j = (f0 + f) / VT, d = 32 * ((f0 + f) % VT) + col;
+        dst[f] = sv[buf][d * 8 + ((4 * (j / 2) + 2 * hf + j % 2) ^ ((d >> 1) & 7))];
       }
-      float top = neg_inf();
+    };
+    read_v(0, vf[0]);
+    const float4v sc[2] = {ss[buf][hf], ss[buf][2 + hf]};
+    float kk[2] = {sc[0][0], sc[1][0]};
+    if (t0 < wave_all_lo || t0 + 64 > wave_all_hi || t0 + 64 > k1 || __any(__builtin_fminf(kk[0], kk[1]) < 0.0f)) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        float t = x[half][0];
+        const int tg = t0 + 32 * half + 16 * hf;
+        const int have = kk[half] < 0.0f ? 0 : clamp16(k1 - tg);
+        const int lo = clamp16(vlo - tg), hi = clamp16(vhi - tg);
+        const int upto = hi < have ? hi : have;
 #pragma unroll
-        for (int r = 1; r < 16; ++r) t = __builtin_fmaxf(t, x[half][r]);
-        top = __builtin_fmaxf(top, t * kk[half]);  // kk >= 0
+        for (int r = 0; r < 16; ++r) x[half][r] = r >= lo && r < upto ? x[half][r] * kk[half] : neg_inf();
+        kk[half] = 1.0f;
       }
-      {
-        const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-        top = __builtin_fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+    }
+    float top = neg_inf();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float t = x[half][0];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) t = __builtin_fmaxf(t, x[half][r]);
+      top = __builtin_fmaxf(top, t * kk[half]);  // kk >= 0
+    }
+    {
+      const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+      top = __builtin_fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+    }
+    if (__any(top > m + 8.0f)) {
+      top = __builtin_fmaxf(top, m);
+      const float back = exp2_fast(m - (top == neg_inf() ? 0.0f : top));
+      l *= back;
+#pragma unroll
+      for (int i = 0; i < VT; ++i) o[i] *= back;
+      m = top;
+    }
+    const float safe = m == neg_inf() ? 0.0f : m;
+    const bool factor = __any(sc[0][3] != 1.0f || sc[1][3] != 1.0f);
+    trim_values(t0 + 64);
+    bf16x8 p[2][2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const float shift = sc[half][1] - safe;
+      float w[16], sum = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        w[r] = exp2_fast(__builtin_fmaf(x[half][r], kk[half], shift));
+        sum += w[r];
       }
-      if (__any(top > m + 8.0f)) {
-        top = __builtin_fmaxf(top, m);
-        const float back = exp2_fast(m - (top == neg_inf() ? 0.0f : top));
-        l *= back;
-#pragma unroll
-        for (int i = 0; i < VT; ++i) o[i] *= back;
-        m = top;
-      }
-      const float safe = m == neg_inf() ? 0.0f : m;
-      const bool factor = __any(sc[0][3] != 1.0f || sc[1][3] != 1.0f);
-      bf16x8 p[2][2];
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float shift = sc[half][1] - safe;
-        float w[16], sum = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          w[r] = exp2_fast(__builtin_fmaf(x[half][r], kk[half], shift));
-          sum += w[r];
-        }
-        l += sum * sc[half][2];
-        if (factor)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) w[r] *= sc[half][3];
-        p[half][0] = round8(w);
-        p[half][1] = round8(w + 8);
-      }
+      l += sum * sc[half][2];
+      p[half][0] = round8(w);
+      p[half][1] = round8(w + 8);
+    }
+    if (factor)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < VT; ++i) {
-          const int d = 32 * i + col;
-          const bf16x8 vf = __builtin_bit_cast(bf16x8, sv[buf][d * 8 + ((4 * (j / 2) + 2 * hf + j % 2) ^ ((d >> 1) & 7))]);
-          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf, p[j / 2][j % 2], o[i], 0, 0, 0);
-        }
+        for (int e = 0; e < 8; ++e) p[j / 2][j % 2][e] = (__bf16)((float)p[j / 2][j % 2][e] * sc[j / 2][3]);  // exact
+#pragma unroll
+    for (int f0 = 0; f0 < 4 * VT; f0 += VB) {
+      if (f0 + VB < 4 * VT) read_v(f0 + VB, vf[(f0 / VB + 1) % 2]);
+#pragma unroll
+      for (int f = 0; f < VB; ++f) {
+        const int j = (f0 + f) / VT, i = (f0 + f) % VT;
+        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[(f0 / VB) % 2][f]), p[j / 2][j % 2], o[i], 0, 0, 0);
+      }
     }
     // the other buffer was last read before this tile's barrier
-    if (more) stage_tile(t0 + 64, buf ^ 1);
+    widen_tile(buf ^ 1);
+    stage_scales(buf ^ 1);
   }
+  __syncthreads();  // the buffers are free, s_nan is whole
 
   {
     const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
     l = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
   }
-  const int tile = bh * row_tiles + rt;
-  float* slab = partial + (int64_t)tile * splits * partial_floats<D>(ROWS);
-  float* mine_p = slab + z * partial_floats<D>(ROWS);
+  const int tile = (b * H + h) * row_tiles + rt;
+  const int nrows = last_row - row0 + 1;
+  float* slab = partial + (int64_t)tile * splits * Partial<D>::floats(ROWS);
+  const Partial<D> part(slab, z, nrows);
   if (ok) {
     const int lr = 32 * wave + col;
+    const OutRow dst = out_row(a, s, h, row);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int i = 0; i < VT; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float4v v = float4v{o[i][4 * r], o[i][4 * r + 1], o[i][4 * r + 2], o[i][4 * r + 3]};
         const int d = 32 * i + 8 * r + 4 * hf;
-        if (ns == 1) write_out4(a, s, h, G, row, d, v, m, l);
-        else put_f4(mine_p + (int64_t)lr * D + d, v);
+        if (ns == 1) put_out4(dst, d, v, l, inv);
+        else part.put4(lr, d / 4, v);
       }
-    if (ns > 1 && hf == 0) put_f2(mine_p + (int64_t)ROWS * D + lr * 2, m, l);
+    if (hf == 0) {
+      if (ns == 1) put_lse(dst, m, l);
+      else part.put_ml(lr, m, l);
+    }
   }
-  __syncthreads();  // s_nan
   if (s_nan != 0u)
-    put_nan_rows<D>(a, c, pb, s, b, h, G, bs_shift, row0, last_row - row0 + 1, k0, k1, first, last,
-                    ns == 1 ? nullptr : mine_p);
+    put_nan_rows<D>(a, c, pb, s, b, h, bs_shift, row0, nrows, k0, k1, first, last,
+                    ns == 1 ? nullptr : &part);
   if (ns == 1) return;
   if (last_to_arrive(counters + tile, ns, &s_flag))
-    join_ranges<D>(a, s, h, G, row0, last_row - row0 + 1, ROWS, ns, slab);
+    join_ranges<D, T>(a, s, h, row0, nrows, ns, slab, reinterpret_cast<float*>(&sk[0][0]));
 }
 
 }  // namespace
@@ -827,24 +956,30 @@ std::string describe_attention(const AttnPlan& p, int D) {
   return std::string(b);
 }
 
-hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, const PagedCache& c, const PagedBatch& pb,
+hipError_t launch_attention(const AttnPlan& p, AttnArgs a, const PagedCache& c, const PagedBatch& pb,
                             uint8_t* workspace, hipStream_t st) {
+  // n / group for n < 2^31: with 2^s >= group * 2^31 > 2^(s - 1) and mul =
+  // floor(2^s / group) + 1 < 2^32, mul * group exceeds 2^s by at most group
+  a.group = a.Hq / c.heads;
+  a.group_shift = 31;
+  while (((uint64_t)1 << (a.group_shift - 31)) < (uint64_t)a.group) ++a.group_shift;
+  a.group_mul = (uint32_t)((((uint64_t)1 << a.group_shift) / (uint64_t)a.group) + 1);
   int shift = 4;
   while ((1 << shift) < c.block_size) ++shift;
   uint32_t* counters = reinterpret_cast<uint32_t*>(workspace);
   float* partial = reinterpret_cast<float*>(workspace + p.counter_bytes);
-  const dim3 grid((unsigned)(pb.B * c.heads), (unsigned)(p.row_tiles * p.splits), 1);
+  const dim3 grid((unsigned)c.heads, (unsigned)pb.B, (unsigned)(p.row_tiles * p.splits));
 #define FQL_A(KIND, KERNEL, DD, N, THREADS)                                                               \
   if (p.kind == KIND && c.D == DD && p.cols == N) {                                                       \
     KERNEL<DD, N><<<grid, THREADS, 0, st>>>(a, c, pb, shift, p.row_tiles, p.splits, p.chunk, partial,     \
                                             counters);                                                    \
     return hipGetLastError();                                                                             \
   }
-  FQL_A(0, attn_kv8_stream_kernel, 64, 1, 256)
-  FQL_A(0, attn_kv8_stream_kernel, 64, 2, 256)
-  FQL_A(0, attn_kv8_stream_kernel, 128, 1, 256)
-  FQL_A(0, attn_kv8_stream_kernel, 128, 2, 256)
-  FQL_A(0, attn_kv8_stream_kernel, 256, 1, 256)
+  FQL_A(0, attn_kv8_stream_kernel, 64, 1, (64 * stream_waves(64, 1)))
+  FQL_A(0, attn_kv8_stream_kernel, 64, 2, (64 * stream_waves(64, 2)))
+  FQL_A(0, attn_kv8_stream_kernel, 128, 1, (64 * stream_waves(128, 1)))
+  FQL_A(0, attn_kv8_stream_kernel, 128, 2, (64 * stream_waves(128, 2)))
+  FQL_A(0, attn_kv8_stream_kernel, 256, 1, (64 * stream_waves(256, 1)))
   FQL_A(1, attn_kv8_tile_kernel, 64, 4, 256)
   FQL_A(1, attn_kv8_tile_kernel, 128, 4, 256)
   FQL_A(1, attn_kv8_tile_kernel, 256, 4, 256)

@@ -1082,7 +1082,8 @@ int check_cache(const fql_kv_cache* c, const fql_kv_batch* b, fql::PagedCache* p
   if (bs < 16 || bs > 256 || (bs & (bs - 1)) != 0)
     return fail(FQL_ERR_UNSUPPORTED, "block_size must be 16, 32, 64, 128 or 256 (got %d)", bs);
   if (c->kv_heads < 1 || c->kv_heads > 4096) return fail(FQL_ERR_INVALID, "kv_heads must be in 1 .. 4096");
-  if (c->num_blocks < 1 || c->num_blocks > INT32_MAX) return fail(FQL_ERR_INVALID, "num_blocks out of range");
+  if (c->num_blocks < 1 || c->num_blocks > INT32_MAX / c->kv_heads)
+    return fail(FQL_ERR_INVALID, "num_blocks must be positive, and num_blocks * kv_heads below 2^31");
   if (b->batch < 1 || b->batch > 65535) return fail(FQL_ERR_INVALID, "batch must be in 1 .. 65535 (got %d)", b->batch);
   if (!b->block_table || !b->lens || !b->cu_seqlens) return fail(FQL_ERR_INVALID, "null batch pointer");
   if (b->table_cols < 1 || b->ld_table < b->table_cols)

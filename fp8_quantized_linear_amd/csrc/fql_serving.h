@@ -134,12 +134,15 @@ struct AttnArgs {
   int64_t o_ld_token, o_ld_head;
   float* lse;         // float32 [T][Hq] or null: log of the softmax's denominator (natural)
   int Hq;
+  int group;             // query heads of one kv head, Hq / heads
+  uint32_t group_mul;    // n / group = (n * group_mul) >> group_shift for 0 <= n < 2^31
+  int group_shift;       // (both set by launch_attention)
   float scale;        // of the scores
   int causal;
   int window;         // keys at positions <= p - window are hidden from position p; 0: none
   bool aligned;       // q rows 16-byte aligned
 };
-hipError_t launch_attention(const AttnPlan& p, const AttnArgs& a, const PagedCache& c, const PagedBatch& pb,
+hipError_t launch_attention(const AttnPlan& p, AttnArgs a, const PagedCache& c, const PagedBatch& pb,
                             uint8_t* workspace, hipStream_t st);
 
 }  // namespace fql
