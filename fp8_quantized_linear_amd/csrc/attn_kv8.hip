@@ -339,7 +339,7 @@ __device__ void put_nan_rows(const AttnArgs& a, const PagedCache& c, const Paged
 //     64 (s / 2) + 16 g + 8 (s % 2) + j (keys and queries alike).
 //   O^T step s (0, 1): k = 8 g + j is token 16 g + 8 s + j, byte 8 s + j of the
 //     lane's 16-byte piece of channel l % 16.
-constexpr int stream_waves(int D, int NC) { return D * NC <= 128 ? 8 : 4; }
+constexpr int stream_waves(int D, int NC) { return D * NC <= 128 || D == 128 ? 8 : 4; }
 
 template <int D, int NC>
 __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kernel(const AttnArgs a, const PagedCache c,
@@ -407,51 +407,54 @@ __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kern
     for (int i = 0; i < VT; ++i) o[t][i] = float4v{0.f, 0.f, 0.f, 0.f};
   }
 
-  const int64_t page_bytes = (int64_t)H * bs * D;
+  const uint64_t page_bytes = (uint64_t)H * bs * D;
   const uint8_t* kbase = c.k + (int64_t)h * bs * D + (col & 3) * D + 16 * g;
   const uint8_t* vbase = c.v + (int64_t)h * bs * D + col * 16;
   const int32_t* table = pb.table + (int64_t)b * pb.ld_table;
-  // the block of token t: -1 past the keys of this workgroup or outside the cache
-  auto block_of = [&](int t) -> int64_t {
-    if (t >= kmax) return -1;  // kmax <= len <= the table's capacity
-    const int64_t p = table[t >> bs_shift];
-    return p >= 0 && p < c.num_blocks ? p : -1;
+  // Blocks are looked up two tiles ahead, before that tile's loads are issued:
+  // loads return in order, so a table entry asked for any later would make the
+  // next keys wait for all loads before it. Past the last key the last entry
+  // is taken; kmax <= len <= the table's capacity.
+  struct Entries {
+    int k, v;  // of this lane's keys (tokens 16 (col / 4) ..) and of its values and scales (16 g ..)
+  };
+  auto look_up = [&](int t0) -> Entries {
+    const int tk = t0 + 16 * (col >> 2), tv = t0 + 16 * g;
+    return Entries{table[(tk < kmax ? tk : kmax - 1) >> bs_shift], table[(tv < kmax ? tv : kmax - 1) >> bs_shift]};
   };
   uint4v kw[4][KI], vw[VT];
   uint32_t ksb = 0, vsb = 0;
+  bool there = false;  // whether the block of this lane's tokens is in the cache
   // loads of a tile; a block that is not there is read from block 0 and masked
-  auto load_k = [&](int t0, int64_t blk) {
+  auto load_k = [&](int t0, const Entries& e) {
     const int t = t0 + 16 * (col >> 2);
-    const uint8_t* p = kbase + (blk < 0 ? 0 : blk) * page_bytes + (int64_t)(t & (bs - 1)) * D;
+    const uint32_t blk = (uint32_t)e.k < (uint32_t)c.num_blocks ? (uint32_t)e.k : 0u;
+    const uint8_t* p = kbase + blk * page_bytes + (uint32_t)((t & (bs - 1)) * D);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < KI; ++j) kw[i][j] = *reinterpret_cast<const uint4v*>(p + i * 4 * D + j * 64);
   };
-  auto load_v = [&](int t0, int64_t blk) {
+  auto load_v = [&](int t0, const Entries& e) {
     const int t = t0 + 16 * g;
-    const int64_t bk = blk < 0 ? 0 : blk;
-    const uint8_t* p = vbase + bk * page_bytes + (int64_t)(t & (bs - 1)) * D;
+    there = (uint32_t)e.v < (uint32_t)c.num_blocks;
+    const uint32_t blk = there ? (uint32_t)e.v : 0u, at = blk * (uint32_t)H + (uint32_t)h;
+    ksb = c.k_scale[at];
+    vsb = c.v_scale[at];
+    const uint8_t* p = vbase + blk * page_bytes + (uint32_t)((t & (bs - 1)) * D);
 #pragma unroll
     for (int i = 0; i < VT; ++i) vw[i] = *reinterpret_cast<const uint4v*>(p + i * 256);
   };
-  auto load_scales = [&](int64_t blk) {
-    const int64_t at = (blk < 0 ? 0 : blk) * H + h;
-    ksb = c.k_scale[at];
-    vsb = blk < 0 ? 0u : c.v_scale[at];  // its weights are zero, and stay so under a finite scale
-  };
 
   int t0 = k0 + 64 * wave;
-  int64_t blk = -1, blk_k = -1;
+  Entries next = {0, 0}, after = {0, 0};
   if (t0 < k1) {
-    blk = block_of(t0 + 16 * g);
-    blk_k = block_of(t0 + 16 * (col >> 2));
-    load_k(t0, blk_k);
-    load_scales(blk);
-    load_v(t0, blk);
+    next = look_up(t0);
+    after = look_up(t0 + STEP);
+    load_k(t0, next);
+    load_v(t0, next);
   }
   for (; t0 < k1; t0 += STEP) {
-    const int64_t blk_next = block_of(t0 + STEP + 16 * g), blk_k_next = block_of(t0 + STEP + 16 * (col >> 2));
     const bool more = t0 + STEP < k1;
     float x[NC][16];
 #pragma unroll
@@ -471,15 +474,20 @@ __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kern
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[t][4 * i + r] = acc[t][r];
     }
-    const float ks = e8m0(ksb) * sl2, vs = e8m0(vsb);
-    if (more) load_k(t0 + STEP, blk_k_next);
+    const bool in = there;
+    const float ks = e8m0(ksb) * sl2, vs = in ? e8m0(vsb) : 0.0f;
+    next = after;
+    if (more) {
+      after = look_up(t0 + 2 * STEP);
+      load_k(t0 + STEP, next);
+    }
     const int tg = t0 + 16 * g;  // this lane's 16 tokens start here
     // Masked in edge tiles only: keys hidden from some row, past this range
     // (the ranges meet at multiples of 64, so only past kmax) or of a block
     // that is not there.
-    const bool edge = t0 < last.lo || t0 + 64 > first.hi || t0 + 64 > k1 || __any(blk < 0);
+    const bool edge = t0 < last.lo || t0 + 64 > first.hi || t0 + 64 > k1 || __any(!in);
     if (edge) {
-      const int have = blk < 0 ? 0 : clamp16(k1 - tg), skip = clamp16(first.lo - tg);
+      const int have = in ? clamp16(k1 - tg) : 0, skip = clamp16(first.lo - tg);
 #pragma unroll
       for (int t = 0; t < NC; ++t) {
         const int lo = clamp16(vlo[t] - tg), hi = clamp16(vhi[t] - tg);
@@ -536,11 +544,7 @@ __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kern
         o[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, p[t][1], o[t][i], 0, 0, 0);
       }
     }
-    blk = blk_next;
-    if (more) {
-      load_scales(blk);
-      load_v(t0 + STEP, blk);
-    }
+    if (more) load_v(t0 + STEP, next);
   }
 
   // join the waves
@@ -932,10 +936,32 @@ AttnPlan plan_attention(int B, int Hq, int Hkv, int D, int64_t max_new, int64_t 
   // 64 below its first visible key
   int64_t span = max_len < 1 ? 1 : max_len;
   if (window > 0) span = std::min<int64_t>(span, (int64_t)window + max_new - 1 + 63);
-  // ranges of keys: about 2048 workgroups, of at least 256 keys each (many
-  // rows: 1024)
-  int64_t splits = std::max<int64_t>(1, std::min<int64_t>((2048 + tiles - 1) / tiles, (span + 255) / 256));
-  if (p.kind == 1) splits = std::max<int64_t>(1, std::min<int64_t>(2048 / tiles, span / 1024));
+  // Ranges of keys. Every workgroup pays its start (about as long as one step
+  // of 64 tokens a wave) and a call with several ranges their joining, so the
+  // ranges are as few as fill the card: the count with the least rounds *
+  // (steps + 1) + joining, a round being the workgroups that run at once
+  // (MI355X sweep over 1 .. 512 ranges: one sequence of 131072 tokens and 8 kv
+  // heads 57 us with 32 ranges, 77 with 16, 63 with 64; eight of up to 4096
+  // tokens 18.5 us with 4, 22 with 2, 23 with 8).
+  int64_t splits = 1;
+  if (p.kind == 0) {
+    const int waves = stream_waves(D, p.cols);
+    const int64_t slots = D == 64 && p.cols == 1 ? 512 : 256;
+    double best = 0.0;
+    for (int64_t s = 1; s <= 64; ++s) {
+      const int64_t steps = (span + s * 64 * waves - 1) / (s * 64 * waves);
+      const double cost = (double)((tiles * s + slots - 1) / slots) * (double)(steps + 1) +
+                          (s > 1 ? 0.75 + (double)s * (double)std::min<int64_t>(rows, rows_of(p)) / 512.0 : 0.0);
+      if (s == 1 || cost < best) {
+        best = cost;
+        splits = s;
+      }
+    }
+  } else {
+    // many rows: two rounds of workgroups (sequences differ in length), of at
+    // least 2048 keys (2 x 512 tokens on 32768: 1.15 ms whole, 1.11 in two)
+    splits = std::max<int64_t>(1, std::min<int64_t>((1024 + tiles - 1) / tiles, span / 2048));
+  }
   // one arrival counter a tile, below the words a linear call keeps its device scalars in
   if (tiles > kWorkspaceScalarOffset / 4) splits = 1;
   int64_t chunk = round_up((span + splits - 1) / splits, 64);
