@@ -103,22 +103,6 @@ FMT_FP8_BLOCK = 5
 _c_int, _c_i64, _c_f32, _c_vp, _c_sz = (ctypes.c_int, ctypes.c_int64, ctypes.c_float,
                                          ctypes.c_void_p, ctypes.c_size_t)
 
-class KvCacheStruct(ctypes.Structure):
-    """fql_kv_cache."""
-    _fields_ = [("k", _c_vp), ("v", _c_vp), ("k_scale", _c_vp), ("v_scale", _c_vp),
-                ("num_blocks", _c_i64), ("kv_heads", ctypes.c_int32), ("block_size", ctypes.c_int32),
-                ("head_dim", ctypes.c_int32)]
-
-
-class KvBatchStruct(ctypes.Structure):
-    """fql_kv_batch."""
-    _fields_ = [("block_table", _c_vp), ("ld_table", _c_i64), ("lens", _c_vp), ("cu_seqlens", _c_vp),
-                ("tokens", _c_i64), ("table_cols", ctypes.c_int32), ("batch", ctypes.c_int32),
-                ("max_new", ctypes.c_int32)]
-
-
-_c_cache, _c_batch = ctypes.POINTER(KvCacheStruct), ctypes.POINTER(KvBatchStruct)
-
 # name -> (restype, argtypes); must match include/fql.h
 SIGNATURES = {
     "fql_version": (_c_int, []),
@@ -206,13 +190,13 @@ SIGNATURES = {
     "fql_linear_fused": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_f32, _c_vp, _c_vp,
                                   _c_i64, _c_f32, _c_vp, _c_vp, _c_int, _c_vp, _c_i64, _c_vp,
                                   _c_i64, _c_vp, _c_sz, _c_vp]),
-    "fql_kv_append": (_c_int, [_c_cache, _c_batch, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64,
+    "fql_kv_append": (_c_int, [_c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64,
                                _c_vp]),
     "fql_attention_kv8_workspace_bytes": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_i64, _c_i64,
                                                    _c_int, ctypes.POINTER(_c_sz)]),
     "fql_attention_kv8_describe": (_c_int, [_c_int, _c_int, _c_int, _c_int, _c_i64, _c_i64, _c_int,
                                             ctypes.c_char_p, _c_sz]),
-    "fql_attention_kv8": (_c_int, [_c_cache, _c_batch, _c_vp, _c_i64, _c_i64, _c_int, _c_f32,
+    "fql_attention_kv8": (_c_int, [_c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_f32,
                                    _c_int, _c_int, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp,
                                    _c_sz, _c_vp]),
 }

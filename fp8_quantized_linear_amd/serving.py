@@ -20,15 +20,34 @@ One layer of a decoder, all tensors on the GPU:
 """
 
 import ctypes
+import functools
+import struct
 
 import torch
 
-from . import (FMT_FP8, FMT_FP8_BLOCK, FMT_MXFP4, FMT_MXFP8, FQLError, KvBatchStruct, KvCacheStruct,
-               _check, _ptr, _require_cuda, _rows_view, _size_query, _stream, _workspace, lib,
-               linear_sc_workspace_bytes)
+from . import (FMT_FP8, FMT_FP8_BLOCK, FMT_MXFP4, FMT_MXFP8, FQLError, _check, _rows_view, _size_query, _workspaces,
+               lib, linear_sc_workspace_bytes, new_workspace)
 
 FORMATS = {"mxfp4": FMT_MXFP4, "mxfp8": FMT_MXFP8, "fp8": FMT_FP8, "fp8_block": FMT_FP8_BLOCK}
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
+
+# A decode step's calls take a few microseconds on the GPU, so what Python does
+# around them counts: addresses go to the library as plain integers, the
+# structs of include/fql.h as packed bytes, sizes that depend on shapes alone
+# are remembered.
+_stream = torch._C._cuda_getCurrentRawStream  # device index -> hipStream_t of torch's current stream
+_bf16, _u8, _i32 = torch.bfloat16, torch.uint8, torch.int32
+_linear_workspace_bytes = functools.lru_cache(4096)(linear_sc_workspace_bytes)
+_query = functools.lru_cache(4096)(_size_query)
+
+
+def _workspace(device, nbytes):
+    """The binding's workspace of this device and stream (shared with the linear calls)."""
+    key = (device.type, device.index, _stream(device.index))
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspaces[key] = new_workspace(nbytes, device)
+    return ws
 
 
 def _format(fmt):
@@ -37,11 +56,25 @@ def _format(fmt):
     return FORMATS[fmt]
 
 
-def _bf16_rows(t, name, shape):
-    _require_cuda(t, name)
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape):
-        raise FQLError(f"{name} must be a bfloat16 tensor of shape {tuple(shape)}")
-    return _rows_view(t, name)
+def _cuda(t, name, dtype):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise FQLError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype is not dtype:
+        raise FQLError(f"{name} must be {dtype}")
+
+
+def _rows(t, name, shape=None):
+    """(address, rows, columns, row stride) of a bf16 [..., K] tensor, of the given shape if any."""
+    _cuda(t, name, _bf16)
+    if shape is not None and t.shape != shape:
+        raise FQLError(f"{name} must have shape {tuple(shape)}")
+    if t.dim() == 2:
+        M, K = t.shape
+        ld, unit = t.stride()
+        if unit == 1:
+            return t.data_ptr(), M, K, ld if M > 1 or ld > K else K
+    t2, ld = _rows_view(t, name)
+    return t2.data_ptr(), t2.shape[0], t2.shape[1], ld
 
 
 def _scale_arg(fmt, scale):
@@ -52,10 +85,11 @@ def _scale_arg(fmt, scale):
     return ctypes.c_float(float(scale)).value
 
 
-def _bf16_vector(t, name, n):
-    _require_cuda(t, name)
-    if t.dtype != torch.bfloat16 or t.numel() != n or not t.is_contiguous():
+def _vector(t, name, n):
+    _cuda(t, name, _bf16)
+    if t.numel() != n or not t.is_contiguous():
         raise FQLError(f"{name} must be a contiguous bf16 tensor of {n} elements")
+    return t.data_ptr()
 
 
 # ---------------------------------------------------------------------------
@@ -80,27 +114,25 @@ class QuantizedActivation:
 
 def _new_operand(x, fmt, scale):
     K = x.shape[-1]
-    lead = tuple(x.shape[:-1])
-    q = QuantizedActivation(None, fmt, lead, K, scale if fmt == "fp8" else None)
-    nbytes = _size_query("fql_operand_bytes", _format(fmt), q.M, K)
-    q.data = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    q = QuantizedActivation(None, fmt, x.shape[:-1], K, scale if fmt == "fp8" else None)
+    q.data = torch.empty(_query("fql_operand_bytes", _format(fmt), q.M, K), dtype=_u8, device=x.device)
     return q
 
 
 def _norm_args(x, weight, residual, residual_out):
-    _require_cuda(x, "x")
-    if x.dtype != torch.bfloat16:
-        raise FQLError("x must be bfloat16")
-    x2, ld = _rows_view(x, "x")
-    _bf16_vector(weight, "weight", x.shape[-1])
-    r2, ldr, h, h2, ldh = None, 0, None, None, 0
-    if residual is not None:
-        r2, ldr = _bf16_rows(residual, "residual", x.shape)
-        h = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device) if residual_out is None else residual_out
-        h2, ldh = _bf16_rows(h, "residual_out", x.shape)
-    elif residual_out is not None:
-        raise FQLError("residual_out needs a residual")
-    return x2, ld, r2, ldr, h, h2, ldh
+    """(address, M, K, ld of x, of the residual: address, ld, weight's address, h, its address and ld)."""
+    xp, M, K, ld = _rows(x, "x")
+    wp = _vector(weight, "weight", K)
+    if residual is None:
+        if residual_out is not None:
+            raise FQLError("residual_out needs a residual")
+        return xp, M, K, ld, 0, 0, wp, None, 0, 0
+    rp, _, _, ldr = _rows(residual, "residual", x.shape)
+    if residual_out is None:
+        h = torch.empty(x.shape, dtype=_bf16, device=x.device)
+        return xp, M, K, ld, rp, ldr, wp, h, h.data_ptr(), K
+    hp, _, _, ldh = _rows(residual_out, "residual_out", x.shape)
+    return xp, M, K, ld, rp, ldr, wp, residual_out, hp, ldh
 
 
 def rms_norm_quant(x, weight, fmt, eps=1e-6, residual=None, scale=None, residual_out=None):
@@ -109,18 +141,18 @@ def rms_norm_quant(x, weight, fmt, eps=1e-6, residual=None, scale=None, residual
     Returns (codes uint8 [..., K], scales as quant_<fmt> gives them or None, h bf16 or None without a
     residual). residual_out may be x or residual itself."""
     f = _format(fmt)
-    x2, ld, r2, ldr, h, h2, ldh = _norm_args(x, weight, residual, residual_out)
-    M, K = x2.shape
-    lead = tuple(x.shape[:-1])
-    codes = torch.empty(lead + (K,), dtype=torch.uint8, device=x.device)
-    scales = None
+    xp, M, K, ld, rp, ldr, wp, h, hp, ldh = _norm_args(x, weight, residual, residual_out)
+    dev = x.device
+    codes = torch.empty(x.shape, dtype=_u8, device=dev)
+    scales, sp = None, 0
     if fmt == "mxfp8":
-        scales = torch.empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
+        scales = torch.empty(x.shape[:-1] + (K // 32,), dtype=_u8, device=dev)
     elif fmt == "fp8_block":
-        scales = torch.empty(lead + (K // 128,), dtype=torch.float32, device=x.device)
-    _check(lib().fql_rms_norm_quant(f, _ptr(x2), M, K, ld, _ptr(r2), ldr, _ptr(weight), float(eps),
-                                    _scale_arg(fmt, scale), _ptr(codes), _ptr(scales), _ptr(h2), ldh,
-                                    _stream(x.device)))
+        scales = torch.empty(x.shape[:-1] + (K // 128,), dtype=torch.float32, device=dev)
+    if scales is not None:
+        sp = scales.data_ptr()
+    _check(lib().fql_rms_norm_quant(f, xp, M, K, ld, rp, ldr, wp, eps, _scale_arg(fmt, scale), codes.data_ptr(), sp,
+                                    hp, ldh, _stream(dev.index)))
     return codes, scales, h
 
 
@@ -128,26 +160,21 @@ def rms_norm_operand(x, weight, fmt, eps=1e-6, residual=None, scale=None, residu
     """rms_norm_quant with the quantized activation as a QuantizedActivation for linear_fused;
     returns (activation, h or None)."""
     f = _format(fmt)
-    x2, ld, r2, ldr, h, h2, ldh = _norm_args(x, weight, residual, residual_out)
-    M, K = x2.shape
+    xp, M, K, ld, rp, ldr, wp, h, hp, ldh = _norm_args(x, weight, residual, residual_out)
     s = _scale_arg(fmt, scale)
     q = _new_operand(x, fmt, s)
-    _check(lib().fql_rms_norm_operand(f, _ptr(x2), M, K, ld, _ptr(r2), ldr, _ptr(weight), float(eps), s,
-                                      _ptr(q.data), q.data.numel(), _ptr(h2), ldh, _stream(x.device)))
+    _check(lib().fql_rms_norm_operand(f, xp, M, K, ld, rp, ldr, wp, eps, s, q.data.data_ptr(), q.data.numel(), hp, ldh,
+                                      _stream(x.device.index)))
     return q, h
 
 
 def quant_operand(x, fmt, scale=None):
     """bf16 x [..., K] quantized once for several linear_fused calls (also "mxfp4")."""
     f = _format(fmt)
-    _require_cuda(x, "x")
-    if x.dtype != torch.bfloat16:
-        raise FQLError("x must be bfloat16")
-    x2, ld = _rows_view(x, "x")
-    M, K = x2.shape
+    xp, M, K, ld = _rows(x, "x")
     s = _scale_arg(fmt, scale)
     q = _new_operand(x, fmt, s)
-    _check(lib().fql_quant_operand(f, _ptr(x2), M, K, ld, s, _ptr(q.data), q.data.numel(), _stream(x.device)))
+    _check(lib().fql_quant_operand(f, xp, M, K, ld, s, q.data.data_ptr(), q.data.numel(), _stream(x.device.index)))
     return q
 
 
@@ -178,38 +205,36 @@ def linear_fused(x, weight, activation=None, bias=None, residual=None, alpha=Non
     if fmt not in FORMATS:
         raise FQLError("linear_fused takes MXFP4, MXFP8, FP8 and block FP8 weights")
     N, K = weight.N, weight.K
-    quantized = isinstance(x, QuantizedActivation)
-    if quantized:
+    xp = op = ld = 0
+    if isinstance(x, QuantizedActivation):
         if x.fmt != fmt:
             raise FQLError(f"the activation is {x.fmt}, the weight {fmt}")
         if fmt == "fp8" and x.scale != weight.input_scale:
             raise FQLError("the activation was quantized with another scale than the weight's input_scale")
-        if x.K != K:
-            raise FQLError(f"x has K={x.K}, weight has K={K}")
-        lead, M, ld, x2, op, dev = x.lead, x.M, 0, None, x.data, x.data.device
+        lead, M, xK, op, dev = x.lead, x.M, x.K, x.data.data_ptr(), x.data.device
     else:
-        _require_cuda(x, "x")
-        if x.dtype != torch.bfloat16:
-            raise FQLError("linear_fused takes bfloat16 activations or a QuantizedActivation")
-        if x.shape[-1] != K:
-            raise FQLError(f"x has K={x.shape[-1]}, weight has K={K}")
-        lead, dev, op = tuple(x.shape[:-1]), x.device, None
-        x2, ld = _rows_view(x, "x")
-        M = x2.shape[0]
-    if bias is not None:
-        _bf16_vector(bias, "bias", N)
-    shape = lead + (N // 2 if activation == "swiglu" else N,)
+        xp, M, xK, ld = _rows(x, "x")
+        lead, dev = x.shape[:-1], x.device
+    if xK != K:
+        raise FQLError(f"x has K={xK}, weight has K={K}")
+    bp = 0 if bias is None else _vector(bias, "bias", N)
+    No = N // 2 if activation == "swiglu" else N
+    shape = lead + (No,)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-    y2, ldy = _bf16_rows(out, "out", shape)
-    r2, ldr = (None, 0) if residual is None else _bf16_rows(residual, "residual", shape)
+        out = torch.empty(shape, dtype=_bf16, device=dev)
+        yp, ldy = out.data_ptr(), No
+    else:
+        yp, _, _, ldy = _rows(out, "out", shape)
+    rp = ldr = 0
+    if residual is not None:
+        rp, _, _, ldr = _rows(residual, "residual", shape)
     if workspace is None:
-        workspace = _workspace(dev, linear_sc_workspace_bytes(fmt, M, N, K))
-    alpha_dev = weight.alpha_dev if fmt == "fp8" and alpha is None else None
-    _check(lib().fql_linear_fused(FORMATS[fmt], _ptr(x2), M, K, ld, getattr(weight, "input_scale", 0), _ptr(op),
-                                  _ptr(weight.packed), N, 1.0 if alpha is None else float(alpha), _ptr(alpha_dev),
-                                  _ptr(bias), ACTIVATIONS[activation], _ptr(r2), ldr, _ptr(y2), ldy,
-                                  _ptr(workspace), workspace.numel(), _stream(dev)))
+        workspace = _workspace(dev, _linear_workspace_bytes(fmt, M, N, K))
+    scale = weight.input_scale if fmt == "fp8" else 0
+    ap = weight.alpha_dev.data_ptr() if fmt == "fp8" and alpha is None else 0
+    _check(lib().fql_linear_fused(FORMATS[fmt], xp, M, K, ld, scale, op, weight.packed.data_ptr(), N,
+                                  1.0 if alpha is None else alpha, ap, bp, ACTIVATIONS[activation], rp, ldr, yp, ldy,
+                                  workspace.data_ptr(), workspace.numel(), _stream(dev.index)))
     return out
 
 
@@ -227,9 +252,9 @@ class KVCache8:
 
     def __init__(self, k, v, k_scale, v_scale):
         for t, name in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
-            _require_cuda(t, name)
-            if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != k.device:
-                raise FQLError(f"{name} must be a contiguous uint8 tensor on the cache's device")
+            _cuda(t, name, _u8)
+            if not t.is_contiguous() or t.device != k.device:
+                raise FQLError(f"{name} must be contiguous and on the cache's device")
         if k.dim() != 4 or k.shape[2] % 16 != 0:
             raise FQLError("k must be [blocks, kv_heads, block_size, head_dim], block_size a multiple of 16")
         self.num_blocks, self.kv_heads, self.block_size, self.head_dim = k.shape
@@ -238,8 +263,8 @@ class KVCache8:
         if not tuple(k_scale.shape) == tuple(v_scale.shape) == (self.num_blocks, self.kv_heads):
             raise FQLError("scales must be [blocks, kv_heads]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self._struct = KvCacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                     self.num_blocks, self.kv_heads, self.block_size, self.head_dim)
+        self._struct = struct.pack("PPPPqiii4x", k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                   self.num_blocks, self.kv_heads, self.block_size, self.head_dim)  # fql_kv_cache
 
     @classmethod
     def empty(cls, num_blocks, kv_heads, block_size, head_dim, device="cuda"):
@@ -250,32 +275,39 @@ class KVCache8:
         return cls(k, v, s[0], s[1])
 
 
-def _heads(t, name, tokens, heads, head_dim):
-    """(tensor, token stride, head stride) of a bf16 [tokens, heads, head_dim] tensor."""
-    _require_cuda(t, name)
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
-        raise FQLError(f"{name} must be a bfloat16 tensor [tokens, {heads}, {head_dim}]")
-    if tokens is not None and t.shape[0] != tokens:
-        raise FQLError(f"{name} must have {tokens} tokens")
-    if t.stride(2) != 1:
+def _heads(t, name, shape):
+    """(address, token stride, head stride) of a bf16 [tokens, heads, head_dim] tensor."""
+    _cuda(t, name, _bf16)
+    if t.shape != shape:
+        raise FQLError(f"{name} must have shape {shape}")
+    ld_token, ld_head, unit = t.stride()
+    if unit != 1:
         raise FQLError(f"{name} must have unit stride in its last dimension")
-    return t, t.stride(0), t.stride(1)
+    return t.data_ptr(), ld_token, ld_head
 
 
 def _batch(cache, block_table, lens, cu_seqlens, max_new, tokens):
+    """A packed fql_kv_batch, the batch size and its bound of new tokens."""
+    dev = cache.k.device
     for t, name in ((block_table, "block_table"), (lens, "lens"), (cu_seqlens, "cu_seqlens")):
-        _require_cuda(t, name)
-        if t.dtype != torch.int32 or t.device != cache.k.device:
-            raise FQLError(f"{name} must be an int32 tensor on the cache's device")
-    B = lens.shape[0] if lens.dim() == 1 else -1
-    if B < 1 or tuple(cu_seqlens.shape) != (B + 1,) or block_table.dim() != 2 or block_table.shape[0] != B:
+        _cuda(t, name, _i32)
+        if t.device != dev:
+            raise FQLError(f"{name} must be on the cache's device")
+    if lens.dim() != 1 or cu_seqlens.dim() != 1 or block_table.dim() != 2:
         raise FQLError("block_table must be [batch, columns], lens [batch], cu_seqlens [batch + 1]")
-    if block_table.stride(1) != 1 or not lens.is_contiguous() or not cu_seqlens.is_contiguous():
+    B = lens.shape[0]
+    rows, cols = block_table.shape
+    if B < 1 or rows != B or cu_seqlens.shape[0] != B + 1:
+        raise FQLError("block_table must be [batch, columns], lens [batch], cu_seqlens [batch + 1]")
+    ld, unit = block_table.stride()
+    if (unit != 1 and cols > 1) or not lens.is_contiguous() or not cu_seqlens.is_contiguous():
         raise FQLError("block_table's rows, lens and cu_seqlens must be contiguous")
-    cols = block_table.shape[1]
-    ld = block_table.stride(0) if B > 1 else max(cols, block_table.stride(0))
-    return KvBatchStruct(block_table.data_ptr(), ld, lens.data_ptr(), cu_seqlens.data_ptr(), tokens, cols, B,
-                         min(int(max_new), tokens))
+    new = int(max_new)
+    if new < 0:
+        raise FQLError("max_new must be >= 0")
+    new = new if new < tokens else tokens
+    return struct.pack("PqPPqiii4x", block_table.data_ptr(), ld if B > 1 and ld > cols else cols, lens.data_ptr(),
+                       cu_seqlens.data_ptr(), tokens, cols, B, new), B, cols, new
 
 
 def kv_append(cache, k, v, block_table, lens, cu_seqlens, max_new):
@@ -283,13 +315,15 @@ def kv_append(cache, k, v, block_table, lens, cu_seqlens, max_new):
     the cache. block_table int32 [B, columns], lens int32 [B] (tokens of each sequence with the new
     ones), cu_seqlens int32 [B + 1] (first row of each sequence's new tokens), max_new: an upper bound
     of a sequence's new tokens. Nothing is read back to the host."""
-    k, kt, kh = _heads(k, "k", None, cache.kv_heads, cache.head_dim)
-    v, vt, vh = _heads(v, "v", k.shape[0], cache.kv_heads, cache.head_dim)
-    b = _batch(cache, block_table, lens, cu_seqlens, max_new, k.shape[0])
-    if k.shape[0] == 0:
-        return
-    _check(lib().fql_kv_append(ctypes.byref(cache._struct), ctypes.byref(b), _ptr(k), kt, kh, _ptr(v), vt, vh,
-                               _stream(cache.k.device)))
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise FQLError("k must be a tensor [tokens, kv_heads, head_dim]")
+    T = k.shape[0]
+    shape = (T, cache.kv_heads, cache.head_dim)
+    kp, kt, kh = _heads(k, "k", shape)
+    vp, vt, vh = _heads(v, "v", shape)
+    b, _, _, _ = _batch(cache, block_table, lens, cu_seqlens, max_new, T)
+    if T > 0:
+        _check(lib().fql_kv_append(cache._struct, b, kp, kt, kh, vp, vt, vh, _stream(k.device.index)))
 
 
 def attention_kv8_plan(batch, q_heads, kv_heads, head_dim, max_new, max_len, window=0):
@@ -308,22 +342,28 @@ def attention_kv8(q, cache, block_table, lens, cu_seqlens, max_new, causal=True,
     is known on the host (the launch is planned by it). Returns out [tokens, q_heads, head_dim] bf16, or
     (out, lse float32 [tokens, q_heads]). Rows outside cu_seqlens' ranges are not written."""
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise FQLError("q must be [tokens, q_heads, head_dim]")
-    T, Hq = q.shape[0], q.shape[1]
-    q, qt, qh = _heads(q, "q", None, Hq, cache.head_dim)
+        raise FQLError("q must be a tensor [tokens, q_heads, head_dim]")
+    T, Hq, _ = q.shape
+    D, dev = cache.head_dim, q.device
+    shape = (T, Hq, D)
+    qp, qt, qh = _heads(q, "q", shape)
     if out is None:
-        out = torch.empty((T, Hq, cache.head_dim), dtype=torch.bfloat16, device=q.device)
-    out, ot, oh = _heads(out, "out", T, Hq, cache.head_dim)
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-    b = _batch(cache, block_table, lens, cu_seqlens, max_new, T)
+        out = torch.empty(shape, dtype=_bf16, device=dev)
+        op, ot, oh = out.data_ptr(), Hq * D, D
+    else:
+        op, ot, oh = _heads(out, "out", shape)
+    lse, lp = None, 0
+    if return_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lp = lse.data_ptr()
+    b, B, cols, new = _batch(cache, block_table, lens, cu_seqlens, max_new, T)
     if T > 0:
         if max_len is None:
-            max_len = b.table_cols * cache.block_size
+            max_len = cols * cache.block_size
         if workspace is None:
-            workspace = _workspace(q.device, _size_query("fql_attention_kv8_workspace_bytes", b.batch, Hq,
-                                                         cache.kv_heads, cache.head_dim, b.max_new, max_len, window))
-        s = cache.head_dim ** -0.5 if scale is None else float(scale)
-        _check(lib().fql_attention_kv8(ctypes.byref(cache._struct), ctypes.byref(b), _ptr(q), qt, qh, Hq, s,
-                                       int(bool(causal)), int(window), int(max_len), _ptr(out), ot, oh, _ptr(lse),
-                                       _ptr(workspace), workspace.numel(), _stream(q.device)))
+            workspace = _workspace(dev, _query("fql_attention_kv8_workspace_bytes", B, Hq, cache.kv_heads, D, new,
+                                               max_len, window))
+        _check(lib().fql_attention_kv8(cache._struct, b, qp, qt, qh, Hq, D ** -0.5 if scale is None else scale,
+                                       bool(causal), window, max_len, op, ot, oh, lp, workspace.data_ptr(),
+                                       workspace.numel(), _stream(dev.index)))
     return (out, lse) if return_lse else out

@@ -89,20 +89,36 @@ def test_linear_refusals():
     refused(linear(size=16), "workspace", code=-4)
 
 
+class CacheStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [("num_blocks", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("kv_heads", "block_size", "head_dim")]
+
+
+class BatchStruct(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("ld_table", ctypes.c_int64), ("lens", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("table_cols", ctypes.c_int32),
+                ("batch", ctypes.c_int32), ("max_new", ctypes.c_int32)]
+
+
 def cache(**kw):
     d = dict(k=1 << 20, v=1 << 20, k_scale=1 << 20, v_scale=1 << 20, num_blocks=8, kv_heads=2, block_size=16, head_dim=64)
     d.update(kw)
-    from fp8_quantized_linear_amd import KvCacheStruct
-
-    return KvCacheStruct(**d)
+    return CacheStruct(**d)
 
 
 def batch(**kw):
     d = dict(block_table=1 << 20, ld_table=4, lens=1 << 20, cu_seqlens=1 << 20, tokens=3, table_cols=4, batch=2, max_new=2)
     d.update(kw)
-    from fp8_quantized_linear_amd import KvBatchStruct
+    return BatchStruct(**d)
 
-    return KvBatchStruct(**d)
+
+def test_binding_packs_the_structs_as_the_header_lays_them_out():
+    import struct
+
+    c = struct.pack("PPPPqiii4x", 1, 2, 3, 4, 5, 6, 7, 8)
+    assert c[:ctypes.sizeof(CacheStruct)] == bytes(CacheStruct(1, 2, 3, 4, 5, 6, 7, 8)) and len(c) == ctypes.sizeof(CacheStruct)
+    b = struct.pack("PqPPqiii4x", 1, 2, 3, 4, 5, 6, 7, 8)
+    assert b == bytes(BatchStruct(1, 2, 3, 4, 5, 6, 7, 8))
 
 
 def append(c=None, b=None, k=P, v=P, st=128):
