@@ -84,6 +84,7 @@ __all__ = [
     "rms_norm_operand",
     "quant_operand",
     "linear_fused",
+    "linear_fused_plan",
     "interleave_gate_up",
     "KVCache8",
     "kv_append",
@@ -187,6 +188,8 @@ SIGNATURES = {
                                       _c_f32, _c_f32, _c_vp, _c_sz, _c_vp, _c_i64, _c_vp]),
     "fql_quant_operand": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_f32, _c_vp, _c_sz,
                                    _c_vp]),
+    "fql_linear_fused_workspace_bytes": (_c_int, [_c_int, _c_i64, _c_i64, _c_i64, ctypes.POINTER(_c_sz)]),
+    "fql_linear_fused_describe": (_c_int, [_c_int, _c_i64, _c_i64, _c_i64, ctypes.c_char_p, _c_sz]),
     "fql_linear_fused": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_f32, _c_vp, _c_vp,
                                   _c_i64, _c_f32, _c_vp, _c_vp, _c_int, _c_vp, _c_i64, _c_vp,
                                   _c_i64, _c_vp, _c_sz, _c_vp]),
@@ -1014,5 +1017,5 @@ def warmup(layers, token_counts, device=None):
 
 
 from .serving import (KVCache8, QuantizedActivation, attention_kv8, attention_kv8_plan,  # noqa: E402
-                      interleave_gate_up, kv_append, linear_fused, quant_operand, rms_norm_operand,
-                      rms_norm_quant)
+                      interleave_gate_up, kv_append, linear_fused, linear_fused_plan, quant_operand,
+                      rms_norm_operand, rms_norm_quant)

@@ -93,6 +93,11 @@ ScPlan cached_plan_sc_gemm(int fmt, int64_t M, int64_t N, int64_t K) {
   return cache.get(M, N, K, fmt, [&] { return plan_sc_gemm(fmt, M, N, K); });
 }
 
+ScPlan cached_plan_sc_fused(int fmt, int64_t M, int64_t N, int64_t K) {
+  thread_local PlanCache<ScPlan> cache;
+  return cache.get(M, N, K, fmt, [&] { return plan_sc_fused(fmt, M, N, K); });
+}
+
 }  // namespace fql
 
 namespace {
@@ -1161,6 +1166,29 @@ int fql_quant_operand(int format, const void* x, int64_t M, int64_t K, int64_t l
   });
 }
 
+int fql_linear_fused_workspace_bytes(int format, int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  return guarded([&] {
+    const int fmt = sc_format(format, true);
+    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no fused epilogue (MXFP4, MXFP8, FP8, block FP8 have)", format);
+    if (!bytes) return fail(FQL_ERR_INVALID, "null pointer");
+    if (int r = check_sc_shape(fmt, M, K, K, "M", false)) return r;
+    if (int r = check_sc_shape(fmt, N, K, K, "N", true)) return r;
+    *bytes = (size_t)fql::cached_plan_sc_fused(fmt, M, N, K).total_bytes;
+    return ok();
+  });
+}
+
+int fql_linear_fused_describe(int format, int64_t M, int64_t N, int64_t K, char* buf, size_t buf_len) {
+  return guarded([&] {
+    const int fmt = sc_format(format, true);
+    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no fused epilogue (MXFP4, MXFP8, FP8, block FP8 have)", format);
+    if (int r = check_sc_shape(fmt, M, K, K, "M", false)) return r;
+    if (int r = check_sc_shape(fmt, N, K, K, "N", true)) return r;
+    write_reason(buf, buf_len, fql::describe_sc_plan(fql::plan_sc_fused(fmt, M, N, K)));
+    return ok();
+  });
+}
+
 int fql_linear_fused(int format, const void* x, int64_t M, int64_t K, int64_t ldx, float input_scale,
                      const void* x_operand, const void* w_packed, int64_t N, float alpha, const float* alpha_dev,
                      const void* bias, int activation, const void* residual, int64_t ldr, void* y, int64_t ldy,
@@ -1187,7 +1215,7 @@ int fql_linear_fused(int format, const void* x, int64_t M, int64_t K, int64_t ld
     if (x) {
       if (int r = inverse_scale(fmt, input_scale, "input_scale", &inv)) return r;
     }
-    const fql::ScPlan plan = fql::cached_plan_sc_gemm(fmt, M, N, K);
+    const fql::ScPlan plan = fql::cached_plan_sc_fused(fmt, M, N, K);
     if (workspace_bytes < (size_t)plan.total_bytes)
       return fail(FQL_ERR_WORKSPACE, "workspace holds %zu bytes, %lld needed", workspace_bytes, (long long)plan.total_bytes);
     if (plan.splits > 1 && plan.groups > plan.counter_bytes / 4)

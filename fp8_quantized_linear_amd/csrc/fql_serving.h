@@ -45,7 +45,9 @@ struct ScEpilogue {
   const uint16_t* residual;  // bf16 [M][ldr] or null; may be y itself
   int64_t ldr;
 };
-// launch_sc_linear with the epilogue above. x is used when x_operand is null;
+ScPlan plan_sc_fused(int fmt, int64_t M, int64_t N, int64_t K);
+ScPlan cached_plan_sc_fused(int fmt, int64_t M, int64_t N, int64_t K);
+// launch_sc_linear with the epilogue above, on a plan of plan_sc_fused. x is used when x_operand is null;
 // x_operand is an operand of operand_dims(p.fmt, M, K).
 hipError_t launch_sc_linear_fused(const ScPlan& p, const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
                                   bool aligned, float inv_scale, const uint8_t* x_operand,

@@ -803,6 +803,12 @@ __global__ __launch_bounds__(64 * W) void gemv_sc_kernel(
   FQL_SC_CONFIGS_FP4(X, SC_MXFP4) FQL_SC_CONFIGS_ANY(X, SC_MXFP8) FQL_SC_CONFIGS_ANY(X, SC_FP8) \
   FQL_SC_CONFIGS_ANY(X, SC_FP8_BLOCK)
 
+// Configurations of the fused-epilogue calls alone (see plan_sc_fused), 8-bit
+// formats: 64 x 64, 128 x 64 and 128 x 128 tiles, the latter two on 8 waves.
+#define FQL_SCX_CONFIGS(X, F) X(F, 2, 2, 2, 2, 4) X(F, 4, 2, 2, 2, 4) X(F, 2, 4, 4, 2, 4)
+#define FQL_SCX_CONFIGS_ALL(X) \
+  FQL_SCX_CONFIGS(X, SC_MXFP8) FQL_SCX_CONFIGS(X, SC_FP8) FQL_SCX_CONFIGS(X, SC_FP8_BLOCK)
+
 // (W, MT, NT, D) GEMV configurations built: 4 waves, one row tile with four
 // (FP4) or two (8-bit) column tiles, two row tiles with two column tiles.
 #define FQL_SCV_CONFIGS_FP4(X, F) X(F, 4, 1, 4, 3) X(F, 4, 2, 2, 3)
@@ -971,6 +977,69 @@ ScPlan plan_sc_gemm(int fmt, int64_t M, int64_t N, int64_t K) {
   return p;
 }
 
+// Plan of a fused-epilogue call. Where the plain plan fills the card with split
+// ranges of K, joining them costs more than it saves (sweep of every built tile
+// and 1 .. 8 ranges at M = 33 .. 2048 on six layers: 4096 x 4096 at M = 256
+// 31.6 us with 128 x 128 tiles in four ranges, 12.5 with 64 x 64 tiles whole).
+// So the tile is chosen by time: rounds * (chunks * tc + f) + joining, in us,
+// with tc of one 128-deep chunk and f of a workgroup's start and epilogue as
+// the sweep gives them (8-bit formats: the two columns of `tiles` are MXFP8 and
+// per-tensor FP8, block FP8). The two smaller tiles fit twice into a CU's LDS;
+// two chunks then take `pair` times one.
+ScPlan plan_sc_fused(int fmt, int64_t M, int64_t N, int64_t K) {
+  const ScPlan plain = plan_sc_gemm(fmt, M, N, K);
+  if (fmt == SC_MXFP4 || plain.kind == 1 || !plan_override(kOverrideScGemm).empty()) return plain;
+  struct Tile {
+    int wm, wn, mtw, ntw, st;
+    double tc[2], f, pair;
+  };
+  static constexpr Tile tiles[] = {
+      {1, 4, 1, 2, 4, {0.22, 0.26}, 5.0, 1.6},  {2, 2, 2, 2, 4, {0.19, 0.30}, 6.3, 1.8},
+      {4, 2, 2, 2, 4, {0.31, 0.38}, 6.0, 0.0},  {2, 4, 4, 2, 4, {0.45, 0.60}, 9.0, 0.0},
+      {4, 2, 4, 4, 3, {0.80, 1.00}, 15.0, 0.0},
+  };
+  const ScDims w = sc_dims(fmt, N, K, true);
+  const Tile* best = nullptr;
+  int64_t best_splits = 1;
+  double best_cost = 0.0;
+  for (const Tile& t : tiles) {
+    const int64_t rows = 16 * t.wm * t.mtw, cols = 16 * t.wn * t.ntw;
+    const int64_t groups = (round_up(M, rows) / rows) * (round_up(N, cols) / cols);
+    for (int64_t s = 1; s <= 8 && (s == 1 || (w.KC / s >= 8 && groups <= 16384)); ++s) {
+      const double chunks = (double)((w.KC + s - 1) / s), tc = t.tc[fmt == SC_FP8_BLOCK ? 1 : 0];
+      const int64_t wgs = groups * s;
+      double cost;
+      if (wgs <= 256 || t.pair == 0.0) cost = (double)((wgs + 255) / 256) * (chunks * tc + t.f);
+      else cost = (double)((wgs + 511) / 512) * (chunks * tc * t.pair + t.f);
+      if (s > 1) cost += 2.0 + (double)(rows * cols) / 256.0 * (0.035 * (double)s + 0.09);
+      if (best == nullptr || cost < best_cost) {
+        best = &t;
+        best_splits = s;
+        best_cost = cost;
+      }
+    }
+  }
+  if (best->wm == plain.wm && best->wn == plain.wn && best->mtw == plain.mtw && best->ntw == plain.ntw &&
+      best_splits == 1 && plain.dp_groups > 0)
+    return plain;  // the same tile whole, with the plain plan's treatment of the last round
+  ScPlan p = plain;
+  p.wm = best->wm; p.wn = best->wn; p.mtw = best->mtw; p.ntw = best->ntw; p.st = best->st;
+  const int tile_rows = 16 * p.wm * p.mtw, tile_cols = 16 * p.wn * p.ntw;
+  p.Mp = round_up(M, tile_rows);
+  p.ngroups = (w.rows_p + tile_cols - 1) / tile_cols;
+  p.groups = p.ngroups * (p.Mp / tile_rows);
+  p.kc_per_split = (int)((w.KC + best_splits - 1) / best_splits);
+  p.splits = (int)((w.KC + p.kc_per_split - 1) / p.kc_per_split);
+  p.dp_groups = p.splits > 1 ? 0 : p.groups;
+  const ScDims x = sc_dims(fmt, p.Mp, K, false);
+  p.xcode_bytes = round_up(x.code_bytes, 256);
+  p.xscale_bytes = round_up(x.scale_bytes, 256);
+  const int64_t slab = (int64_t)p.splits * p.wm * p.wn * p.mtw * p.ntw * 64 * 16;
+  p.partial_bytes = p.splits > 1 ? round_up(p.groups * slab, 256) : 0;
+  p.total_bytes = p.counter_bytes + p.xcode_bytes + p.xscale_bytes + p.partial_bytes;
+  return p;
+}
+
 std::string describe_sc_plan(const ScPlan& p) {
   char b[240];
   if (p.kind == 1 && p.fq) {
@@ -1024,6 +1093,20 @@ static hipError_t launch_sc_t(const ScPlan& p, const uint8_t* xc, const uint8_t*
 #undef FQL_GEMM
     return hipGetLastError();
   }
+}
+
+// A configuration that is built with the fused epilogue only.
+template <int F, int WM, int WN, int MTW, int NTW, int ST>
+static hipError_t launch_scx_t(const ScPlan& p, const uint8_t* xc, const uint8_t* xs, const uint8_t* packed,
+                               const ScDims& w, int64_t M, int64_t N, const ScOut& o, float4v* partial,
+                               uint32_t* counters, hipStream_t st) {
+  static_assert(sc_config_fits<F, WM, WN, MTW, NTW, ST>(), "ring in LDS");
+  if (o.epi == nullptr) return hipErrorInvalidValue;
+  const int64_t grid = p.dp_groups + (p.groups - p.dp_groups) * p.splits;
+  gemm_sc_kernel<F, WM, WN, MTW, NTW, ST, true><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(
+      xc, xs, packed, packed + w.code_bytes, (int)M, (int)N, w.KC, (int)(w.rows_p / 16), w.quads, (int)p.ngroups,
+      p.kc_per_split, (int)p.dp_groups, p.splits, o.alpha, o.alpha_dev, o.bias, o.y, o.ldy, partial, counters, *o.epi);
+  return hipGetLastError();
 }
 
 template <int F, int W, int MT, int NT, int D>
@@ -1097,6 +1180,11 @@ static hipError_t launch_sc_any(const ScPlan& p, const uint16_t* x, int64_t M, i
     return launch_sc_t<F0, A, B, C, D, E>(p, xc, xs, packed, w, M, N, o, partial, counters, st);
   FQL_SC_CONFIGS_ALL(FQL_X)
 #undef FQL_X
+#define FQL_X(F0, A, B, C, D, E)                                                       \
+  if (p.fmt == F0 && p.wm == A && p.wn == B && p.mtw == C && p.ntw == D && p.st == E)  \
+    return launch_scx_t<F0, A, B, C, D, E>(p, xc, xs, packed, w, M, N, o, partial, counters, st);
+  FQL_SCX_CONFIGS_ALL(FQL_X)
+#undef FQL_X
   return hipErrorInvalidValue;
 }
 
@@ -1113,10 +1201,8 @@ hipError_t launch_sc_linear_fused(const ScPlan& p, const uint16_t* x, int64_t M,
                                   const uint8_t* packed, int64_t N, float alpha, const float* alpha_dev,
                                   const uint16_t* bias, const ScEpilogue& epi, uint16_t* y, int64_t ldy,
                                   uint8_t* workspace, hipStream_t st) {
-  // no activation and no residual: the plain kernels' epilogue
-  const bool plain = epi.act == kActNone && epi.residual == nullptr;
   return launch_sc_any(p, x, M, K, ldx, aligned, inv_scale, x_operand, packed, N,
-                       ScOut{alpha, alpha_dev, bias, y, ldy, plain ? nullptr : &epi}, workspace, st);
+                       ScOut{alpha, alpha_dev, bias, y, ldy, &epi}, workspace, st);
 }
 
 }  // namespace fql

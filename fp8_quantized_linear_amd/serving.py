@@ -26,7 +26,7 @@ import struct
 import torch
 
 from . import (FMT_FP8, FMT_FP8_BLOCK, FMT_MXFP4, FMT_MXFP8, FQLError, _check, _rows_view, _size_query, _workspaces,
-               lib, linear_sc_workspace_bytes, new_workspace)
+               lib, new_workspace)
 
 FORMATS = {"mxfp4": FMT_MXFP4, "mxfp8": FMT_MXFP8, "fp8": FMT_FP8, "fp8_block": FMT_FP8_BLOCK}
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
@@ -37,7 +37,6 @@ ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu":
 # are remembered.
 _stream = torch._C._cuda_getCurrentRawStream  # device index -> hipStream_t of torch's current stream
 _bf16, _u8, _i32 = torch.bfloat16, torch.uint8, torch.int32
-_linear_workspace_bytes = functools.lru_cache(4096)(linear_sc_workspace_bytes)
 _query = functools.lru_cache(4096)(_size_query)
 
 
@@ -192,6 +191,13 @@ def interleave_gate_up(gate, up):
     return both.flatten(0, 2).contiguous()
 
 
+def linear_fused_plan(fmt, M, N, K):
+    """One-line description of the launch plan of a linear_fused call."""
+    buf = ctypes.create_string_buffer(256)
+    _check(lib().fql_linear_fused_describe(_format(fmt), int(M), int(N), int(K), buf, 256))
+    return buf.value.decode()
+
+
 def linear_fused(x, weight, activation=None, bias=None, residual=None, alpha=None, out=None, workspace=None):
     """y = bf16(act(alpha * x_q @ W_q^T + bias) + residual), rounded once.
 
@@ -229,7 +235,7 @@ def linear_fused(x, weight, activation=None, bias=None, residual=None, alpha=Non
     if residual is not None:
         rp, _, _, ldr = _rows(residual, "residual", shape)
     if workspace is None:
-        workspace = _workspace(dev, _linear_workspace_bytes(fmt, M, N, K))
+        workspace = _workspace(dev, _query("fql_linear_fused_workspace_bytes", FORMATS[fmt], M, N, K))
     scale = weight.input_scale if fmt == "fp8" else 0
     ap = weight.alpha_dev.data_ptr() if fmt == "fp8" and alpha is None else 0
     _check(lib().fql_linear_fused(FORMATS[fmt], xp, M, K, ld, scale, op, weight.packed.data_ptr(), N,

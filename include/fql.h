@@ -538,8 +538,13 @@ int fql_quant_operand(int format, const void* x, int64_t M, int64_t K, int64_t l
  *              in groups of 16 gate rows followed by their 16 up rows, N is a
  *              multiple of 32, and y and residual have N / 2 columns.
  *   residual   [M][ldr] bf16 or NULL; may be y itself (same pointer, stride).
- *   workspace  as fql_linear_<format> (fql_linear_<format>_workspace_bytes).
+ *   workspace  as fql_linear_<format>, of fql_linear_fused_workspace_bytes. The
+ *              call has launch plans of its own, so its float32 sum over K may
+ *              be in another order than fql_linear_<format>'s.
  */
+int fql_linear_fused_workspace_bytes(int format, int64_t M, int64_t N, int64_t K, size_t* bytes);
+/* One-line description of the launch plan (host-side). */
+int fql_linear_fused_describe(int format, int64_t M, int64_t N, int64_t K, char* buf, size_t buf_len);
 int fql_linear_fused(int format, const void* x, int64_t M, int64_t K, int64_t ldx, float input_scale,
                      const void* x_operand, const void* w_packed, int64_t N, float alpha,
                      const float* alpha_dev, const void* bias, int activation, const void* residual,

@@ -273,16 +273,53 @@ def test_linear_residual_in_place(fmt, M):
 
 
 @pytest.mark.parametrize("fmt", ("mxfp4",) + FMTS)
-def test_linear_without_epilogue_is_the_plain_layer(fmt):
+def test_linear_without_epilogue(fmt):
     announce(f"linear plain {fmt}")
     rng = np.random.default_rng(5)
     for M in (3, 40, 200):
-        x, _ = bf16(rng.standard_normal((M, 512)))
-        g, _ = layer(fmt, rng.standard_normal((384, 512)) * 0.1)
-        b, _ = bf16(rng.standard_normal(384))
-        plain = {"mxfp4": fql.linear_mxfp4, "mxfp8": fql.linear_mxfp8, "fp8": fql.linear_fp8,
-                 "fp8_block": fql.linear_fp8_block}[fmt]
-        assert torch.equal(fql.linear_fused(x, g, bias=b), plain(x, g, bias=b))
+        x, x64 = bf16(rng.standard_normal((M, 512)))
+        g, wh = layer(fmt, rng.standard_normal((384, 512)) * 0.1)
+        b, b64 = bf16(rng.standard_normal(384))
+        y = fql.linear_fused(x, g, bias=b)
+        check_linear(y, activation_hat(fmt, x64), wh, b64, "none", None, fmt)
+        if M <= 32:  # one plan, one order of the sum: the plain layer bit for bit
+            plain = {"mxfp4": fql.linear_mxfp4, "mxfp8": fql.linear_mxfp8, "fp8": fql.linear_fp8,
+                     "fp8_block": fql.linear_fp8_block}[fmt]
+            assert torch.equal(y, plain(x, g, bias=b))
+
+
+# (M, N, K) whose plans are, in turn: 16 x 128, 64 x 64, 128 x 64, 128 x 128 and 256 x 128 tiles whole, and
+# 64 x 64, 128 x 64 and 128 x 128 tiles with K in ranges (checked on rows and columns of a sample)
+PLANNED = [(40, 1000, 1024, "MTW=1,NTW=2"), (250, 4096, 1024, "MTW=2,NTW=2"), (500, 4000, 512, "WM=4,WN=2,MTW=2"),
+           (1000, 4096, 512, "WM=2,WN=4,MTW=4"), (1900, 4096, 512, "WM=4,WN=2,MTW=4"), (60, 4096, 14336, "splits=4"),
+           (120, 4096, 14336, "splits"), (250, 5120, 12800, "splits")]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K,kind", PLANNED)
+def test_linear_planned_tiles(fmt, M, N, K, kind):
+    N = N // 128 * 128 if fmt == "fp8_block" else N
+    announce(f"linear {fmt} {M}x{N}x{K} {fql.linear_fused_plan(fmt, M, N, K)}")
+    rng = np.random.default_rng([M, N])
+    x, x64 = bf16(rng.standard_normal((M, K), dtype=np.float32))
+    W = rng.standard_normal((N, K), dtype=np.float32) * np.float32(0.05)
+    wd = torch.from_numpy(W).to(DEV)
+    g = {"fp8": lambda: fql.FP8Weight.from_float(wd, input_scale=0.1), "mxfp8": lambda: fql.MXFP8Weight.from_float(wd),
+         "fp8_block": lambda: fql.FP8BlockWeight.from_float(wd)}[fmt]()
+    r, r64 = bf16(rng.standard_normal((M, N), dtype=np.float32))
+    y = fql.linear_fused(x, g, activation="silu", residual=r)
+    rows = np.unique(np.concatenate([[0, 15, 16, 31, M // 2, M - 17, M - 1], rng.integers(0, M, 16)]))
+    cols = np.arange(N) if N < 256 else np.unique(np.concatenate([np.arange(128), np.arange(N - 128, N)]))
+    if fmt == "fp8":
+        wh = F.e4m3_decode(P.quant_fp8_tensor(W[cols], g.weight_scale)) * g.weight_scale
+    elif fmt == "mxfp8":
+        wh = P.dequant_mxfp8(*P.quant_mxfp8(W[cols]))
+    else:
+        wh = P.dequant_fp8_block_weight(*P.quant_fp8_block_weight(W[cols]))
+    check_linear(y[rows][:, cols], activation_hat(fmt, x64[rows]), wh, None, "silu", r64[np.ix_(rows, cols)],
+                 (fmt, M, N, K))
+    torch.cuda.synchronize()
+    assert torch.equal(fql.linear_fused(x, g, activation="silu", residual=r), y)  # and again: counters are back at zero
 
 
 @pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu", "swiglu"])

@@ -89,6 +89,25 @@ def test_linear_refusals():
     refused(linear(size=16), "workspace", code=-4)
 
 
+def test_linear_plans():
+    """The planner's tiles over the range; workspaces hold the activation operand and the partial sums."""
+    n = ctypes.c_size_t()
+    seen = set()
+    for fmt, code in (("mxfp4", MXFP4), ("mxfp8", MXFP8), ("fp8", FP8), ("fp8_block", BLOCK)):
+        for M in (1, 16, 33, 64, 100, 128, 250, 500, 1000, 1900, 4096):
+            for N, K in ((128, 128), (4096, 4096), (28672, 4096), (4096, 14336), (5120, 25600)):
+                assert fql.lib().fql_linear_fused_workspace_bytes(code, M, N, K, ctypes.byref(n)) == 0
+                assert n.value >= 65536 + M * K // (2 if fmt == "mxfp4" else 1)
+                plan = fql.linear_fused_plan(fmt, M, N, K)
+                if fmt == "mxfp4" or M <= 32:
+                    assert plan == fql.linear_sc_plan(fmt, M, N, K)
+                seen.add(plan.split("<")[-1].split(">")[0].split(",", 1)[1])
+    assert {"WM=2,WN=2,MTW=2,NTW=2,ST=4", "WM=4,WN=2,MTW=2,NTW=2,ST=4", "WM=2,WN=4,MTW=4,NTW=2,ST=4",
+            "WM=4,WN=2,MTW=4,NTW=4,ST=3", "WM=1,WN=4,MTW=1,NTW=2,ST=4"} <= seen, seen
+    refused(fql.lib().fql_linear_fused_workspace_bytes(NVFP4, 4, 64, 128, ctypes.byref(n)), "format", code=-2)
+    refused(fql.lib().fql_linear_fused_workspace_bytes(MXFP8, 4, 64, 100, ctypes.byref(n)), "32")
+
+
 class CacheStruct(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + [("num_blocks", ctypes.c_int64)] + [
         (n, ctypes.c_int32) for n in ("kv_heads", "block_size", "head_dim")]
