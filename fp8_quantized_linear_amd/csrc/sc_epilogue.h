@@ -46,15 +46,23 @@ __device__ __forceinline__ float half_erfc_tail(float a) {
   return 0.5f * a * t * p * __expf(-0.5f * a * a);
 }
 
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+  if (ACT == kActRelu) return z > 0.0f ? z : (z == z ? 0.0f : z);  // NaN stays
+  if (ACT == kActGelu) {
+    const float h = half_erfc_tail(__builtin_fminf(__builtin_fabsf(z), 64.0f));  // 0 beyond
+    return z > 0.0f ? z - h : (z == z ? -h : z);
+  }
+  if (ACT == kActGeluTanh) return z_sigmoid(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
+  if (ACT == kActSilu) return z_sigmoid(z, z);
+  return z;
+}
 __device__ __forceinline__ float apply_act(float z, int act) {
   switch (act) {
-    case kActRelu: return z > 0.0f ? z : (z == z ? 0.0f : z);  // NaN stays
-    case kActGelu: {
-      const float h = half_erfc_tail(__builtin_fminf(__builtin_fabsf(z), 64.0f));  // 0 beyond
-      return z > 0.0f ? z - h : (z == z ? -h : z);
-    }
-    case kActGeluTanh: return z_sigmoid(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
-    case kActSilu: return z_sigmoid(z, z);
+    case kActRelu: return act_of<kActRelu>(z);
+    case kActGelu: return act_of<kActGelu>(z);
+    case kActGeluTanh: return act_of<kActGeluTanh>(z);
+    case kActSilu: return act_of<kActSilu>(z);
     default: return z;
   }
 }
@@ -168,37 +176,48 @@ __device__ __forceinline__ void finish_frags_fused(float4v (&frag)[FR], RowOf ro
   if (tid == 0) __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// write_tile16_staged with the epilogue. The residual's tile is first brought
-// into the staging buffer by 16-byte row pieces (in accumulator order it would
-// be 2-byte gathers); each lane then adds its element to the float32 value and
-// puts the bf16 result in the same place, and the tile leaves by row pieces.
-// GATED: half the columns. The residual may be y itself: a piece is read and
-// written by this workgroup only, the reads before the barrier.
-template <int MT, int NT, int WM, int WN, bool GATED>
-__device__ __forceinline__ void write_tile16_staged_fused(const float4v (&acc)[MT][NT], int m0, int n0, int wm, int wn,
-                                                          const EpiOut& o, uint16_t* lds) {
+// The residual of an R x C output tile as 16-byte row pieces, piece q0 + tid of
+// every round of 64 NW: loaded before the products begin, so that its way from
+// memory passes under them (a workgroup that fills the LDS has no neighbour to
+// hide it under). The residual may be y itself: the tile is read and written
+// by this workgroup only.
+template <int R, int C, int NW, int RP>
+__device__ __forceinline__ void load_residual(const EpiOut& o, int m0, int no, int Nout, uint4v (&piece)[RP]) {
+  static_assert(R * C / 8 <= 64 * NW * RP && R * C / 8 % (64 * NW) == 0, "whole pieces per thread");
+  const bool vec = (o.e.ldr & 7) == 0 && (reinterpret_cast<uintptr_t>(o.e.residual) & 15) == 0;
+#pragma unroll
+  for (int i = 0; i < R * C / 8 / (64 * NW); ++i) {
+    const int q = i * 64 * NW + threadIdx.x;
+    const int m = m0 + q / (C / 8), n = no + (q % (C / 8)) * 8;
+    piece[i] = uint4v{0u, 0u, 0u, 0u};
+    if (m >= o.M) continue;
+    const uint16_t* src = o.e.residual + (int64_t)m * o.e.ldr + n;
+    if (vec && n + 8 <= Nout) {
+      piece[i] = *reinterpret_cast<const uint4v*>(src);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (n + j < Nout) piece[i][j / 2] |= (uint32_t)src[j] << (16 * (j % 2));
+    }
+  }
+}
+
+// write_tile16_staged with the epilogue: the residual's pieces go into the
+// staging buffer (in accumulator order they would be 2-byte gathers), each
+// lane adds its element to the float32 value and puts the bf16 result in the
+// same place, and the tile leaves by row pieces. GATED: half the columns.
+template <int MT, int NT, int WM, int WN, bool GATED, int ACT, int RP>
+__device__ __forceinline__ void write_tile16_act(const float4v (&acc)[MT][NT], int m0, int n0, int wm, int wn,
+                                                 const EpiOut& o, const uint4v (&piece)[RP], uint16_t* lds) {
   constexpr int NW = WM * WN, R = WM * MT * 16, C = WN * NT * 16 / (GATED ? 2 : 1), P = StagedPitch<C>::P;
   const int lane = threadIdx.x & 63;
   const int no = GATED ? n0 / 2 : n0, Nout = GATED ? o.N / 2 : o.N;
   const bool res = o.e.residual != nullptr;
   if (res) {
-    const bool vec = (o.e.ldr & 7) == 0 && (reinterpret_cast<uintptr_t>(o.e.residual) & 15) == 0;
-    constexpr int PIECES = R * C / 8;
-    static_assert(PIECES % (64 * NW) == 0, "whole pieces per thread");
 #pragma unroll
-    for (int q0 = 0; q0 < PIECES; q0 += 64 * NW) {
-      const int q = q0 + threadIdx.x;
-      const int row = q / (C / 8), c0 = (q % (C / 8)) * 8;
-      const int m = m0 + row, n = no + c0;
-      if (m >= o.M) continue;
-      const uint16_t* src = o.e.residual + (int64_t)m * o.e.ldr + n;
-      if (vec && n + 8 <= Nout) {
-        *reinterpret_cast<uint4v*>(&lds[row * P + c0]) = *reinterpret_cast<const uint4v*>(src);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n + i < Nout) lds[row * P + c0 + i] = src[i];
-      }
+    for (int i = 0; i < R * C / 8 / (64 * NW); ++i) {
+      const int q = i * 64 * NW + threadIdx.x;
+      *reinterpret_cast<uint4v*>(&lds[q / (C / 8) * P + (q % (C / 8)) * 8]) = piece[i];
     }
     __syncthreads();
   }
@@ -213,15 +232,37 @@ __device__ __forceinline__ void write_tile16_staged_fused(const float4v (&acc)[M
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) r[mt][i] = res ? bf16_bits_to_f32(p[(mt * 16 + i) * P]) : 0.0f;
+    const float b = o.bias_at(n);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const float4v v = GATED ? o.gate(acc[mt][nt], acc[mt][GATED ? nt + 1 : nt], n) : o.plain(acc[mt][nt], n);
+      float4v v;
+      if (GATED) {
+        v = o.gate(acc[mt][nt], acc[mt][GATED ? nt + 1 : nt], n);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = act_of<ACT>(o.alpha * acc[mt][nt][i] + b);
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[(mt * 16 + i) * P] = (uint16_t)f32_to_bf16_bits(v[i] + r[mt][i]);
     }
   }
   __syncthreads();
   store_staged_tile<R, C, NW>(lds, o.M, Nout, m0, no, o.y, o.ldy);
+}
+
+template <int MT, int NT, int WM, int WN, int RP>
+__device__ __forceinline__ void write_tile16_staged_fused(const float4v (&acc)[MT][NT], int m0, int n0, int wm, int wn,
+                                                          const EpiOut& o, const uint4v (&piece)[RP], uint16_t* lds) {
+#define FQL_ACT(GATED, ACT) write_tile16_act<MT, NT, WM, WN, GATED, ACT>(acc, m0, n0, wm, wn, o, piece, lds)
+  switch (o.e.act) {  // once a tile, not once an element
+    case kActRelu: return FQL_ACT(false, kActRelu);
+    case kActGelu: return FQL_ACT(false, kActGelu);
+    case kActGeluTanh: return FQL_ACT(false, kActGeluTanh);
+    case kActSilu: return FQL_ACT(false, kActSilu);
+    case kActSwiglu: return FQL_ACT(true, kActSwiglu);
+    default: return FQL_ACT(false, kActNone);
+  }
+#undef FQL_ACT
 }
 
 }  // namespace fql

@@ -231,6 +231,25 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_sc_kernel(
 #pragma unroll
     for (int nt = 0; nt < NTW; ++nt) acc[mt][nt] = float4v{0.f, 0.f, 0.f, 0.f};
 
+  const int m0 = mgroup * TA * 16, n0 = ngroup * TB * 16;
+  constexpr bool kStaged = sizeof(stage) >= (size_t)TA * 16 * StagedPitch<TB * 16>::P * 2 &&
+                           (TA * 16 * TB * 16 / 8) % (64 * NW) == 0;
+  // (the gated tile's half as many pieces have to divide evenly too)
+  constexpr bool kStagedFused = EX && kStaged && (TA * 16 * TB * 16 / 16) % (64 * NW) == 0;
+  constexpr int RP = kStagedFused ? TA * 16 * TB * 16 / 8 / (64 * NW) : 1;
+  constexpr bool kPieces = RP <= (T::BLOCK ? 4 : 8);  // registers for the residual through the K loop
+  uint4v piece[RP];
+  auto load_pieces = [&]() {
+    if constexpr (kStagedFused) {
+      const EpiOut o = {M, N, alpha, bias, epi, y, ldy};
+      if (o.gated()) load_residual<TA * 16, TB * 8, NW>(o, m0, n0 / 2, N / 2, piece);
+      else load_residual<TA * 16, TB * 16, NW>(o, m0, n0, N, piece);
+    }
+  };
+  if constexpr (kStagedFused && kPieces) {
+    if (nsplit == 1 && epi.residual != nullptr) load_pieces();
+  }
+
   if constexpr (PF) {
     // This wave's operand fragments of one chunk, in two register sets: the
     // MFMAs of chunk i read set i % 2 while the LDS reads of chunk i+1 fill the
@@ -440,20 +459,17 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_sc_kernel(
   }
   wait_vmcnt<0>();  // no LDS load may still be in flight when the workgroup ends
 
-  const int m0 = mgroup * TA * 16, n0 = ngroup * TB * 16;
   // a whole tile goes out through the ring's LDS when the staged tile fits it
   // (and its 16-byte pieces divide evenly among the threads)
-  constexpr bool kStaged = sizeof(stage) >= (size_t)TA * 16 * StagedPitch<TB * 16>::P * 2 &&
-                           (TA * 16 * TB * 16 / 8) % (64 * NW) == 0;
   if constexpr (EX) {
     const EpiOut o = {M, N, alpha, bias, epi, y, ldy};
-    // the gated tile's half as many pieces have to divide evenly too
-    if constexpr (kStaged && (TA * 16 * TB * 16 / 16) % (64 * NW) == 0) {
+    if constexpr (kStagedFused) {
       if (nsplit == 1) {
+        if constexpr (!kPieces) {
+          if (epi.residual != nullptr) load_pieces();
+        }
         __syncthreads();  // every wave's loads have landed: the ring is free
-        uint16_t* lds = reinterpret_cast<uint16_t*>(&stage[0]);
-        if (o.gated()) write_tile16_staged_fused<MTW, NTW, WM, WN, true>(acc, m0, n0, wm, wn, o, lds);
-        else write_tile16_staged_fused<MTW, NTW, WM, WN, false>(acc, m0, n0, wm, wn, o, lds);
+        write_tile16_staged_fused<MTW, NTW, WM, WN>(acc, m0, n0, wm, wn, o, piece, reinterpret_cast<uint16_t*>(&stage[0]));
         return;
       }
     }
