@@ -1159,9 +1159,8 @@ int fql_quant_operand(int format, const void* x, int64_t M, int64_t K, int64_t l
     if (int r = check_operand(fmt, M, K, operand, operand_bytes)) return r;
     uint8_t* codes = static_cast<uint8_t*>(operand);
     return hip_status(
-        fql::launch_sc_quant_operand(fmt, static_cast<const uint16_t*>(x), M, K, ldx, aligned16(x, ldx, 2), inv,
-                                     fql::round_up(M, 16), codes, codes + fql::operand_dims(fmt, M, K).code_bytes,
-                                     static_cast<hipStream_t>(stream)),
+        fql::launch_quant_operand(fmt, static_cast<const uint16_t*>(x), M, K, ldx, aligned16(x, ldx, 2), inv, codes,
+                                  codes + fql::operand_dims(fmt, M, K).code_bytes, static_cast<hipStream_t>(stream)),
         "quant launch");
   });
 }

@@ -19,6 +19,11 @@ inline ScDims operand_dims(int fmt, int64_t M, int64_t K) {
   return sc_dims(fmt, round_up(M, kOperandRows), K, false);
 }
 
+// bf16 x quantized into an operand's codes and scales (either layout's row
+// padding; rows past M are not written).
+hipError_t launch_quant_operand(int fmt, const uint16_t* x, int64_t M, int64_t K, int64_t ldx, bool aligned,
+                                float inv_scale, uint8_t* codes, void* scales, hipStream_t st);
+
 // ---- residual add + root-mean-square norm + 8-bit quantizer ------------------
 struct NormArgs {
   const uint16_t* x;         // bf16 [M][ldx]

@@ -236,7 +236,77 @@ hipError_t launch_t(const NormArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// The formats' activation quantizer straight into an operand: one wave a
+// 16-row tile and 128-deep chunk, lane 16 kg + r the 32-block kg of row r. The
+// operand interleaves 16 rows in runs of 256 bytes, so in this order every
+// store instruction fills whole runs; with a row's blocks in neighbouring
+// lanes (the standalone quantizer's order) they are 16-byte pieces 256 bytes
+// apart. The block arithmetic is quant_block32's. Rows past M are not written.
+template <int F>
+__global__ __launch_bounds__(256) void quant_operand_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
+                                                            int64_t ldx, bool aligned, float inv_scale, int64_t KC,
+                                                            int64_t waves, uint8_t* __restrict__ codes,
+                                                            void* __restrict__ scales) {
+  constexpr int H = F == SC_MXFP4 ? 1 : 2;
+  const int64_t w = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (w >= waves) return;
+  const int lane = threadIdx.x & 63, r = lane & 15, kg = lane >> 4;
+  const int64_t tile = w / KC, c = w - tile * KC, m = tile * 16 + r, b = 4 * c + kg;
+  const bool valid = m < M && b * 32 < K;
+  float v[32];
+  if (valid) load32(x + m * ldx + b * 32, aligned, v);
+  else
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+  uint32_t q[8], sb = 0;
+  float gs = 0.0f;
+  if (F == SC_FP8_BLOCK) {
+    float a = amax32(v);
+    a = __builtin_fmaxf(a, __shfl_xor(a, 16));
+    a = __builtin_fmaxf(a, __shfl_xor(a, 32));
+    gs = a / 448.0f;
+    encode_fp8x32(v, safe_reciprocal(gs), q);
+  } else {
+    quant_block32<F>(v, valid, inv_scale, q, sb, gs);
+  }
+  if (m >= M) return;
+  if (!valid) {  // past K: zero codes, zero scale bytes
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = 0u;
+    sb = 0;
+  }
+  uint8_t* const base = codes + w * (H * 1024);
+  if (F == SC_MXFP4) {
+    *reinterpret_cast<uint4v*>(base + lane * 16) = uint4v{q[0], q[1], q[2], q[3]};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int h16 = 2 * kg + j;
+      *reinterpret_cast<uint4v*>(base + (h16 / 4) * 1024 + ((h16 % 4) * 16 + r) * 16) =
+          uint4v{q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]};
+    }
+  }
+  const int64_t quad = m / 64;
+  if (F == SC_MXFP4 || F == SC_MXFP8)
+    static_cast<uint8_t*>(scales)[((quad * KC + c) * 64 + lane) * 4 + (int)(tile % 4)] = (uint8_t)sb;
+  if (F == SC_FP8_BLOCK && kg == 0) static_cast<float*>(scales)[(quad * KC + c) * 64 + m % 64] = gs;
+}
+
 }  // namespace
+
+hipError_t launch_quant_operand(int fmt, const uint16_t* x, int64_t M, int64_t K, int64_t ldx, bool aligned,
+                                float inv_scale, uint8_t* codes, void* scales, hipStream_t st) {
+  const int64_t KC = (K + 127) / 128, waves = (M + 15) / 16 * KC;
+  const unsigned grid = (unsigned)((waves + 3) / 4);
+#define FQL_Q(F)                                                                                                   \
+  if (fmt == F) {                                                                                                  \
+    quant_operand_kernel<F><<<grid, 256, 0, st>>>(x, M, K, ldx, aligned, inv_scale, KC, waves, codes, scales);     \
+    return hipGetLastError();                                                                                      \
+  }
+  FQL_Q(SC_MXFP4) FQL_Q(SC_MXFP8) FQL_Q(SC_FP8) FQL_Q(SC_FP8_BLOCK)
+#undef FQL_Q
+  return hipErrorInvalidValue;
+}
 
 hipError_t launch_rms_norm_quant(int fmt, bool operand, const NormArgs& a, hipStream_t st) {
 #define FQL_F(F) \

@@ -1180,7 +1180,9 @@ static hipError_t launch_sc_any(const ScPlan& p, const uint16_t* x, int64_t M, i
 #undef FQL_X
     return hipErrorInvalidValue;
   } else {
-    const hipError_t e = launch_sc_quant_operand(p.fmt, x, M, K, ldx, aligned, inv_scale, p.Mp, xc_ws, xs_ws, st);
+    const hipError_t e =
+        o.epi != nullptr ? launch_quant_operand(p.fmt, x, M, K, ldx, aligned, inv_scale, xc_ws, xs_ws, st)
+                         : launch_sc_quant_operand(p.fmt, x, M, K, ldx, aligned, inv_scale, p.Mp, xc_ws, xs_ws, st);
     if (e != hipSuccess) return e;
   }
   if (p.kind == 1) {
