@@ -475,7 +475,8 @@ __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kern
         for (int r = 0; r < 4; ++r) x[t][4 * i + r] = acc[t][r];
     }
     const bool in = there;
-    const float ks = e8m0(ksb) * sl2, vs = in ? e8m0(vsb) : 0.0f;
+    const float ks = e8m0(ksb) * sl2;
+    float vs = e8m0(vsb);
     next = after;
     if (more) {
       after = look_up(t0 + 2 * STEP);
@@ -498,6 +499,7 @@ __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kern
       // Values of tokens that no row sees may hold anything, and 0 * NaN is
       // not 0: they are zeroed.
       mask_values<VT>(vw, have, skip);
+      if (skip >= have) vs = 0.0f;  // and so may their block's scale (0 * 2^128)
       // NaN where rows differ in what they see: see put_nan_rows
       if ((t0 < last.lo || t0 + 64 > first.hi) && drop_nan<VT>(vw)) s_nan = 1u;
     } else {

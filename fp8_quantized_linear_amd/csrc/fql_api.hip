@@ -1280,7 +1280,7 @@ int fql_attention_kv8(const fql_kv_cache* cache, const fql_kv_batch* batch, cons
     if (int r = check_attention(b.B, q_heads, c.heads, c.D, b.max_new, max_len, window)) return r;
     if (!q || !out || !workspace) return fail(FQL_ERR_INVALID, "null pointer");
     if (q_ld_token < 0 || q_ld_head < 0 || o_ld_token < 0 || o_ld_head < 0) return fail(FQL_ERR_INVALID, "negative stride");
-    if (!(scale >= 0.0f) || !std::isfinite(scale)) return fail(FQL_ERR_INVALID, "scale must be finite and >= 0");
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(FQL_ERR_INVALID, "scale must be finite and > 0");
     if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return fail(FQL_ERR_INVALID, "workspace must be 256-byte aligned");
     if (b.T == 0 || b.max_new == 0) return ok();
     const fql::AttnPlan plan = fql::plan_attention(b.B, q_heads, c.heads, c.D, b.max_new, max_len, window);

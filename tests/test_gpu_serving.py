@@ -546,6 +546,23 @@ def test_attention_blocks_outside_the_cache_are_absent(new):
     assert_attention(out, lse, S.attention(q64, cache, table, [L], [0, new], D ** -0.5), "blocks")
 
 
+@pytest.mark.parametrize("new", [1, 5, 60])
+def test_attention_blocks_below_the_window_may_hold_anything(new):
+    rng = np.random.default_rng([12, new])
+    bs, H, D, Hq, L, window = 16, 2, 128, 4, 300, 40
+    table = tables(rng, 1, 19, 21, [L], bs, -1)
+    cache = random_cache(rng, 21, H, bs, D)
+    poison(cache, table, [L])
+    for i in range((L - new - window + 1) // bs):  # blocks that no row sees
+        blk = table[0, i]
+        cache.k[blk], cache.v[blk], cache.ke[blk], cache.ve[blk] = 0x7F, 0x7F, 128, 128  # scale byte 255
+    q, q64 = bf16(rng.standard_normal((new, Hq, D)))
+    announce(f"attention stale blocks new={new}")
+    out, lse = fql.attention_kv8(q, to_device(cache), i32(table), i32([L]), i32([0, new]), new, window=window,
+                                 return_lse=True)
+    assert_attention(out, lse, S.attention(q64, cache, table, [L], [0, new], D ** -0.5, window=window), "stale")
+
+
 @pytest.mark.parametrize("new", [6, 40, 200])
 @pytest.mark.parametrize("Hq", [1, 4])
 def test_attention_nan_tokens_reach_only_rows_that_see_them(new, Hq):

@@ -186,6 +186,7 @@ def test_append_and_attention_refusals():
     refused(attend(Hq=0), "q_heads")
     refused(attend(scale=float("inf")), "scale")
     refused(attend(scale=-0.1), "scale")
+    refused(attend(scale=0.0), "scale")
     refused(attend(window=-1), "window")
     refused(attend(max_len=0), "max_len")
     refused(attend(ws=ctypes.c_void_p((1 << 20) + 16)), "256")
