@@ -8,8 +8,13 @@
 //   FP8 or MXFP8; quant_block8 below)
 //
 // Roundings: h is rounded to bf16 only where it is stored; the norm and the
-// quantizer take the unrounded float32 sum, so a code carries one rounding.
-// The sum of squares is float32: per thread in element order, then a tree.
+// quantizer take the unrounded float32 sum. The sum of squares and the row's
+// factor 1 / sqrt(..) are float64 (float32 for block FP8), y is float32; where the codes of FP8 and
+// MXFP8 could differ for a y off by its rounding, they are made again from
+// float64 (exact_codes), so a code carries one rounding, its own. The codes of
+// block FP8 are those of the float32 y over the float32 scale.
+#include <type_traits>
+
 #include "fql_device.h"
 #include "fql_serving.h"
 #include "sc_quant.h"
@@ -51,14 +56,51 @@ __device__ __forceinline__ void store8(uint16_t* p, const Vec8& r, bool aligned)
   }
 }
 
+// 2^e-scaled or plain quotient d -> float32, rounded to odd: the E4M3 rounding
+// of the result is that of d itself (float32 has more than two bits more).
+__device__ __forceinline__ float round_to_odd(double d) {
+  const float t = (float)d;
+  uint32_t b = __float_as_uint(t);
+  const double back = (double)t;
+  if (back == d || d != d) return t;
+  if (__builtin_fabs(back) > __builtin_fabs(d)) b -= 1u;
+  return __uint_as_float(b | 1u);
+}
+
+// Codes of eight values h * rinv * w * f from float64, where those of the
+// float32 product (off by at most 4 roundings, 2^-22) are not sure: one vector
+// in some ten thousand.
+__device__ __forceinline__ void exact_codes(const Vec8& h, const Vec8& wt, double rinv, const Vec8& y, float f,
+                                            uint32_t w[2]) {
+#pragma clang fp contract(off)
+  const float lo = f * (1.0f - 0x1p-21f), hi = f * (1.0f + 0x1p-21f);
+  uint32_t differ = 0u;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    differ |= fp8x4(y.v[4 * j] * lo, y.v[4 * j + 1] * lo, y.v[4 * j + 2] * lo, y.v[4 * j + 3] * lo) ^
+              fp8x4(y.v[4 * j] * hi, y.v[4 * j + 1] * hi, y.v[4 * j + 2] * hi, y.v[4 * j + 3] * hi);
+  if (differ == 0u) return;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float u = h.v[4 * j + i];
+      __asm__("" : "+v"(u));  // converted here: kept from the sum of squares, its float64 would spill
+      c[i] = round_to_odd((double)u * rinv * (double)wt.v[4 * j + i] * (double)f);
+    }
+    w[j] = fp8x4(c[0], c[1], c[2], c[3]);
+  }
+}
+
 // Codes of eight consecutive values (two words) and the scale of their block.
 // A block of 32 (MXFP8) or 128 (block FP8) values is held by 4 or 16
 // neighbouring lanes, all of which must call this.
 template <int F>
 __device__ __forceinline__ void quant_block8(const Vec8& y, float inv_scale, uint32_t w[2], uint32_t& sbyte,
-                                             float& gscale) {
+                                             float& gscale, float& f) {
 #pragma clang fp contract(off)
-  float f = inv_scale;
+  f = inv_scale;
   if (F != SC_FP8) {
     float a = 0.0f;
 #pragma unroll
@@ -123,19 +165,21 @@ __device__ __forceinline__ Vec8 load_h(const NormArgs& a, const NormFlags& f, in
 
 template <int F, bool OP>
 __device__ __forceinline__ void finish_vec(const NormArgs& a, const NormFlags& f, int64_t m, int64_t v, int64_t nv,
-                                           int64_t nvp, const Vec8& h, float rinv) {
+                                           int64_t nvp, const Vec8& h, double rinv) {
 #pragma clang fp contract(off)
-  Vec8 y;
+  Vec8 y, w;
+  const float r = (float)rinv;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) y.v[j] = 0.0f;
+  for (int j = 0; j < 8; ++j) y.v[j] = w.v[j] = 0.0f;
   if (v < nv) {
-    const Vec8 w = load8(a.weight + 8 * v, f.w);
+    w = load8(a.weight + 8 * v, f.w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y.v[j] = h.v[j] * rinv * w.v[j];
+    for (int j = 0; j < 8; ++j) y.v[j] = h.v[j] * r * w.v[j];
   }
   uint32_t q[2], sb = 0;
-  float gs = 0.0f;
-  quant_block8<F>(y, a.inv_scale, q, sb, gs);
+  float gs = 0.0f, factor;
+  quant_block8<F>(y, a.inv_scale, q, sb, gs, factor);
+  if (F != SC_FP8_BLOCK) exact_codes(h, w, rinv, y, factor, q);
   if (OP && v >= nv) sb = 0;  // padding up to the chunk: zero codes, zero scale bytes
   if (v < (OP ? nvp : nv)) store_codes<F, OP>(a, m, v, q, sb, gs);
 }
@@ -145,7 +189,7 @@ __device__ __forceinline__ void finish_vec(const NormArgs& a, const NormFlags& f
 // thread). STREAM: rows too long for that read x and the residual twice.
 template <int F, bool OP, int I, bool WAVE, bool STREAM>
 __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, const NormFlags f) {
-  __shared__ float red[16];
+  __shared__ std::conditional_t<F == SC_FP8_BLOCK, float, double> red[16];
   int64_t m;
   int t, T;
   if (WAVE) {
@@ -166,7 +210,10 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
   }
   const int64_t nv = a.K / 8, nvp = OP ? (a.K + 127) / 128 * 16 : nv;
   Vec8 h[I];
-  float ss = 0.0f;
+  // float32 where the codes are those of a float32 y (float64 takes 8192 x 5120
+  // block FP8 from 58 to 60 us)
+  using Sum = std::conditional_t<F == SC_FP8_BLOCK, float, double>;
+  Sum ss = 0;
   if (!STREAM) {
 #pragma unroll
     for (int i = 0; i < I; ++i) {
@@ -176,13 +223,13 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i].v[j] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss += h[i].v[j] * h[i].v[j];
+      for (int j = 0; j < 8; ++j) ss += (Sum)h[i].v[j] * (Sum)h[i].v[j];
     }
   } else {
     for (int64_t v = t; v < nv; v += T) {
       const Vec8 u = load_h(a, f, m, v, false);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss += u.v[j] * u.v[j];
+      for (int j = 0; j < 8; ++j) ss += (Sum)u.v[j] * (Sum)u.v[j];
     }
   }
 #pragma unroll
@@ -190,10 +237,12 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
   if (!WAVE) {
     if ((t & 63) == 0) red[t >> 6] = ss;
     __syncthreads();
-    ss = 0.0f;
+    ss = 0;
     for (int i = 0; i < T / 64; ++i) ss += red[i];
   }
-  const float rinv = 1.0f / __builtin_sqrtf(ss / (float)a.K + a.eps);
+  Sum rinv;
+  if constexpr (F == SC_FP8_BLOCK) rinv = 1.0f / __builtin_sqrtf(ss / (float)a.K + a.eps);
+  else rinv = 1.0 / __builtin_sqrt(ss / (double)a.K + (double)a.eps);
   if (!STREAM) {
 #pragma unroll
     for (int i = 0; i < I; ++i) {

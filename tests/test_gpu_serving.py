@@ -106,6 +106,24 @@ def test_norm(fmt, M, K):
         assert h2 is None or torch.equal(h2, hout)
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp8"])
+@pytest.mark.parametrize("M,K", [(700, 4096), (3000, 512), (40, 70016)])
+def test_norm_codes_are_those_of_the_exact_values(fmt, M, K):
+    """One rounding: every code is that of the float64 y (whose own error, some 2^-50, no value here
+    is near enough to a tie to show)."""
+    announce(f"norm exact codes {fmt} {M}x{K}")
+    rng = np.random.default_rng([7, M, K])
+    x, x64 = bf16(rng.standard_normal((M, K)))
+    w, w64 = bf16(1 + 0.2 * rng.standard_normal(K))
+    y, _ = S.rms_norm(x64, w64, float(np.float32(1e-5)), None)
+    codes, scales, _ = fql.rms_norm_quant(x, w, fmt, eps=float(np.float32(1e-5)), scale=0.0625 if fmt == "fp8" else None)
+    s = 0.0625 if fmt == "fp8" else np.repeat(np.ldexp(1.0, scales.cpu().numpy().astype(np.int64) - 127), 32, axis=1)
+    got = codes.cpu().view(torch.float8_e4m3fn).double().numpy()
+    v = np.clip(y / s, -448, 448)
+    step = np.ldexp(1.0, np.maximum(np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -40))), -6).astype(np.int64) - 3)
+    assert np.array_equal(got, np.rint(v / step) * step)
+
+
 @pytest.mark.parametrize("fmt,K", [("fp8", 4096 + 32), ("mxfp8", 96), ("mxfp8", 4096 + 32), ("fp8", 32)])
 def test_norm_columns_that_end_inside_a_chunk(fmt, K):
     announce(f"norm tail {fmt} K={K}")
