@@ -633,10 +633,21 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 31, hf = lane >> 5;
-  const int h = blockIdx.x, b = blockIdx.y, H = c.heads, bs = c.block_size;
+  // Workgroups go in turn to the XCDs and, within one, to its four shader
+  // engines, so with blockIdx.y taken as it is the long sequences of a batch of
+  // 2, 4 or 8 would all run on the same engines: the assignment moves on by one
+  // every second blockIdx.z (prompts of 2048, 1098, 1685, 736 tokens, 32 heads:
+  // 154 -> 104 us).
+  const int h = blockIdx.x, H = c.heads, bs = c.block_size;
+  const int b = gridDim.y == 1 ? 0 : (int)((blockIdx.y + blockIdx.z / 2) % gridDim.y);
   const int z = splits == 1 ? 0 : (int)blockIdx.z / row_tiles;
-  // the last row tiles see the most keys under a causal mask: they start first
-  const int rt = row_tiles - 1 - ((int)blockIdx.z - z * row_tiles);
+  // The last row tiles see the most keys under a causal mask: they start first.
+  // Where all workgroups run at once, two a CU, the second half starts with the
+  // fewest, so that long ones get short neighbours (a prompt of 2048 tokens, 32
+  // heads: 66 -> 59 us).
+  const int ri = (int)blockIdx.z - z * row_tiles, upper = (row_tiles + 1) / 2;
+  const bool at_once = D != 256 && gridDim.x * gridDim.y * gridDim.z <= 512;
+  const int rt = at_once && ri >= upper ? ri - upper : row_tiles - 1 - ri;
   const SeqSpan s = seq_span(pb, b, bs);
   const int rows = s.n * a.group, row0 = rt * ROWS;
   if (row0 >= rows) return;
@@ -960,9 +971,11 @@ AttnPlan plan_attention(int B, int Hq, int Hkv, int D, int64_t max_new, int64_t 
       }
     }
   } else {
-    // many rows: two rounds of workgroups (sequences differ in length), of at
-    // least 2048 keys (2 x 512 tokens on 32768: 1.15 ms whole, 1.11 in two)
-    splits = std::max<int64_t>(1, std::min<int64_t>((1024 + tiles - 1) / tiles, span / 2048));
+    // many rows: four rounds of workgroups (sequences differ in length), of at
+    // least 2048 keys. 512 and 274 new tokens on 32768 and 17579, 64 heads: 1.03
+    // ms whole, 1.00 in two ranges, 0.85 in four, 0.82 in eight; 512 each on
+    // 32768: 1.14 in two and four, 1.17 in eight, 1.26 in ranges of 2048.
+    splits = std::max<int64_t>(1, std::min<int64_t>((2048 + tiles - 1) / tiles, span / 2048));
   }
   // one arrival counter a tile, below the words a linear call keeps its device scalars in
   if (tiles > kWorkspaceScalarOffset / 4) splits = 1;
