@@ -505,7 +505,7 @@ def linear_plan(M, N, K, aligned=True, transform=False, hadamard_block=0):
 
 
 _workspaces = {}
-
+_outgrown = []  # replaced workspaces: a captured graph may hold their addresses
 
 def new_workspace(nbytes, device):
     """A zero-filled workspace buffer (its leading arrival counters must start at zero;
@@ -517,8 +517,20 @@ def _workspace(device, nbytes):
     key = (device.type, device.index, torch.cuda.current_stream(device).cuda_stream)
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = new_workspace(nbytes, device)
-        _workspaces[key] = ws
+        ws = _grow_workspace(key, nbytes, device)
+    return ws
+
+
+def _grow_workspace(key, nbytes, device):
+    """A new workspace for `key`, at least twice as large as the one it replaces: those are kept,
+    and so hold no more than the newest in all."""
+    old = _workspaces.get(key)
+    if old is not None:
+        nbytes = max(nbytes, 2 * old.numel())
+    ws = new_workspace(nbytes, device)
+    if old is not None:
+        _outgrown.append(old)
+    _workspaces[key] = ws
     return ws
 
 

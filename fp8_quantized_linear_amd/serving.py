@@ -25,8 +25,8 @@ import struct
 
 import torch
 
-from . import (FMT_FP8, FMT_FP8_BLOCK, FMT_MXFP4, FMT_MXFP8, FQLError, _check, _rows_view, _size_query, _workspaces,
-               lib, new_workspace)
+from . import (FMT_FP8, FMT_FP8_BLOCK, FMT_MXFP4, FMT_MXFP8, FQLError, _check, _grow_workspace, _rows_view,
+               _size_query, _workspaces, lib)
 
 FORMATS = {"mxfp4": FMT_MXFP4, "mxfp8": FMT_MXFP8, "fp8": FMT_FP8, "fp8_block": FMT_FP8_BLOCK}
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
@@ -45,7 +45,7 @@ def _workspace(device, nbytes):
     key = (device.type, device.index, _stream(device.index))
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = _workspaces[key] = new_workspace(nbytes, device)
+        ws = _grow_workspace(key, nbytes, device)
     return ws
 
 
@@ -281,9 +281,11 @@ class KVCache8:
         return cls(k, v, s[0], s[1])
 
 
-def _heads(t, name, shape):
-    """(address, token stride, head stride) of a bf16 [tokens, heads, head_dim] tensor."""
+def _heads(t, name, shape, dev):
+    """(address, token stride, head stride) of a bf16 [tokens, heads, head_dim] tensor on the cache's device."""
     _cuda(t, name, _bf16)
+    if t.device != dev:
+        raise FQLError(f"{name} must be on the cache's device")
     if t.shape != shape:
         raise FQLError(f"{name} must have shape {shape}")
     ld_token, ld_head, unit = t.stride()
@@ -308,12 +310,16 @@ def _batch(cache, block_table, lens, cu_seqlens, max_new, tokens):
     ld, unit = block_table.stride()
     if (unit != 1 and cols > 1) or not lens.is_contiguous() or not cu_seqlens.is_contiguous():
         raise FQLError("block_table's rows, lens and cu_seqlens must be contiguous")
+    if B == 1:
+        ld = cols
+    elif ld < cols:
+        raise FQLError("block_table's rows must not overlap (copy an expanded table)")
     new = int(max_new)
     if new < 0:
         raise FQLError("max_new must be >= 0")
     new = new if new < tokens else tokens
-    return struct.pack("PqPPqiii4x", block_table.data_ptr(), ld if B > 1 and ld > cols else cols, lens.data_ptr(),
-                       cu_seqlens.data_ptr(), tokens, cols, B, new), B, cols, new
+    return struct.pack("PqPPqiii4x", block_table.data_ptr(), ld, lens.data_ptr(), cu_seqlens.data_ptr(), tokens, cols, B,
+                       new), B, cols, new
 
 
 def kv_append(cache, k, v, block_table, lens, cu_seqlens, max_new):
@@ -325,8 +331,8 @@ def kv_append(cache, k, v, block_table, lens, cu_seqlens, max_new):
         raise FQLError("k must be a tensor [tokens, kv_heads, head_dim]")
     T = k.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
-    kp, kt, kh = _heads(k, "k", shape)
-    vp, vt, vh = _heads(v, "v", shape)
+    kp, kt, kh = _heads(k, "k", shape, cache.k.device)
+    vp, vt, vh = _heads(v, "v", shape, cache.k.device)
     b, _, _, _ = _batch(cache, block_table, lens, cu_seqlens, max_new, T)
     if T > 0:
         _check(lib().fql_kv_append(cache._struct, b, kp, kt, kh, vp, vt, vh, _stream(k.device.index)))
@@ -352,12 +358,12 @@ def attention_kv8(q, cache, block_table, lens, cu_seqlens, max_new, causal=True,
     T, Hq, _ = q.shape
     D, dev = cache.head_dim, q.device
     shape = (T, Hq, D)
-    qp, qt, qh = _heads(q, "q", shape)
+    qp, qt, qh = _heads(q, "q", shape, cache.k.device)
     if out is None:
         out = torch.empty(shape, dtype=_bf16, device=dev)
         op, ot, oh = out.data_ptr(), Hq * D, D
     else:
-        op, ot, oh = _heads(out, "out", shape)
+        op, ot, oh = _heads(out, "out", shape, dev)
     lse, lp = None, 0
     if return_lse:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)

@@ -736,3 +736,46 @@ def test_side_stream_and_repeats_are_bitwise_equal():
         got = fql.attention_kv8(q, *args)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_expanded_tables_are_refused():
+    """Rows of stride 0 are not what the kernels step by."""
+    announce("expanded table")
+    cache = fql.KVCache8.empty(4, 1, 16, 64, DEV)
+    q, _ = bf16(np.zeros((2, 2, 64)))
+    k, _ = bf16(np.zeros((2, 1, 64)))
+    table, lens, cu = i32([[0, 1]]).expand(2, 2), i32([1, 1]), i32([0, 1, 2])
+    with pytest.raises(fql.FQLError, match="overlap"):
+        fql.attention_kv8(q, cache, table, lens, cu, 1)
+    with pytest.raises(fql.FQLError, match="overlap"):
+        fql.kv_append(cache, k, k, table, lens, cu, 1)
+    assert fql.attention_kv8(q, cache, table.contiguous(), lens, cu, 1).shape == (2, 2, 64)
+
+
+def test_a_graph_keeps_its_workspace_when_a_later_call_needs_a_larger_one():
+    announce("outgrown workspace")
+    rng = np.random.default_rng(4)
+    bs, H, D, Hq = 64, 2, 128, 8
+
+    def case(lens, blocks, max_len):
+        table = tables(rng, len(lens), max_len // bs, blocks, lens, bs, -1)
+        q, _ = bf16(rng.standard_normal((len(lens), Hq, D)))
+        return (q, to_device(random_cache(rng, blocks, H, bs, D)), i32(table), i32(lens), i32(range(len(lens) + 1)), 1)
+
+    small, large = case([900], 20, 1024), case([300 + 7 * i for i in range(40)], 400, 16384)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        want = fql.attention_kv8(*small)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got = fql.attention_kv8(*small)
+        key = ("cuda", 0, s.cuda_stream)
+        before = fql._workspaces[key]
+        fql._grow_workspace(key, 1, before.device)  # what a larger call does
+        assert fql._workspaces[key].numel() >= 2 * before.numel() and any(w is before for w in fql._outgrown)
+        for _ in range(4):
+            fql.attention_kv8(*large)
+            g.replay()
+            s.synchronize()
+            assert torch.equal(got, want)
