@@ -36,7 +36,7 @@ ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu":
 # structs of include/fql.h as packed bytes, sizes that depend on shapes alone
 # are remembered.
 _stream = torch._C._cuda_getCurrentRawStream  # device index -> hipStream_t of torch's current stream
-_bf16, _u8, _i32 = torch.bfloat16, torch.uint8, torch.int32
+_bf16, _u8, _i32, _f32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
 _query = functools.lru_cache(4096)(_size_query)
 
 
@@ -47,6 +47,15 @@ def _workspace(device, nbytes):
     if ws is None or ws.numel() < nbytes:
         ws = _grow_workspace(key, nbytes, device)
     return ws
+
+
+def _new(shape, dtype, dev):
+    """torch.empty of a contiguous tensor, a microsecond sooner for two dimensions (given as a
+    torch.Size, it takes 2.2 us; so, 1.3)."""
+    if len(shape) == 2:
+        M, n = shape
+        return torch.empty_strided((M, n), (n, 1), dtype=dtype, device=dev)
+    return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _format(fmt):
@@ -114,7 +123,7 @@ class QuantizedActivation:
 def _new_operand(x, fmt, scale):
     K = x.shape[-1]
     q = QuantizedActivation(None, fmt, x.shape[:-1], K, scale if fmt == "fp8" else None)
-    q.data = torch.empty(_query("fql_operand_bytes", _format(fmt), q.M, K), dtype=_u8, device=x.device)
+    q.data = torch.empty_strided((_query("fql_operand_bytes", _format(fmt), q.M, K),), (1,), dtype=_u8, device=x.device)
     return q
 
 
@@ -128,7 +137,7 @@ def _norm_args(x, weight, residual, residual_out):
         return xp, M, K, ld, 0, 0, wp, None, 0, 0
     rp, _, _, ldr = _rows(residual, "residual", x.shape)
     if residual_out is None:
-        h = torch.empty(x.shape, dtype=_bf16, device=x.device)
+        h = _new(x.shape, _bf16, x.device)
         return xp, M, K, ld, rp, ldr, wp, h, h.data_ptr(), K
     hp, _, _, ldh = _rows(residual_out, "residual_out", x.shape)
     return xp, M, K, ld, rp, ldr, wp, residual_out, hp, ldh
@@ -142,12 +151,12 @@ def rms_norm_quant(x, weight, fmt, eps=1e-6, residual=None, scale=None, residual
     f = _format(fmt)
     xp, M, K, ld, rp, ldr, wp, h, hp, ldh = _norm_args(x, weight, residual, residual_out)
     dev = x.device
-    codes = torch.empty(x.shape, dtype=_u8, device=dev)
+    codes = _new(x.shape, _u8, dev)
     scales, sp = None, 0
     if fmt == "mxfp8":
-        scales = torch.empty(x.shape[:-1] + (K // 32,), dtype=_u8, device=dev)
+        scales = _new(x.shape[:-1] + (K // 32,), _u8, dev)
     elif fmt == "fp8_block":
-        scales = torch.empty(x.shape[:-1] + (K // 128,), dtype=torch.float32, device=dev)
+        scales = _new(x.shape[:-1] + (K // 128,), _f32, dev)
     if scales is not None:
         sp = scales.data_ptr()
     _check(lib().fql_rms_norm_quant(f, xp, M, K, ld, rp, ldr, wp, eps, _scale_arg(fmt, scale), codes.data_ptr(), sp,
@@ -227,7 +236,7 @@ def linear_fused(x, weight, activation=None, bias=None, residual=None, alpha=Non
     No = N // 2 if activation == "swiglu" else N
     shape = lead + (No,)
     if out is None:
-        out = torch.empty(shape, dtype=_bf16, device=dev)
+        out = _new(shape, _bf16, dev)
         yp, ldy = out.data_ptr(), No
     else:
         yp, _, _, ldy = _rows(out, "out", shape)
@@ -360,13 +369,13 @@ def attention_kv8(q, cache, block_table, lens, cu_seqlens, max_new, causal=True,
     shape = (T, Hq, D)
     qp, qt, qh = _heads(q, "q", shape, cache.k.device)
     if out is None:
-        out = torch.empty(shape, dtype=_bf16, device=dev)
+        out = torch.empty_strided(shape, (Hq * D, D, 1), dtype=_bf16, device=dev)
         op, ot, oh = out.data_ptr(), Hq * D, D
     else:
         op, ot, oh = _heads(out, "out", shape, dev)
     lse, lp = None, 0
     if return_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = _new((T, Hq), _f32, dev)
         lp = lse.data_ptr()
     b, B, cols, new = _batch(cache, block_table, lens, cu_seqlens, max_new, T)
     if T > 0:
