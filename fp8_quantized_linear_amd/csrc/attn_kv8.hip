@@ -323,13 +323,18 @@ __device__ void put_nan_rows(const AttnArgs& a, const PagedCache& c, const Paged
 //
 // NC tiles of 16 rows; the W waves of a workgroup (eight where their registers
 // allow it: the more, the fewer ranges have to be joined across workgroups)
-// take 64-token tiles in turn and keep their own running maximum, sum and output, joined through LDS
-// at the end. The call is a stream over the cache: codes go straight from
-// memory into registers (16-byte loads; keys: a lane's 16 bytes of 4
-// neighbouring lanes make 64 bytes of a row, values: 256-byte runs), the next
-// tile's keys are loaded while this tile's weights and values are worked on
-// and the other way round, so about one tile of keys or values per wave is
-// always in flight and no barrier is in the loop.
+// take 64-token tiles in turn and keep their own running maximum, sum and
+// output, joined through LDS at the end. The call is a stream over the cache:
+// codes go straight from memory into registers (16-byte loads; keys: a lane's
+// 16 bytes of 4 neighbouring lanes make 64 bytes of a row, values: 256-byte
+// runs), the next tile's keys are loaded while this tile's weights and values
+// are worked on and the other way round, so about one tile of keys or values
+// per wave is always in flight and no barrier is in the loop.
+//
+// Bound by memory: 64 sequences of up to 16384 tokens, 64 query and 8 kv heads
+// of 128 channels: 1.34 GB in 257 us, 5.2 TB/s (a large copy: 5.0). One
+// sequence of 1000 tokens is a chain of dependent accesses (lengths, table,
+// keys, values, partial results, arrival, join): 8.9 us for 2 MB.
 //
 // v_mfma_f32_16x16x32_bf16: A lane l holds row l % 16, k = 8 (l / 16) + j;
 // B column l % 16, the same k; the result column l % 16, rows 4 (l / 16) + i.
@@ -617,6 +622,16 @@ __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kern
 // The running maximum moves only when a tile exceeds it by more than 2^8 (the
 // weights then stay below 2^8, which costs no precision): the accumulators
 // are rescaled a few times a row instead of at every tile.
+//
+// Bound by the issue of vector instructions beside the matrix ones: a wave's 32
+// products of a tile take 1024 cycles, its 32 exponentials 512 and the rest of
+// the softmax, widening and addressing 500 to 740. 8192 causal tokens, 32 query
+// and 8 kv heads of 128 channels: 570 us, 965 TFLOP/s (a large bf16 matrix
+// product: 1140); four prompts of up to 2048 tokens 99 us, 725 TFLOP/s, the
+// starts and ends of their short workgroups being the rest; head_dim 64 630
+// TFLOP/s (per product the softmax weighs twice), 256 565 (one workgroup a CU).
+// Tried at this size and slower: scales folded into the widening (640 us), the
+// softmax interleaved with the products by hand, waves with raised priority.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kernel(
     const AttnArgs a, const PagedCache c, const PagedBatch pb, int bs_shift, int row_tiles, int splits, int chunk,
@@ -628,7 +643,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
   static_assert(KP >= 1 && 4 * D % T == 0 && T % D == 0 && D % 64 == 0, "a wave's pieces in one group");
   __shared__ uint4v sk[2][64 * KC];
   __shared__ uint4v sv[2][D * 8];
-  __shared__ float4v ss[2][4];  // per group of 16 tokens: score factor (-1: no block), see stage_tile
+  __shared__ float4v ss[2][4];  // per group of 16 tokens: score factor (-1: no block), see stage_scales
   __shared__ uint32_t s_flag, s_nan;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);

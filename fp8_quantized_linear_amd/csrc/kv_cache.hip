@@ -146,6 +146,8 @@ __device__ __forceinline__ uint64_t codes8(const float f[8], int e) {
 
 // Few new tokens a sequence (decode): nothing is kept between the maximum and
 // the codes, and one or a few waves do a block.
+// Its time is its chain of dependent accesses (lengths, table, tokens, scale,
+// group): 64 sequences x 8 heads x 128 channels, one token each, 5.5 us for 0.4 MB.
 __global__ __launch_bounds__(256) void kv_append_kernel(const PagedCache c, const PagedBatch pb,
                                                         const uint16_t* __restrict__ k,
                                                         const uint16_t* __restrict__ v, int64_t k_ldt,
@@ -215,6 +217,10 @@ __device__ __forceinline__ uint32_t quad_xor1(uint32_t v) { return __builtin_amd
 // 4 q .. 4 q + 3 of a group of 16, packs each channel's four codes into a
 // word, and a transposition within the quad leaves it channels 8 d8 + 2 q and
 // + 1 with all 16 tokens: 32 contiguous bytes of the cache.
+// Five prompts of up to 2500 tokens (8 heads, 128 channels, 52 MB): 16.5 us, 3.1
+// TB/s, 28 us when a workgroup read its block twice and wrote values byte by
+// byte. A workgroup's chain (lengths, table, tokens, maximum, scale) is exposed
+// in part: there are 6.5 of them a CU at that size.
 template <int R>
 __global__ __launch_bounds__(256) void kv_append_block_kernel(const PagedCache c, const PagedBatch pb,
                                                               const uint16_t* __restrict__ k,

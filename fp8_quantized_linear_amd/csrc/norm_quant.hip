@@ -27,22 +27,23 @@ namespace {
 struct Vec8 {
   float v[8];
 };
-__device__ __forceinline__ Vec8 load8(const uint16_t* p, bool aligned) {
+__device__ __forceinline__ uint4v load_raw8(const uint16_t* p, bool aligned) {
+  if (aligned) return *reinterpret_cast<const uint4v*>(p);
+  uint4v u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) u[j] = (uint32_t)p[2 * j] | ((uint32_t)p[2 * j + 1] << 16);
+  return u;
+}
+__device__ __forceinline__ Vec8 widen(const uint4v& u) {
   Vec8 r;
-  if (aligned) {
-    const uint4v u = *reinterpret_cast<const uint4v*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      r.v[2 * j] = __uint_as_float(w[j] << 16);
-      r.v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r.v[j] = bf16_bits_to_f32(p[j]);
+  for (int j = 0; j < 4; ++j) {
+    r.v[2 * j] = __uint_as_float(u[j] << 16);
+    r.v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
   }
   return r;
 }
+__device__ __forceinline__ Vec8 load8(const uint16_t* p, bool aligned) { return widen(load_raw8(p, aligned)); }
 __device__ __forceinline__ void store8(uint16_t* p, const Vec8& r, bool aligned) {
   if (aligned) {
     uint4v u;
@@ -163,19 +164,15 @@ __device__ __forceinline__ Vec8 load_h(const NormArgs& a, const NormFlags& f, in
   return h;
 }
 
+// h and the weight are zeros past the row.
 template <int F, bool OP>
-__device__ __forceinline__ void finish_vec(const NormArgs& a, const NormFlags& f, int64_t m, int64_t v, int64_t nv,
-                                           int64_t nvp, const Vec8& h, double rinv) {
+__device__ __forceinline__ void finish_vec(const NormArgs& a, int64_t m, int64_t v, int64_t nv, int64_t nvp,
+                                           const Vec8& h, const Vec8& w, double rinv) {
 #pragma clang fp contract(off)
-  Vec8 y, w;
+  Vec8 y;
   const float r = (float)rinv;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) y.v[j] = w.v[j] = 0.0f;
-  if (v < nv) {
-    w = load8(a.weight + 8 * v, f.w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) y.v[j] = h.v[j] * r * w.v[j];
-  }
+  for (int j = 0; j < 8; ++j) y.v[j] = v < nv ? h.v[j] * r * w.v[j] : 0.0f;
   uint32_t q[2], sb = 0;
   float gs = 0.0f, factor;
   quant_block8<F>(y, a.inv_scale, q, sb, gs, factor);
@@ -187,6 +184,12 @@ __device__ __forceinline__ void finish_vec(const NormArgs& a, const NormFlags& f
 // One row per workgroup (WAVE: per wave, four rows a workgroup), its values in
 // registers: vector v = t + T * i of thread t (T threads a row, I vectors a
 // thread). STREAM: rows too long for that read x and the residual twice.
+//
+// Bound by memory where there are many rows: 8192 x 5120 block FP8 with a
+// residual moves 294 MB in 58 us, 5.1 TB/s, what a large copy reaches. Few rows
+// are one dependent chain (load, reduce, barrier, encode): one row of 4096 takes
+// 3.7 us, 333 x 5120 MXFP8 7.1 us (1.7 TB/s; two vectors a thread, so that one
+// row's chain is short and its loads are all in flight at once).
 template <int F, bool OP, int I, bool WAVE, bool STREAM>
 __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, const NormFlags f) {
   __shared__ std::conditional_t<F == SC_FP8_BLOCK, float, double> red[16];
@@ -209,6 +212,12 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
     if (m >= a.M) return;
   }
   const int64_t nv = a.K / 8, nvp = OP ? (a.K + 127) / 128 * 16 : nv;
+  // the weight's loads run beside the sum of squares where registers allow it
+  // (an access less in the chain: 8 x 4096 FP8 5.8 -> 5.4 us, 8192 x 5120 block
+  // FP8 59.4 -> 58.3)
+  constexpr bool EARLY = !STREAM && I <= 4;
+  auto load_w = [&](int64_t v) { return v < nv ? load_raw8(a.weight + 8 * v, f.w) : uint4v{0u, 0u, 0u, 0u}; };
+  uint4v w[EARLY ? I : 1];
   Vec8 h[I];
   // float32 where the codes are those of a float32 y (float64 takes 8192 x 5120
   // block FP8 from 58 to 60 us)
@@ -218,6 +227,7 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int64_t v = t + (int64_t)T * i;
+      if (EARLY) w[i] = load_w(v);
       if (v < nv) h[i] = load_h(a, f, m, v, true);
       else
 #pragma unroll
@@ -247,7 +257,8 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       // whole groups of T vectors, so that every lane of a block takes part
-      if ((int64_t)T * i < nvp) finish_vec<F, OP>(a, f, m, t + (int64_t)T * i, nv, nvp, h[i], rinv);
+      const int64_t v = t + (int64_t)T * i;
+      if ((int64_t)T * i < nvp) finish_vec<F, OP>(a, m, v, nv, nvp, h[i], widen(EARLY ? w[i] : load_w(v)), rinv);
     }
   } else {
     for (int64_t v0 = 0; v0 < nvp; v0 += T) {
@@ -256,7 +267,7 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
 #pragma unroll
       for (int j = 0; j < 8; ++j) u.v[j] = 0.0f;
       if (v < nv) u = load_h(a, f, m, v, true);
-      finish_vec<F, OP>(a, f, m, v, nv, nvp, u, rinv);
+      finish_vec<F, OP>(a, m, v, nv, nvp, u, widen(load_w(v)), rinv);
     }
   }
 }
@@ -291,6 +302,7 @@ hipError_t launch_t(const NormArgs& a, hipStream_t st) {
 // store instruction fills whole runs; with a row's blocks in neighbouring
 // lanes (the standalone quantizer's order) they are 16-byte pieces 256 bytes
 // apart. The block arithmetic is quant_block32's. Rows past M are not written.
+// 4096 x 4096 MXFP8: 10 us, 4.9 TB/s (15.9 us in the quantizer's order).
 template <int F>
 __global__ __launch_bounds__(256) void quant_operand_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                             int64_t ldx, bool aligned, float inv_scale, int64_t KC,

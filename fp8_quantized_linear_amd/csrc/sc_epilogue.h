@@ -9,6 +9,8 @@
 //              and their 16 up columns, so a lane's accumulators of column
 //              tiles 2j and 2j + 1 are one output's pair and nothing has to
 //              move between lanes.
+// What it costs: 4096 x 4096 x 14336 MXFP8 with bias and tanh-GELU 234 us a
+// product (2.06 PFLOP/s) against 225 without either.
 #pragma once
 
 #include "fql_gemm.h"
