@@ -71,18 +71,6 @@ __device__ __forceinline__ Row row_of(const AttnArgs& a, int row) {
   return Row{t, row - t * a.group};
 }
 
-// The keys the rows of a new token see: [lo, hi).
-struct Visible {
-  int lo, hi;
-};
-__device__ __forceinline__ Visible visible_of(const SeqSpan& s, int token, int causal, int window) {
-  const int p = s.pos0 + token;
-  Visible v;
-  v.hi = causal ? (p + 1 < s.len ? p + 1 : s.len) : s.len;
-  v.lo = window > 0 && p - window + 1 > 0 ? p - window + 1 : 0;
-  return v;
-}
-
 __device__ __forceinline__ int clamp16(int v) { return v < 0 ? 0 : (v > 16 ? 16 : v); }
 
 // A lane's 16-token pieces of VT channels: tokens skip .. have - 1 stay, the
@@ -307,7 +295,7 @@ __device__ void put_nan_rows(const AttnArgs& a, const PagedCache& c, const Paged
       for (int d = threadIdx.x; d < D; d += blockDim.x) {
         if ((v[d * 16] & 0x7F) != 0x7F) continue;
         for (int r = 0; r < nrows; ++r) {
-          const Visible w = visible_of(s, row_of(a, row0 + r).token, a.causal, a.window);
+          const Visible w = visible_keys(s, row_of(a, row0 + r).token, a.causal, a.window);
           if (t < w.lo || t >= w.hi) continue;
           if (part != nullptr) part->put_nan(r, d);
           else out_row(a, s, h, row0 + r).p[d] = 0x7FC0;
@@ -366,8 +354,8 @@ __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kern
   if (row0 >= rows) return;
   const int last_row = row0 + 16 * NC < rows ? row0 + 16 * NC - 1 : rows - 1;
   // every row sees [last.lo, first.hi), some row each of [first.lo, last.hi)
-  const Visible first = visible_of(s, row_of(a, row0).token, a.causal, a.window);
-  const Visible last = visible_of(s, row_of(a, last_row).token, a.causal, a.window);
+  const Visible first = visible_keys(s, row_of(a, row0).token, a.causal, a.window);
+  const Visible last = visible_keys(s, row_of(a, last_row).token, a.causal, a.window);
   const int kmin = first.lo & ~63, kmax = last.hi;
   int ns = 1;
   if (splits > 1) {
@@ -389,7 +377,7 @@ __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kern
     const int row = row0 + 16 * t + col;
     const bool ok = row < rows;
     const Row rw = row_of(a, ok ? row : 0);
-    const Visible v = visible_of(s, rw.token, a.causal, a.window);
+    const Visible v = visible_keys(s, rw.token, a.causal, a.window);
     vlo[t] = v.lo;
     vhi[t] = ok ? v.hi : 0;
     const uint16_t* qp = a.q + (s.row0 + rw.token) * a.q_ld_token + (int64_t)(h * a.group + rw.head) * a.q_ld_head;
@@ -667,8 +655,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
   const int rows = s.n * a.group, row0 = rt * ROWS;
   if (row0 >= rows) return;
   const int last_row = row0 + ROWS < rows ? row0 + ROWS - 1 : rows - 1;
-  const Visible first = visible_of(s, row_of(a, row0).token, a.causal, a.window);
-  const Visible last = visible_of(s, row_of(a, last_row).token, a.causal, a.window);
+  const Visible first = visible_keys(s, row_of(a, row0).token, a.causal, a.window);
+  const Visible last = visible_keys(s, row_of(a, last_row).token, a.causal, a.window);
   const int kmin = first.lo & ~63, kmax = last.hi;
   int ns = 1;
   if (splits > 1) {
@@ -685,11 +673,11 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
   const int wrow = row0 + 32 * wave, row = wrow + col;
   const bool ok = row < rows;
   const Row rw = row_of(a, ok ? row : 0);
-  const Visible mine = visible_of(s, rw.token, a.causal, a.window);
+  const Visible mine = visible_keys(s, rw.token, a.causal, a.window);
   const int vlo = mine.lo, vhi = ok ? mine.hi : 0;
-  const Visible wave_last = visible_of(s, row_of(a, wrow + 31 < rows ? wrow + 31 : rows - 1).token, a.causal, a.window);
+  const Visible wave_last = visible_keys(s, row_of(a, wrow + 31 < rows ? wrow + 31 : rows - 1).token, a.causal, a.window);
   const int wave_all_lo = wave_last.lo;
-  const int wave_all_hi = visible_of(s, row_of(a, wrow < rows ? wrow : rows - 1).token, a.causal, a.window).hi;
+  const int wave_all_hi = visible_keys(s, row_of(a, wrow < rows ? wrow : rows - 1).token, a.causal, a.window).hi;
   const int wave_any_hi = wrow < rows ? wave_last.hi : 0;
   bf16x8 q[SK];
   {

@@ -100,7 +100,7 @@ struct SeqSpan {
   int len;       // tokens with the new ones (at most the table's capacity)
   int pos0;      // position of its first new token (negative when lens[b] < n)
 };
-__device__ __forceinline__ SeqSpan seq_span(const PagedBatch& pb, int b, int block_size) {
+__host__ __device__ __forceinline__ SeqSpan seq_span(const PagedBatch& pb, int b, int block_size) {
   SeqSpan s;
   int64_t c0 = pb.cu[b], c1 = pb.cu[b + 1];
   c0 = c0 < 0 ? 0 : (c0 > pb.T ? pb.T : c0);
@@ -113,6 +113,19 @@ __device__ __forceinline__ SeqSpan seq_span(const PagedBatch& pb, int b, int blo
   s.pos0 = (int)((len < 0 ? 0 : len) - n);
   s.len = (int)(len < 0 ? 0 : (len < cap ? len : cap));
   return s;
+}
+
+// The keys that the rows of a sequence's new token see: [lo, hi), empty where
+// hi <= lo (hi may be negative).
+struct Visible {
+  int lo, hi;
+};
+__host__ __device__ __forceinline__ Visible visible_keys(const SeqSpan& s, int token, int causal, int window) {
+  const int p = s.pos0 + token;
+  Visible v;
+  v.hi = causal ? (p + 1 < s.len ? p + 1 : s.len) : s.len;
+  v.lo = window > 0 && p >= window ? p - window + 1 : 0;
+  return v;
 }
 #endif
 

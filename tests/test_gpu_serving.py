@@ -779,3 +779,10 @@ def test_a_graph_keeps_its_workspace_when_a_later_call_needs_a_larger_one():
             g.replay()
             s.synchronize()
             assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("new", [5, 90])
+def test_attention_window_wider_than_any_position(new):
+    """The widest window hides nothing, also from a batch with more new tokens than its length."""
+    out, lse, ref = attention_case([13, new], [new, 3], [new - 3, 60], 4, 2, 64, 16, window=2 ** 31 - 1)
+    assert_attention(out, lse, ref, "wide window")
