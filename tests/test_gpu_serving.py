@@ -786,3 +786,30 @@ def test_attention_window_wider_than_any_position(new):
     """The widest window hides nothing, also from a batch with more new tokens than its length."""
     out, lse, ref = attention_case([13, new], [new, 3], [new - 3, 60], 4, 2, 64, 16, window=2 ** 31 - 1)
     assert_attention(out, lse, ref, "wide window")
+
+
+@pytest.mark.parametrize("new", [1, 70])
+def test_caches_past_32_bits_of_offset(new):
+    """Blocks beyond 4 GiB of keys hold and give what the same blocks of a small cache do."""
+    announce(f"large cache new={new}")
+    bs, H, D, Hq, blocks = 256, 8, 256, 16, 8200  # 4.3 GB of keys and of values each
+    lens = [300, 700]
+    rng = np.random.default_rng([14, new])
+    small = fql.KVCache8.empty(8, H, bs, D, DEV)
+    k = torch.empty((blocks, H, bs, D), dtype=torch.uint8, device=DEV)
+    v = torch.empty((blocks, H, bs // 16, D, 16), dtype=torch.uint8, device=DEV)
+    s = torch.zeros((2, blocks, H), dtype=torch.uint8, device=DEV)
+    assert k.numel() > 2 ** 32
+    large = fql.KVCache8(k, v, s[0], s[1])
+    t_small = i32([[0, 1, 2], [3, 4, 5]])
+    kv = [bf16(rng.standard_normal((sum(lens), H, D)))[0] for _ in range(2)]
+    q, _ = bf16(rng.standard_normal((2 * new, Hq, D)))
+    outs = []
+    for cache, table in ((small, t_small), (large, t_small + (blocks - 8))):
+        fql.kv_append(cache, *kv, table, i32(lens), i32([0, lens[0], sum(lens)]), max(lens))
+        outs.append(fql.attention_kv8(q, cache, table, i32(lens), i32([0, new, 2 * new]), new))
+    assert torch.equal(outs[0], outs[1])
+    for i in (0, 3, 4):  # the blocks that are written whole
+        assert torch.equal(large.k[i - 8], small.k[i]) and torch.equal(large.v[i - 8], small.v[i])
+    for i in range(5):
+        assert i == 2 or torch.equal(large.v_scale[i - 8], small.v_scale[i])
