@@ -955,23 +955,27 @@ AttnPlan plan_attention(int B, int Hq, int Hkv, int D, int64_t max_new, int64_t 
   // Ranges of keys. Every workgroup pays its start (about as long as one step
   // of 64 tokens a wave) and a call with several ranges their joining, so the
   // ranges are as few as fill the card: the count with the least rounds *
-  // (steps + 1) + joining, a round being the workgroups that run at once
-  // (MI355X sweep over 1 .. 512 ranges: one sequence of 131072 tokens and 8 kv
-  // heads 57 us with 32 ranges, 77 with 16, 63 with 64; eight of up to 4096
-  // tokens 18.5 us with 4, 22 with 2, 23 with 8).
+  // (steps + 1) + joining, a round being the workgroups that run at once. A
+  // last step that not all waves take counts by its share, down to a half
+  // (MI355X sweeps, 8 kv heads: 131072 tokens 57 us with 32 ranges, 77 with 16,
+  // 63 with 64; 2000 tokens 9.7 us with 8, 10.1 with 4, 12.4 with 2; 1000 tokens
+  // 9.0 with 4, 9.6 with 2, 9.3 with 8; eight sequences of up to 4096 tokens
+  // 18.5 us with 4, 22 with 2, 23 with 8).
   int64_t splits = 1;
   if (p.kind == 0) {
-    const int waves = stream_waves(D, p.cols);
+    const int step = 64 * stream_waves(D, p.cols);
     const int64_t slots = D == 64 && p.cols == 1 ? 512 : 256;
     double best = 0.0;
     for (int64_t s = 1; s <= 64; ++s) {
-      const int64_t steps = (span + s * 64 * waves - 1) / (s * 64 * waves);
-      const double cost = (double)((tiles * s + slots - 1) / slots) * (double)(steps + 1) +
+      const int64_t keys = (span + s - 1) / s;
+      const double steps = keys <= step / 2 ? 0.5 : (double)keys / step;
+      const double cost = (double)((tiles * s + slots - 1) / slots) * (steps + 1.0) +
                           (s > 1 ? 0.75 + (double)s * (double)std::min<int64_t>(rows, rows_of(p)) / 512.0 : 0.0);
       if (s == 1 || cost < best) {
         best = cost;
         splits = s;
       }
+      if (keys <= step / 2) break;  // more ranges only cost more
     }
   } else {
     // many rows: four rounds of workgroups (sequences differ in length), of at

@@ -1101,7 +1101,8 @@ int check_cache(const fql_kv_cache* c, const fql_kv_batch* b, fql::PagedCache* p
   return FQL_OK;
 }
 
-int check_attention(int batch, int Hq, int Hkv, int D, int64_t max_new, int64_t max_len, int window) {
+// The checks of an attention call and, passed, its plan.
+int check_attention(int batch, int Hq, int Hkv, int D, int64_t max_new, int64_t max_len, int window, fql::AttnPlan* plan) {
   if (batch < 1 || Hkv < 1 || Hkv > 4096 || Hq < Hkv || Hq % Hkv != 0 || Hq > 1 << 20)
     return fail(FQL_ERR_INVALID, "q_heads must be a positive multiple of kv_heads (got %d, %d)", Hq, Hkv);
   if (D != 64 && D != 128 && D != 256) return fail(FQL_ERR_UNSUPPORTED, "head_dim must be 64, 128 or 256 (got %d)", D);
@@ -1109,8 +1110,8 @@ int check_attention(int batch, int Hq, int Hkv, int D, int64_t max_new, int64_t 
   if (max_new < 0 || max_new > 1 << 24) return fail(FQL_ERR_INVALID, "max_new must be in 0 .. 2^24");
   if (max_len < 1 || max_len > (int64_t)1 << 30) return fail(FQL_ERR_INVALID, "max_len must be in 1 .. 2^30");
   if (window < 0) return fail(FQL_ERR_INVALID, "window must be >= 0");
-  const fql::AttnPlan p = fql::plan_attention(batch, Hq, Hkv, D, max_new, max_len, window);
-  if (max_new * (Hq / Hkv) > (int64_t)1 << 30 || (int64_t)p.row_tiles * p.splits > 65535)
+  *plan = fql::plan_attention(batch, Hq, Hkv, D, max_new, max_len, window);
+  if (max_new * (Hq / Hkv) > (int64_t)1 << 30 || (int64_t)plan->row_tiles * plan->splits > 65535)
     return fail(FQL_ERR_UNSUPPORTED, "too many query rows in one call");
   return FQL_OK;
 }
@@ -1252,8 +1253,9 @@ int fql_attention_kv8_workspace_bytes(int batch, int q_heads, int kv_heads, int 
                                       int64_t max_len, int window, size_t* bytes) {
   return guarded([&] {
     if (!bytes) return fail(FQL_ERR_INVALID, "null pointer");
-    if (int r = check_attention(batch, q_heads, kv_heads, head_dim, max_new, max_len, window)) return r;
-    *bytes = (size_t)fql::plan_attention(batch, q_heads, kv_heads, head_dim, max_new, max_len, window).total_bytes;
+    fql::AttnPlan plan;
+    if (int r = check_attention(batch, q_heads, kv_heads, head_dim, max_new, max_len, window, &plan)) return r;
+    *bytes = (size_t)plan.total_bytes;
     return ok();
   });
 }
@@ -1261,10 +1263,9 @@ int fql_attention_kv8_workspace_bytes(int batch, int q_heads, int kv_heads, int 
 int fql_attention_kv8_describe(int batch, int q_heads, int kv_heads, int head_dim, int64_t max_new, int64_t max_len,
                                int window, char* buf, size_t buf_len) {
   return guarded([&] {
-    if (int r = check_attention(batch, q_heads, kv_heads, head_dim, max_new, max_len, window)) return r;
-    write_reason(buf, buf_len,
-                 fql::describe_attention(
-                     fql::plan_attention(batch, q_heads, kv_heads, head_dim, max_new, max_len, window), head_dim));
+    fql::AttnPlan plan;
+    if (int r = check_attention(batch, q_heads, kv_heads, head_dim, max_new, max_len, window, &plan)) return r;
+    write_reason(buf, buf_len, fql::describe_attention(plan, head_dim));
     return ok();
   });
 }
@@ -1277,13 +1278,13 @@ int fql_attention_kv8(const fql_kv_cache* cache, const fql_kv_batch* batch, cons
     fql::PagedCache c;
     fql::PagedBatch b;
     if (int r = check_cache(cache, batch, &c, &b)) return r;
-    if (int r = check_attention(b.B, q_heads, c.heads, c.D, b.max_new, max_len, window)) return r;
+    fql::AttnPlan plan;
+    if (int r = check_attention(b.B, q_heads, c.heads, c.D, b.max_new, max_len, window, &plan)) return r;
     if (!q || !out || !workspace) return fail(FQL_ERR_INVALID, "null pointer");
     if (q_ld_token < 0 || q_ld_head < 0 || o_ld_token < 0 || o_ld_head < 0) return fail(FQL_ERR_INVALID, "negative stride");
     if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(FQL_ERR_INVALID, "scale must be finite and > 0");
     if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return fail(FQL_ERR_INVALID, "workspace must be 256-byte aligned");
     if (b.T == 0 || b.max_new == 0) return ok();
-    const fql::AttnPlan plan = fql::plan_attention(b.B, q_heads, c.heads, c.D, b.max_new, max_len, window);
     if (workspace_bytes < (size_t)plan.total_bytes)
       return fail(FQL_ERR_WORKSPACE, "workspace holds %zu bytes, %lld needed", workspace_bytes, (long long)plan.total_bytes);
     fql::AttnArgs a{};

@@ -42,7 +42,8 @@ _query = functools.lru_cache(4096)(_size_query)
 
 def _workspace(device, nbytes):
     """The binding's workspace of this device and stream (shared with the linear calls)."""
-    key = (device.type, device.index, _stream(device.index))
+    index = device.index
+    key = ("cuda", index, _stream(index))
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = _grow_workspace(key, nbytes, device)
@@ -278,6 +279,7 @@ class KVCache8:
         if not tuple(k_scale.shape) == tuple(v_scale.shape) == (self.num_blocks, self.kv_heads):
             raise FQLError("scales must be [blocks, kv_heads]")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._index = k.get_device()
         self._struct = struct.pack("PPPPqiii4x", k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                    self.num_blocks, self.kv_heads, self.block_size, self.head_dim)  # fql_kv_cache
 
@@ -290,10 +292,10 @@ class KVCache8:
         return cls(k, v, s[0], s[1])
 
 
-def _heads(t, name, shape, dev):
+def _heads(t, name, shape, index):
     """(address, token stride, head stride) of a bf16 [tokens, heads, head_dim] tensor on the cache's device."""
-    _cuda(t, name, _bf16)
-    if t.device != dev:
+    if not isinstance(t, torch.Tensor) or t.dtype is not _bf16 or t.get_device() != index:
+        _cuda(t, name, _bf16)
         raise FQLError(f"{name} must be on the cache's device")
     if t.shape != shape:
         raise FQLError(f"{name} must have shape {shape}")
@@ -303,13 +305,18 @@ def _heads(t, name, shape, dev):
     return t.data_ptr(), ld_token, ld_head
 
 
+def _is_i32(t, index):
+    return isinstance(t, torch.Tensor) and t.dtype is _i32 and t.get_device() == index
+
+
 def _batch(cache, block_table, lens, cu_seqlens, max_new, tokens):
     """A packed fql_kv_batch, the batch size and its bound of new tokens."""
-    dev = cache.k.device
-    for t, name in ((block_table, "block_table"), (lens, "lens"), (cu_seqlens, "cu_seqlens")):
-        _cuda(t, name, _i32)
-        if t.device != dev:
-            raise FQLError(f"{name} must be on the cache's device")
+    index = cache._index
+    if not (_is_i32(block_table, index) and _is_i32(lens, index) and _is_i32(cu_seqlens, index)):
+        for t, name in ((block_table, "block_table"), (lens, "lens"), (cu_seqlens, "cu_seqlens")):
+            _cuda(t, name, _i32)
+            if t.get_device() != index:
+                raise FQLError(f"{name} must be on the cache's device")
     if lens.dim() != 1 or cu_seqlens.dim() != 1 or block_table.dim() != 2:
         raise FQLError("block_table must be [batch, columns], lens [batch], cu_seqlens [batch + 1]")
     B = lens.shape[0]
@@ -340,11 +347,11 @@ def kv_append(cache, k, v, block_table, lens, cu_seqlens, max_new):
         raise FQLError("k must be a tensor [tokens, kv_heads, head_dim]")
     T = k.shape[0]
     shape = (T, cache.kv_heads, cache.head_dim)
-    kp, kt, kh = _heads(k, "k", shape, cache.k.device)
-    vp, vt, vh = _heads(v, "v", shape, cache.k.device)
+    kp, kt, kh = _heads(k, "k", shape, cache._index)
+    vp, vt, vh = _heads(v, "v", shape, cache._index)
     b, _, _, _ = _batch(cache, block_table, lens, cu_seqlens, max_new, T)
     if T > 0:
-        _check(lib().fql_kv_append(cache._struct, b, kp, kt, kh, vp, vt, vh, _stream(k.device.index)))
+        _check(lib().fql_kv_append(cache._struct, b, kp, kt, kh, vp, vt, vh, _stream(cache._index)))
 
 
 def attention_kv8_plan(batch, q_heads, kv_heads, head_dim, max_new, max_len, window=0):
@@ -367,12 +374,12 @@ def attention_kv8(q, cache, block_table, lens, cu_seqlens, max_new, causal=True,
     T, Hq, _ = q.shape
     D, dev = cache.head_dim, q.device
     shape = (T, Hq, D)
-    qp, qt, qh = _heads(q, "q", shape, cache.k.device)
+    qp, qt, qh = _heads(q, "q", shape, cache._index)
     if out is None:
         out = torch.empty_strided(shape, (Hq * D, D, 1), dtype=_bf16, device=dev)
         op, ot, oh = out.data_ptr(), Hq * D, D
     else:
-        op, ot, oh = _heads(out, "out", shape, dev)
+        op, ot, oh = _heads(out, "out", shape, cache._index)
     lse, lp = None, 0
     if return_lse:
         lse = _new((T, Hq), _f32, dev)
@@ -386,5 +393,5 @@ def attention_kv8(q, cache, block_table, lens, cu_seqlens, max_new, causal=True,
                                                max_len, window))
         _check(lib().fql_attention_kv8(cache._struct, b, qp, qt, qh, Hq, D ** -0.5 if scale is None else scale,
                                        bool(causal), window, max_len, op, ot, oh, lp, workspace.data_ptr(),
-                                       workspace.numel(), _stream(dev.index)))
+                                       workspace.numel(), _stream(cache._index)))
     return (out, lse) if return_lse else out
