@@ -523,7 +523,10 @@ def _workspace(device, nbytes):
 
 def _grow_workspace(key, nbytes, device):
     """A new workspace for `key`, at least twice as large as the one it replaces: those are kept,
-    and so hold no more than the newest in all."""
+    and so hold no more than the newest in all. Under graph capture the workspace is the graph's
+    own, cleared by every replay, and no eager call ever sees it."""
+    if torch.cuda.is_current_stream_capturing():
+        return new_workspace(nbytes, device)
     old = _workspaces.get(key)
     if old is not None:
         nbytes = max(nbytes, 2 * old.numel())

@@ -813,3 +813,30 @@ def test_caches_past_32_bits_of_offset(new):
         assert torch.equal(large.k[i - 8], small.k[i]) and torch.equal(large.v[i - 8], small.v[i])
     for i in range(5):
         assert i == 2 or torch.equal(large.v_scale[i - 8], small.v_scale[i])
+
+
+def test_a_capture_without_a_call_before_it_leaves_eager_calls_alone():
+    announce("cold capture")
+    rng = np.random.default_rng(15)
+    lens = [4000, 900]
+    table = tables(rng, 2, 63, 90, lens, 64, -1)
+    q, _ = bf16(rng.standard_normal((2, 8, 128)))
+    args = (q, to_device(random_cache(rng, 90, 2, 64, 128)), i32(table), i32(lens), i32([0, 1, 2]), 1)
+    assert "splits=1" not in fql.attention_kv8_plan(2, 8, 2, 128, 1, 63 * 64).split()
+    want = fql.attention_kv8(*args)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    key = ("cuda", 0, s.cuda_stream)
+    fql._workspaces.pop(key, None)  # the stream may be one that an earlier test used
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        got = fql.attention_kv8(*args)
+    assert key not in fql._workspaces
+    with torch.cuda.stream(s):
+        assert torch.equal(fql.attention_kv8(*args), want)
+        for _ in range(4):
+            got.zero_()
+            g.replay()
+            s.synchronize()
+            assert torch.equal(got, want)
+            assert torch.equal(fql.attention_kv8(*args), want)
