@@ -994,14 +994,17 @@ ScPlan plan_sc_gemm(int fmt, int64_t M, int64_t N, int64_t K) {
 }
 
 // Plan of a fused-epilogue call. Where the plain plan fills the card with split
-// ranges of K, joining them costs more than it saves (sweep of every built tile
-// and 1 .. 8 ranges at M = 33 .. 2048 on six layers: 4096 x 4096 at M = 256
+// ranges of K, joining them costs more than it saves (4096 x 4096 at M = 256
 // 31.6 us with 128 x 128 tiles in four ranges, 12.5 with 64 x 64 tiles whole).
 // So the tile is chosen by time: rounds * (chunks * tc + f) + joining, in us,
-// with tc of one 128-deep chunk and f of a workgroup's start and epilogue as
-// the sweep gives them (8-bit formats: the two columns of `tiles` are MXFP8 and
-// per-tensor FP8, block FP8). The two smaller tiles fit twice into a CU's LDS;
-// two chunks then take `pair` times one.
+// with tc of one 128-deep chunk and f of a workgroup's start and epilogue (8-bit
+// formats: the two columns of `tiles` are MXFP8 and per-tensor FP8, block FP8).
+// The two smaller tiles fit twice into a CU's LDS; two chunks then take `pair`
+// times one. The constants are fitted to a sweep of every tile and 1 .. 4 ranges
+// at M = 40 .. 512 on five layers, weights from HBM: what they choose is 0.3%
+// slower than the best of the sweep on average, 11% at most (on seven other
+// layers at M = 48 .. 2048 between 5% slower and 21% faster than constants from
+// cached weights, 7% faster on average where the choice changed).
 ScPlan plan_sc_fused(int fmt, int64_t M, int64_t N, int64_t K) {
   const ScPlan plain = plan_sc_gemm(fmt, M, N, K);
   if (fmt == SC_MXFP4 || plain.kind == 1 || !plan_override(kOverrideScGemm).empty()) return plain;
@@ -1010,9 +1013,9 @@ ScPlan plan_sc_fused(int fmt, int64_t M, int64_t N, int64_t K) {
     double tc[2], f, pair;
   };
   static constexpr Tile tiles[] = {
-      {1, 4, 1, 2, 4, {0.22, 0.26}, 5.0, 1.6},  {2, 2, 2, 2, 4, {0.19, 0.30}, 6.3, 1.8},
-      {4, 2, 2, 2, 4, {0.31, 0.38}, 6.0, 0.0},  {2, 4, 4, 2, 4, {0.45, 0.60}, 9.0, 0.0},
-      {4, 2, 4, 4, 3, {0.80, 1.00}, 15.0, 0.0},
+      {1, 4, 1, 2, 4, {0.364, 0.404}, 2.99, 1.573}, {2, 2, 2, 2, 4, {0.259, 0.301}, 6.21, 1.832},
+      {4, 2, 2, 2, 4, {0.382, 0.413}, 5.75, 0.0},   {2, 4, 4, 2, 4, {0.525, 0.608}, 8.27, 0.0},
+      {4, 2, 4, 4, 3, {0.626, 0.744}, 15.35, 0.0},
   };
   const ScDims w = sc_dims(fmt, N, K, true);
   const Tile* best = nullptr;
@@ -1021,13 +1024,13 @@ ScPlan plan_sc_fused(int fmt, int64_t M, int64_t N, int64_t K) {
   for (const Tile& t : tiles) {
     const int64_t rows = 16 * t.wm * t.mtw, cols = 16 * t.wn * t.ntw;
     const int64_t groups = (round_up(M, rows) / rows) * (round_up(N, cols) / cols);
-    for (int64_t s = 1; s <= 8 && (s == 1 || (w.KC / s >= 8 && groups <= 16384)); ++s) {
+    for (int64_t s = 1; s <= 8 && (s == 1 || (w.KC / s >= 10 && groups <= 16384)); ++s) {
       const double chunks = (double)((w.KC + s - 1) / s), tc = t.tc[fmt == SC_FP8_BLOCK ? 1 : 0];
       const int64_t wgs = groups * s;
       double cost;
       if (wgs <= 256 || t.pair == 0.0) cost = (double)((wgs + 255) / 256) * (chunks * tc + t.f);
       else cost = (double)((wgs + 511) / 512) * (chunks * tc * t.pair + t.f);
-      if (s > 1) cost += 2.0 + (double)(rows * cols) / 256.0 * (0.035 * (double)s + 0.09);
+      if (s > 1) cost += 6.2 + 0.2 * (double)s + (double)(rows * cols) / 256.0 * (0.027 * (double)s + 0.072);
       if (best == nullptr || cost < best_cost) {
         best = &t;
         best_splits = s;
