@@ -740,13 +740,14 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
     bool absent = false;
 #pragma unroll
     for (int i = 0; i < KP; ++i) absent |= blk[i] < 0;
-    if (t0 + 64 > first.hi || t0 < last.lo || absent) {
+    const bool differ = t0 + 64 > first.hi || t0 < last.lo;  // put_nan_rows' condition
+    if (differ || absent) {
 #pragma unroll
       for (int i = 0; i < KP; ++i) {
         uint4v u[1] = {vw[i]};
         const int t = t0 + 16 * (g0 + GS * i);
         mask_values<1>(u, blk[i] < 0 ? 0 : clamp16(kmax - t), clamp16(first.lo - t));
-        if (drop_nan<1>(u)) s_nan = 1u;
+        if (differ && drop_nan<1>(u)) s_nan = 1u;
         vw[i] = u[0];
       }
     }
