@@ -609,7 +609,8 @@ __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kern
 //
 // The running maximum moves only when a tile exceeds it by more than 2^8 (the
 // weights then stay below 2^8, which costs no precision): the accumulators
-// are rescaled a few times a row instead of at every tile.
+// are rescaled a few times a row instead of at every tile. Tiles with a value
+// scale outside 2^+-100 move it at once.
 //
 // Bound by the issue of vector instructions beside the matrix ones: a wave's 32
 // products of a tile take 1024 cycles, its 32 exponentials 512 and the rest of
@@ -855,7 +856,9 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
       const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
       top = __builtin_fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
     }
-    if (__any(top > m + 8.0f)) {
+    // weights of up to 2^8 times a value scale above 2^100 could leave float32
+    const bool factor = __any(sc[0][3] != 1.0f || sc[1][3] != 1.0f);
+    if (__any(top > (factor ? m : m + 8.0f))) {
       top = __builtin_fmaxf(top, m);
       const float back = exp2_fast(m - (top == neg_inf() ? 0.0f : top));
       l *= back;
@@ -864,7 +867,6 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_kv8_tile_kerne
       m = top;
     }
     const float safe = m == neg_inf() ? 0.0f : m;
-    const bool factor = __any(sc[0][3] != 1.0f || sc[1][3] != 1.0f);
     trim_values(t0 + 64);
     bf16x8 p[2][2];
 #pragma unroll
