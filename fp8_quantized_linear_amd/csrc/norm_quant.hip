@@ -9,10 +9,14 @@
 //
 // Roundings: h is rounded to bf16 only where it is stored; the norm and the
 // quantizer take the unrounded float32 sum. The sum of squares and the row's
-// factor 1 / sqrt(..) are float64 (float32 for block FP8), y is float32; where the codes of FP8 and
-// MXFP8 could differ for a y off by its rounding, they are made again from
-// float64 (exact_codes), so a code carries one rounding, its own. The codes of
-// block FP8 are those of the float32 y over the float32 scale.
+// factor 1 / sqrt(..) are float64 (block FP8: float32 while they stay well inside
+// its range), y is float32. Where the codes of FP8 and MXFP8 could differ for a y off by its
+// rounding, they are made again from float64 (exact_codes): an MXFP8 code
+// carries one rounding, its own, an FP8 code that of fl32(1 / scale) besides.
+// The codes of block FP8 are those of the float32 y over the float32 scale.
+//
+// A y that is not a number (a NaN or infinity in its row, 0 / 0 in an all-zero
+// row under eps = 0) has a NaN code, and does not count for its block's scale.
 #include <type_traits>
 
 #include "fql_device.h"
@@ -57,6 +61,18 @@ __device__ __forceinline__ void store8(uint16_t* p, const Vec8& r, bool aligned)
   }
 }
 
+// Four float32 -> four E4M3 bytes; NaN stays NaN. minimum and maximum hand it
+// on and cost what fp8x4's fmin and fmax do, which make it -448.
+__device__ __forceinline__ float clamp_nan(float v) {
+  return __builtin_elementwise_maximum(__builtin_elementwise_minimum(v, 448.0f), -448.0f);
+}
+__device__ __forceinline__ uint32_t fp8x4_nan(float a, float b, float c, float d) {
+  short2v o = {0, 0};
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, clamp_nan(a), clamp_nan(b), 1.0f, false);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, clamp_nan(c), clamp_nan(d), 1.0f, true);
+  return __builtin_bit_cast(uint32_t, o);
+}
+
 // 2^e-scaled or plain quotient d -> float32, rounded to odd: the E4M3 rounding
 // of the result is that of d itself (float32 has more than two bits more).
 __device__ __forceinline__ float round_to_odd(double d) {
@@ -78,8 +94,8 @@ __device__ __forceinline__ void exact_codes(const Vec8& h, const Vec8& wt, doubl
   uint32_t differ = 0u;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    differ |= fp8x4(y.v[4 * j] * lo, y.v[4 * j + 1] * lo, y.v[4 * j + 2] * lo, y.v[4 * j + 3] * lo) ^
-              fp8x4(y.v[4 * j] * hi, y.v[4 * j + 1] * hi, y.v[4 * j + 2] * hi, y.v[4 * j + 3] * hi);
+    differ |= fp8x4_nan(y.v[4 * j] * lo, y.v[4 * j + 1] * lo, y.v[4 * j + 2] * lo, y.v[4 * j + 3] * lo) ^
+              fp8x4_nan(y.v[4 * j] * hi, y.v[4 * j + 1] * hi, y.v[4 * j + 2] * hi, y.v[4 * j + 3] * hi);
   if (differ == 0u) return;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -90,7 +106,7 @@ __device__ __forceinline__ void exact_codes(const Vec8& h, const Vec8& wt, doubl
       __asm__("" : "+v"(u));  // converted here: kept from the sum of squares, its float64 would spill
       c[i] = round_to_odd((double)u * rinv * (double)wt.v[4 * j + i] * (double)f);
     }
-    w[j] = fp8x4(c[0], c[1], c[2], c[3]);
+    w[j] = fp8x4_nan(c[0], c[1], c[2], c[3]);
   }
 }
 
@@ -121,7 +137,7 @@ __device__ __forceinline__ void quant_block8(const Vec8& y, float inv_scale, uin
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    w[j] = fp8x4(y.v[4 * j] * f, y.v[4 * j + 1] * f, y.v[4 * j + 2] * f, y.v[4 * j + 3] * f);
+    w[j] = fp8x4_nan(y.v[4 * j] * f, y.v[4 * j + 1] * f, y.v[4 * j + 2] * f, y.v[4 * j + 3] * f);
 }
 
 // Row-independent addressing of one workgroup's row.
@@ -192,7 +208,8 @@ __device__ __forceinline__ void finish_vec(const NormArgs& a, int64_t m, int64_t
 // row's chain is short and its loads are all in flight at once).
 template <int F, bool OP, int I, bool WAVE, bool STREAM>
 __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, const NormFlags f) {
-  __shared__ std::conditional_t<F == SC_FP8_BLOCK, float, double> red[16];
+  __shared__ double red[16];
+  __shared__ float red32[16];
   int64_t m;
   int t, T;
   if (WAVE) {
@@ -219,10 +236,6 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
   auto load_w = [&](int64_t v) { return v < nv ? load_raw8(a.weight + 8 * v, f.w) : uint4v{0u, 0u, 0u, 0u}; };
   uint4v w[EARLY ? I : 1];
   Vec8 h[I];
-  // float32 where the codes are those of a float32 y (float64 takes 8192 x 5120
-  // block FP8 from 58 to 60 us)
-  using Sum = std::conditional_t<F == SC_FP8_BLOCK, float, double>;
-  Sum ss = 0;
   if (!STREAM) {
 #pragma unroll
     for (int i = 0; i < I; ++i) {
@@ -232,27 +245,60 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
       else
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[i].v[j] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss += (Sum)h[i].v[j] * (Sum)h[i].v[j];
     }
+  }
+  // the row's sum of squares in the type of `ss`
+  auto squares = [&](auto ss, auto* red) {
+    typedef decltype(ss) Sum;
+    if (!STREAM) {
+#pragma unroll
+      for (int i = 0; i < I; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss += (Sum)h[i].v[j] * (Sum)h[i].v[j];
+    } else {
+      for (int64_t v = t; v < nv; v += T) {
+        const Vec8 u = load_h(a, f, m, v, false);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss += (Sum)u.v[j] * (Sum)u.v[j];
+      }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) ss += __shfl_xor(ss, o);
+    if (!WAVE) {
+      if ((t & 63) == 0) red[t >> 6] = ss;
+      __syncthreads();
+      ss = (Sum)0;
+      for (int i = 0; i < T / 64; ++i) ss += red[i];
+    }
+    return ss;
+  };
+  float shift = 1.0f;
+  auto factor64 = [&]() {
+    double r = 1.0 / __builtin_sqrt(squares(0.0, red) / (double)a.K + (double)a.eps);
+    // rows of magnitude 1e38 (under eps = 0 also 1e-39), whose factor is no normal
+    // float32: a power of two goes from it into the row, which changes no y
+    if (!(r >= 0x1p-126 && r <= 0x1p127)) {
+      shift = r > 1.0 ? 0x1p64f : 0x1p-64f;
+      r /= (double)shift;
+      if (!STREAM)
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[i].v[j] *= shift;
+    }
+    return r;
+  };
+  // Block FP8, whose codes are those of a float32 y, sums in float32 and again in
+  // float64 where the squares leave float32's range (float64 at once takes 8192 x
+  // 5120 from 55.5 to 57.5 us).
+  std::conditional_t<F == SC_FP8_BLOCK, float, double> rinv;
+  if constexpr (F == SC_FP8_BLOCK) {
+    const float ss = squares(0.0f, red32);
+    rinv = 1.0f / __builtin_sqrtf(ss / (float)a.K + a.eps);
+    if (!(ss >= 0x1p-100f && ss <= 0x1p126f)) rinv = (float)factor64();
   } else {
-    for (int64_t v = t; v < nv; v += T) {
-      const Vec8 u = load_h(a, f, m, v, false);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss += (Sum)u.v[j] * (Sum)u.v[j];
-    }
+    rinv = factor64();
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) ss += __shfl_xor(ss, o);
-  if (!WAVE) {
-    if ((t & 63) == 0) red[t >> 6] = ss;
-    __syncthreads();
-    ss = 0;
-    for (int i = 0; i < T / 64; ++i) ss += red[i];
-  }
-  Sum rinv;
-  if constexpr (F == SC_FP8_BLOCK) rinv = 1.0f / __builtin_sqrtf(ss / (float)a.K + a.eps);
-  else rinv = 1.0 / __builtin_sqrt(ss / (double)a.K + (double)a.eps);
   if (!STREAM) {
 #pragma unroll
     for (int i = 0; i < I; ++i) {
@@ -267,6 +313,8 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
 #pragma unroll
       for (int j = 0; j < 8; ++j) u.v[j] = 0.0f;
       if (v < nv) u = load_h(a, f, m, v, true);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u.v[j] *= shift;
       finish_vec<F, OP>(a, m, v, nv, nvp, u, widen(load_w(v)), rinv);
     }
   }

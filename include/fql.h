@@ -491,6 +491,8 @@ int fql_linear_fp8_block(const void* x, int64_t M, int64_t K, int64_t ldx, const
  *   codes, scales = the format's quantizer (fql_quant_fp8 with `scale`,
  *   fql_quant_fp8_block, fql_quant_mxfp8) applied to the float32 y.
  *   x, residual [M][ld] bf16; weight [K] bf16; eps finite, >= 0.
+ *   A y that is not a number (NaN or infinity in its row; 0 / 0 in an all-zero
+ *   row under eps = 0) gets a NaN code and does not count for its block's scale.
  *   scale   per-tensor FP8's static scale (ignored otherwise).
  *   codes   [M][K], 8-byte aligned; scales as the format's quantizer writes
  *           them (NULL for per-tensor FP8).

@@ -2,12 +2,14 @@
 
 import numpy as np
 import pytest
+import torch
 
 import fp8_quantized_linear_amd as fql
 from oracle import serving as S
 
 from gpu_helpers import announce
 from serving_helpers import (HALF_BF16, assert_attention, bf16, f64, i32, poison, random_cache, tables, to_device)
+from test_gpu_serving import FMTS, SCALE, check_norm, layer, operand_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +68,66 @@ def test_attention_value_exponents_at_the_ends(E, new):
     ref = S.attention(q64, cache, table, [L], [0, new], D ** -0.5)
     assert np.isfinite(f64(out)).all()
     assert_attention(out, lse, ref, f"2^{E}")
+
+
+# ---------------------------------------------------------------------------
+# norm
+# ---------------------------------------------------------------------------
+
+NORM_SHAPES = [(7, 256), (7, 4096), (1, 256), (7, 14336), (7, 20480), (7, 70016)]
+
+
+def rows_at_the_ends(rng, M, K):
+    """Rows: ordinary, one NaN, one infinity, around 1e30, zeros, bf16 subnormals, ordinary."""
+    x = rng.standard_normal((M, K))
+    if M > 1:
+        x[1, 9], x[2, 5] = np.nan, np.inf
+        x[3] *= 1e30
+        x[4] = 0.0
+        x[5] *= 1e-39
+    return x
+
+
+def check_rows(fmt, codes, scales, y):
+    """Codes are NaN exactly where y is; the others and the scales are those of y without its NaN."""
+    nan = np.isnan(y)
+    assert np.array_equal((codes & 0x7F) == 0x7F, nan), (fmt, [int(r.sum()) for r in (codes & 0x7F) == 0x7F])
+    check_norm(fmt, np.where(nan, np.uint8(0), codes), scales, np.where(nan, 0.0, y))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("M,K", NORM_SHAPES)
+def test_norm_rows_that_are_not_finite_or_at_the_ends_of_the_range(fmt, eps, M, K):
+    """A y that is not a number has a NaN code (an all-zero row under eps = 0 too: 0 / 0), and rows
+    whose squares leave float32's range are normed like any other."""
+    announce(f"norm ends {fmt} {M}x{K} eps={eps}")
+    rng = np.random.default_rng([22, M, K])
+    x, x64 = bf16(rows_at_the_ends(rng, M, K))
+    w, w64 = bf16(1 + 0.2 * rng.standard_normal(K))
+    w[K - 3] = float("nan")  # a column of the weight
+    w64[K - 3] = np.nan
+    with np.errstate(invalid="ignore", divide="ignore"):
+        y, _ = S.rms_norm(x64, w64, eps)
+    sc = SCALE if fmt == "fp8" else None
+    codes, scales, _ = fql.rms_norm_quant(x, w, fmt, eps=eps, scale=sc)
+    codes = codes.cpu().numpy()
+    check_rows(fmt, codes, None if scales is None else scales.cpu().numpy(), y)
+    oc, os_ = operand_rows(fql.rms_norm_operand(x, w, fmt, eps=eps, scale=sc)[0])
+    assert np.array_equal(oc, codes)
+    assert os_ is None or np.array_equal(os_, scales.cpu().numpy())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [3, 80])
+def test_a_row_that_is_not_finite_stays_so_through_the_linear_layer(fmt, M):
+    announce(f"NaN row through the layer {fmt} M={M}")
+    rng = np.random.default_rng([23, M])
+    h, _ = bf16(rng.standard_normal((M, 512)))
+    h[1, 100] = float("inf")
+    r, _ = bf16(rng.standard_normal((M, 512)))
+    w, _ = bf16(np.ones(512))
+    g, _ = layer(fmt, rng.standard_normal((256, 512)) * 0.05)
+    x, _ = fql.rms_norm_operand(h, w, fmt, residual=r, scale=0.1 if fmt == "fp8" else None)
+    y = torch.isnan(fql.linear_fused(x, g))
+    assert y[1].all() and not y[0].any() and not y[2:].any()
