@@ -179,6 +179,7 @@ SIGNATURES = {
     "fql_fp8_scale": (_c_int, [_c_f32, ctypes.POINTER(_c_f32)]),
     "fql_fp8_output_scale": (_c_int, [_c_f32, _c_f32, ctypes.POINTER(_c_f32)]),
     "fql_set_plan_override": (_c_int, [_c_int, ctypes.c_char_p]),
+    "fql_stream_capture_id": (_c_int, [_c_vp, ctypes.POINTER(ctypes.c_uint64)]),
     "fql_linear_nvfp4_noalloc": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_f32, _c_int, _c_vp,
                                           _c_i64, _c_f32, _c_vp, _c_vp, _c_i64, _c_vp]),
     "fql_rms_norm_quant": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp,
@@ -504,8 +505,13 @@ def linear_plan(M, N, K, aligned=True, transform=False, hadamard_block=0):
     return buf.value.decode()
 
 
-_workspaces = {}
-_outgrown = []  # replaced workspaces: a captured graph may hold their addresses
+_workspaces = {}  # of eager calls: (device type, index, stream) -> buffer
+_outgrown = []    # replaced ones
+_captured = {}    # of a stream's newest graph capture: the same key -> (capture id, buffer)
+_COUNTER_BYTES = 64 << 10      # leading part of a workspace that has to start at zero
+_CAPTURED_BYTES = 16 << 20     # serves the layers of a step of up to a hundred tokens: one clearing a graph
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+
 
 def new_workspace(nbytes, device):
     """A zero-filled workspace buffer (its leading arrival counters must start at zero;
@@ -515,6 +521,10 @@ def new_workspace(nbytes, device):
 
 def _workspace(device, nbytes):
     key = (device.type, device.index, torch.cuda.current_stream(device).cuda_stream)
+    if _captured or _capturing():
+        ws = _captured_workspace(key, nbytes, device)
+        if ws is not None:
+            return ws
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = _grow_workspace(key, nbytes, device)
@@ -523,10 +533,7 @@ def _workspace(device, nbytes):
 
 def _grow_workspace(key, nbytes, device):
     """A new workspace for `key`, at least twice as large as the one it replaces: those are kept,
-    and so hold no more than the newest in all. Under graph capture the workspace is the graph's
-    own, cleared by every replay, and no eager call ever sees it."""
-    if torch.cuda.is_current_stream_capturing():
-        return new_workspace(nbytes, device)
+    and so hold no more than the newest in all."""
     old = _workspaces.get(key)
     if old is not None:
         nbytes = max(nbytes, 2 * old.numel())
@@ -534,6 +541,27 @@ def _grow_workspace(key, nbytes, device):
     if old is not None:
         _outgrown.append(old)
     _workspaces[key] = ws
+    return ws
+
+
+def _captured_workspace(key, nbytes, device):
+    """The workspace of the calls that a graph capture on this stream records, None outside of one.
+
+    It is the graph's own, whether the stream has an eager one or not: replays may run beside eager
+    calls and beside other graphs of the stream. Its memory is the graph's (it was allocated under
+    the capture), and the graph clears its counters once, before the first call. This module holds it
+    until the capture's end shows: at the stream's next eager call or its next capture."""
+    if not _capturing():
+        _captured.pop(key, None)
+        return None
+    n = ctypes.c_uint64()
+    _check(lib().fql_stream_capture_id(key[2], ctypes.byref(n)))
+    capture, ws = _captured.get(key, (0, None))
+    if capture != n.value or ws.numel() < nbytes:
+        held = ws.numel() if capture == n.value else 0
+        ws = torch.empty(max(nbytes, 2 * held, _CAPTURED_BYTES), dtype=torch.uint8, device=device)
+        ws[:_COUNTER_BYTES].zero_()
+        _captured[key] = (n.value, ws)
     return ws
 
 

@@ -493,6 +493,17 @@ int fql_set_plan_override(int which, const char* spec) {
   return ok();
 }
 
+int fql_stream_capture_id(void* stream, uint64_t* id) {
+  if (!id) return fail(FQL_ERR_INVALID, "null pointer");
+  hipStreamCaptureStatus status = hipStreamCaptureStatusNone;
+  unsigned long long number = 0;
+  if (int r = hip_status(hipStreamGetCaptureInfo(static_cast<hipStream_t>(stream), &status, &number), "capture info"))
+    return r;
+  if (status == hipStreamCaptureStatusInvalidated) return fail(FQL_ERR_INVALID, "the stream's capture was invalidated");
+  *id = status == hipStreamCaptureStatusActive ? (uint64_t)number + 1 : 0;
+  return ok();
+}
+
 // ---- general block-diagonal transform, dynamic global scale ------------------
 
 }  // extern "C"

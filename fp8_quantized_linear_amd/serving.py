@@ -25,8 +25,8 @@ import struct
 
 import torch
 
-from . import (FMT_FP8, FMT_FP8_BLOCK, FMT_MXFP4, FMT_MXFP8, FQLError, _check, _grow_workspace, _rows_view,
-               _size_query, _workspaces, lib)
+from . import (FMT_FP8, FMT_FP8_BLOCK, FMT_MXFP4, FMT_MXFP8, FQLError, _captured, _captured_workspace, _capturing,
+               _check, _grow_workspace, _rows_view, _size_query, _workspaces, lib)
 
 FORMATS = {"mxfp4": FMT_MXFP4, "mxfp8": FMT_MXFP8, "fp8": FMT_FP8, "fp8_block": FMT_FP8_BLOCK}
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
@@ -41,9 +41,13 @@ _query = functools.lru_cache(4096)(_size_query)
 
 
 def _workspace(device, nbytes):
-    """The binding's workspace of this device and stream (shared with the linear calls)."""
+    """The binding's workspace of this device and stream, or of its capture (shared with the linear calls)."""
     index = device.index
     key = ("cuda", index, _stream(index))
+    if _captured or _capturing():
+        ws = _captured_workspace(key, nbytes, device)
+        if ws is not None:
+            return ws
     ws = _workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = _grow_workspace(key, nbytes, device)

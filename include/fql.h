@@ -285,6 +285,12 @@ int fql_fp8_output_scale(float input_scale, float weight_scale, float* alpha);
 #define FQL_PLAN_SC_GEMV 2
 int fql_set_plan_override(int which, const char* spec);
 
+/* The graph capture that a stream is in: *id is 0 when it is in none, else a
+ * number that no other capture of the process has. Calls captured into
+ * different graphs, or into a graph and made eagerly, need different workspaces
+ * unless nothing ever runs them at the same time. Host-side only. */
+int fql_stream_capture_id(void* stream, uint64_t* id);
+
 /* ---------------------------------------------------------------------------
  * General block-diagonal transform and dynamic global scale ("QUTLASS NVFP4
  * online transforms" write-up: the fused quantizer accepts any

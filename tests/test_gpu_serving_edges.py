@@ -9,7 +9,7 @@ from oracle import serving as S
 
 from gpu_helpers import announce
 from serving_helpers import (HALF_BF16, assert_attention, bf16, f64, i32, poison, random_cache, tables, to_device)
-from test_gpu_serving import FMTS, SCALE, check_norm, layer, operand_rows
+from test_gpu_serving import FMTS, SCALE, Decoder, check_norm, layer, operand_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -131,3 +131,120 @@ def test_a_row_that_is_not_finite_stays_so_through_the_linear_layer(fmt, M):
     x, _ = fql.rms_norm_operand(h, w, fmt, residual=r, scale=0.1 if fmt == "fp8" else None)
     y = torch.isnan(fql.linear_fused(x, g))
     assert y[1].all() and not y[0].any() and not y[2:].any()
+
+
+# ---------------------------------------------------------------------------
+# workspaces under graph capture
+# ---------------------------------------------------------------------------
+
+def split_call(rng, lens, blocks, max_len):
+    """Arguments of an attention call whose keys are split into ranges."""
+    table = tables(rng, len(lens), max_len // 64, blocks, lens, 64, -1)
+    q, _ = bf16(rng.standard_normal((len(lens), 8, 128)))
+    assert "splits=1" not in fql.attention_kv8_plan(len(lens), 8, 2, 128, 1, max_len).split()
+    return (q, to_device(random_cache(rng, blocks, 2, 64, 128)), i32(table), i32(lens), i32(range(len(lens) + 1)), 1)
+
+
+def captured(s, args, warm):
+    with torch.cuda.stream(s):
+        if warm:
+            fql.attention_kv8(*args)
+        s.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            out = fql.attention_kv8(*args)
+    return g, out
+
+
+@pytest.mark.parametrize("warm", [False, True])
+def test_a_graph_does_not_use_its_streams_eager_workspace(warm):
+    """A replay on another stream beside eager calls on the capture's stream: the two must not share
+    arrival counters. A call in flight is stood in for by counters that are not zero."""
+    announce(f"workspace of a graph warm={warm}")
+    rng = np.random.default_rng([24, warm])
+    args = split_call(rng, [4000, 900], 90, 63 * 64)
+    want = fql.attention_kv8(*args)
+    torch.cuda.synchronize()
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    key = ("cuda", 0, s.cuda_stream)
+    fql._workspaces.pop(key, None)
+    g, got = captured(s, args, warm)
+    with torch.cuda.stream(s):
+        fql.attention_kv8(*args)
+        s.synchronize()
+    eager = fql._workspaces[key]
+    for _ in range(4):
+        got.zero_()
+        eager[:65536].fill_(1)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            g.replay()
+        other.synchronize()
+        assert (eager[:65536] == 1).all()
+        eager[:65536].zero_()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        with torch.cuda.stream(s):
+            assert torch.equal(fql.attention_kv8(*args), want)
+        torch.cuda.synchronize()
+
+
+def test_graphs_captured_on_one_stream_do_not_share_counters():
+    announce("two graphs")
+    rng = np.random.default_rng(25)
+    cases = [split_call(rng, [4000, 900], 90, 63 * 64), split_call(rng, [3000, 2900, 10], 100, 63 * 64)]
+    want = [fql.attention_kv8(*a) for a in cases]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    graphs = [captured(s, a, True) for a in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(20):
+        for t, (g, _) in zip(streams, graphs):
+            with torch.cuda.stream(t):
+                g.replay()
+        torch.cuda.synchronize()
+        for (_, got), w in zip(graphs, want):
+            assert torch.equal(got, w)
+            got.zero_()
+        torch.cuda.synchronize()
+
+
+def test_a_capture_clears_one_workspace_and_lets_go_of_it():
+    """A whole layer captured on a stream without a workspace: one buffer, dropped when the stream is
+    used again; replays give the eager results."""
+    announce("one workspace a capture")
+    net = Decoder("mxfp8")
+    rng = np.random.default_rng(26)
+    table, lens, cu = i32([[0, 1, 2, 3], [4, 5, 6, 7]]), i32([20, 30]), i32([0, 1, 2])
+    start = random_cache(rng, 8, 2, 16, 64)
+    caches = [to_device(start) for _ in range(2)]
+    h, _ = bf16(rng.standard_normal((2, 512)))
+    want = net(h, caches[0], table, lens, cu, 1)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    key = ("cuda", 0, s.cuda_stream)
+    for held in (fql._workspaces, fql._captured):
+        held.pop(key, None)
+    g = torch.cuda.CUDAGraph()
+    seen = set()
+    with torch.cuda.graph(g, stream=s):
+        x, _ = fql.rms_norm_operand(h, net.w1, "mxfp8")
+        for _ in range(2):
+            y = fql.linear_fused(x, net.qkv)
+            seen.add(fql._captured[key][1].data_ptr())
+        got = net(h, caches[1], table, lens, cu, 1)
+        fql.linear_mxfp8(h, net.qkv)
+        seen.add(fql._captured[key][1].data_ptr())
+    assert len(seen) == 1 and key not in fql._workspaces and y.shape == (2, 768)
+    for _ in range(3):  # the cache is written with the same tokens each time
+        got.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    with torch.cuda.stream(s):
+        fql.linear_fused(h, net.qkv)
+    torch.cuda.synchronize()
+    assert key not in fql._captured and key in fql._workspaces
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
