@@ -336,6 +336,7 @@ def set_plan_override(spec, which="nvfp4"):
     or "" removes it. Results change at most in the float32 summation order."""
     _check(lib().fql_set_plan_override(PLAN_OVERRIDES[which],
                                        None if not spec else str(spec).encode()))
+    serving._query.cache_clear()  # workspace sizes remembered under the last one
 
 
 class plan_override:
@@ -1059,6 +1060,7 @@ def warmup(layers, token_counts, device=None):
     return calls
 
 
+from . import serving  # noqa: E402
 from .serving import (KVCache8, QuantizedActivation, attention_kv8, attention_kv8_plan,  # noqa: E402
                       interleave_gate_up, kv_append, linear_fused, linear_fused_plan, quant_operand,
                       rms_norm_operand, rms_norm_quant)

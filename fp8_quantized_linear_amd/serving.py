@@ -34,7 +34,7 @@ ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu":
 # A decode step's calls take a few microseconds on the GPU, so what Python does
 # around them counts: addresses go to the library as plain integers, the
 # structs of include/fql.h as packed bytes, sizes that depend on shapes alone
-# are remembered.
+# are remembered (until set_plan_override changes the plans).
 _stream = torch._C._cuda_getCurrentRawStream  # device index -> hipStream_t of torch's current stream
 _bf16, _u8, _i32, _f32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
 _query = functools.lru_cache(4096)(_size_query)
