@@ -350,9 +350,10 @@ hipError_t launch_t(const NormArgs& a, hipStream_t st) {
 // store instruction fills whole runs; with a row's blocks in neighbouring
 // lanes (the standalone quantizer's order) they are 16-byte pieces 256 bytes
 // apart. The block arithmetic is quant_block32's. Rows past M are not written.
-// 4096 x 4096 MXFP8: 10 us, 4.9 TB/s (15.9 us in the quantizer's order).
+// 4096 x 4096 MXFP8: 10 us, 4.9 TB/s (15.9 us in the quantizer's order). It has
+// the name of the plain linear call's operand quantizer: launch plans name it.
 template <int F>
-__global__ __launch_bounds__(256) void quant_operand_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
+__global__ __launch_bounds__(256) void sc_quant_operand_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                             int64_t ldx, bool aligned, float inv_scale, int64_t KC,
                                                             int64_t waves, uint8_t* __restrict__ codes,
                                                             void* __restrict__ scales) {
@@ -409,7 +410,7 @@ hipError_t launch_quant_operand(int fmt, const uint16_t* x, int64_t M, int64_t K
   const unsigned grid = (unsigned)((waves + 3) / 4);
 #define FQL_Q(F)                                                                                                   \
   if (fmt == F) {                                                                                                  \
-    quant_operand_kernel<F><<<grid, 256, 0, st>>>(x, M, K, ldx, aligned, inv_scale, KC, waves, codes, scales);     \
+    sc_quant_operand_kernel<F><<<grid, 256, 0, st>>>(x, M, K, ldx, aligned, inv_scale, KC, waves, codes, scales);  \
     return hipGetLastError();                                                                                      \
   }
   FQL_Q(SC_MXFP4) FQL_Q(SC_MXFP8) FQL_Q(SC_FP8) FQL_Q(SC_FP8_BLOCK)

@@ -134,6 +134,27 @@ def test_a_row_that_is_not_finite_stays_so_through_the_linear_layer(fmt, M):
 
 
 # ---------------------------------------------------------------------------
+# fused linear
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt,M", [("mxfp8", 64), ("fp8_block", 20), ("mxfp4", 100), ("fp8", 4)])
+def test_the_plan_names_the_kernels_that_run(fmt, M):
+    announce(f"kernels of the plan {fmt} M={M}")
+    g, _ = layer(fmt, np.random.default_rng(27).standard_normal((256, 512)))
+    x, _ = bf16(np.ones((M, 512)))
+    fql.linear_fused(x, g)
+    torch.cuda.synchronize()
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as p:
+        fql.linear_fused(x, g)
+        torch.cuda.synchronize()
+    ran = [e.name for e in p.events() if "fql::" in e.name]
+    named = [part.split("<")[0] for part in fql.linear_fused_plan(fmt, M, 256, 512).split(" + ")]
+    assert len(ran) == len(named), (ran, named)
+    for kernel, name in zip(ran, named):
+        assert f":{name}<" in kernel, (kernel, name)
+
+
+# ---------------------------------------------------------------------------
 # workspaces under graph capture
 # ---------------------------------------------------------------------------
 
