@@ -76,10 +76,19 @@ def _cuda(t, name, dtype):
         raise FQLError(f"{name} must be {dtype}")
 
 
-def _rows(t, name, shape=None):
-    """(address, rows, columns, row stride) of a bf16 [..., K] tensor, of the given shape if any."""
-    _cuda(t, name, _bf16)
-    if shape is not None and t.shape != shape:
+def _same_device(t, name, index, of="x"):
+    if t.get_device() != index:
+        raise FQLError(f"{name} must be on {of}'s device")
+
+
+def _rows(t, name, shape=None, index=None):
+    """(address, rows, columns, row stride) of a bf16 [..., K] tensor, of the given shape and on the
+    given device if any."""
+    if shape is None:
+        _cuda(t, name, _bf16)
+    elif not isinstance(t, torch.Tensor) or t.dtype is not _bf16 or t.get_device() != index or t.shape != shape:
+        _cuda(t, name, _bf16)
+        _same_device(t, name, index)
         raise FQLError(f"{name} must have shape {tuple(shape)}")
     if t.dim() == 2:
         M, K = t.shape
@@ -98,8 +107,10 @@ def _scale_arg(fmt, scale):
     return ctypes.c_float(float(scale)).value
 
 
-def _vector(t, name, n):
-    _cuda(t, name, _bf16)
+def _vector(t, name, n, index):
+    if not isinstance(t, torch.Tensor) or t.dtype is not _bf16 or t.get_device() != index:
+        _cuda(t, name, _bf16)
+        _same_device(t, name, index)
     if t.numel() != n or not t.is_contiguous():
         raise FQLError(f"{name} must be a contiguous bf16 tensor of {n} elements")
     return t.data_ptr()
@@ -135,16 +146,17 @@ def _new_operand(x, fmt, scale):
 def _norm_args(x, weight, residual, residual_out):
     """(address, M, K, ld of x, of the residual: address, ld, weight's address, h, its address and ld)."""
     xp, M, K, ld = _rows(x, "x")
-    wp = _vector(weight, "weight", K)
+    index = x.get_device()
+    wp = _vector(weight, "weight", K, index)
     if residual is None:
         if residual_out is not None:
             raise FQLError("residual_out needs a residual")
         return xp, M, K, ld, 0, 0, wp, None, 0, 0
-    rp, _, _, ldr = _rows(residual, "residual", x.shape)
+    rp, _, _, ldr = _rows(residual, "residual", x.shape, index)
     if residual_out is None:
         h = _new(x.shape, _bf16, x.device)
         return xp, M, K, ld, rp, ldr, wp, h, h.data_ptr(), K
-    hp, _, _, ldh = _rows(residual_out, "residual_out", x.shape)
+    hp, _, _, ldh = _rows(residual_out, "residual_out", x.shape, index)
     return xp, M, K, ld, rp, ldr, wp, residual_out, hp, ldh
 
 
@@ -237,24 +249,34 @@ def linear_fused(x, weight, activation=None, bias=None, residual=None, alpha=Non
         lead, dev = x.shape[:-1], x.device
     if xK != K:
         raise FQLError(f"x has K={xK}, weight has K={K}")
-    bp = 0 if bias is None else _vector(bias, "bias", N)
+    index = dev.index
+    packed = weight.packed
+    if packed.get_device() != index:
+        _same_device(packed, "weight", index)
+    bp = 0 if bias is None else _vector(bias, "bias", N, index)
     No = N // 2 if activation == "swiglu" else N
     shape = lead + (No,)
+    rp = ldr = 0
+    if residual is not None:
+        rp, _, _, ldr = _rows(residual, "residual", shape, index)
     if out is None:
         out = _new(shape, _bf16, dev)
         yp, ldy = out.data_ptr(), No
     else:
-        yp, _, _, ldy = _rows(out, "out", shape)
-    rp = ldr = 0
-    if residual is not None:
-        rp, _, _, ldr = _rows(residual, "residual", shape)
+        yp, _, _, ldy = _rows(out, "out", shape, index)
     if workspace is None:
         workspace = _workspace(dev, _query("fql_linear_fused_workspace_bytes", FORMATS[fmt], M, N, K))
-    scale = weight.input_scale if fmt == "fp8" else 0
-    ap = weight.alpha_dev.data_ptr() if fmt == "fp8" and alpha is None else 0
-    _check(lib().fql_linear_fused(FORMATS[fmt], xp, M, K, ld, scale, op, weight.packed.data_ptr(), N,
+    else:
+        _same_device(workspace, "workspace", index)
+    scale, ap = 0, 0
+    if fmt == "fp8":
+        scale = weight.input_scale
+        if alpha is None:
+            _same_device(weight.alpha_dev, "alpha_dev", index)
+            ap = weight.alpha_dev.data_ptr()
+    _check(lib().fql_linear_fused(FORMATS[fmt], xp, M, K, ld, scale, op, packed.data_ptr(), N,
                                   1.0 if alpha is None else alpha, ap, bp, ACTIVATIONS[activation], rp, ldr, yp, ldy,
-                                  workspace.data_ptr(), workspace.numel(), _stream(dev.index)))
+                                  workspace.data_ptr(), workspace.numel(), _stream(index)))
     return out
 
 
@@ -395,6 +417,8 @@ def attention_kv8(q, cache, block_table, lens, cu_seqlens, max_new, causal=True,
         if workspace is None:
             workspace = _workspace(dev, _query("fql_attention_kv8_workspace_bytes", B, Hq, cache.kv_heads, D, new,
                                                max_len, window))
+        else:
+            _same_device(workspace, "workspace", cache._index, "the cache")
         _check(lib().fql_attention_kv8(cache._struct, b, qp, qt, qh, Hq, D ** -0.5 if scale is None else scale,
                                        bool(causal), window, max_len, op, ot, oh, lp, workspace.data_ptr(),
                                        workspace.numel(), _stream(cache._index)))

@@ -1,6 +1,10 @@
 """Edges of the 8-bit serving operators that need no GPU: host queries, checks of arguments."""
 
 import ctypes
+import types
+
+import pytest
+import torch
 
 import fp8_quantized_linear_amd as fql
 
@@ -24,3 +28,73 @@ def test_a_remembered_workspace_size_follows_the_launch_plan_override():
     with fql.plan_override("2,2,4,4,3,4", which="sc_gemm"):
         assert size() == asked() > 4 * plain
     assert size() == asked() == plain
+
+
+# ---------------------------------------------------------------------------
+# tensors of another device
+# ---------------------------------------------------------------------------
+
+class OnDevice(torch.Tensor):
+    """A host tensor that says it lies on a GPU: enough for checks that come before any launch."""
+
+    @staticmethod
+    def make(t, index):
+        t = t.as_subclass(OnDevice)
+        t.index = index
+        return t
+
+    is_cuda = property(lambda self: True)
+    device = property(lambda self: torch.device("cuda", self.index))
+
+    def get_device(self):
+        return self.index
+
+
+def bf16(index, *shape):
+    return OnDevice.make(torch.zeros(shape, dtype=torch.bfloat16), index)
+
+
+def weight(index, fmt="mxfp8", alpha_index=0):
+    w = types.SimpleNamespace(fmt=fmt, N=64, K=128, packed=OnDevice.make(torch.zeros(64, dtype=torch.uint8), index))
+    if fmt == "fp8":
+        w.input_scale, w.alpha_dev = 0.5, OnDevice.make(torch.zeros(1), alpha_index)
+    return w
+
+
+@pytest.mark.parametrize("call", [fql.rms_norm_quant, fql.rms_norm_operand])
+def test_norm_refuses_tensors_of_another_device(call):
+    x = bf16(0, 4, 128)
+    for name, args in (("weight", dict(weight=bf16(1, 128))), ("residual", dict(residual=bf16(1, 4, 128))),
+                       ("residual_out", dict(residual=bf16(0, 4, 128), residual_out=bf16(1, 4, 128)))):
+        args = {"weight": bf16(0, 128), **args}
+        with pytest.raises(fql.FQLError, match=f"{name} must be on x's device"):
+            call(x, fmt="mxfp8", **args)
+
+
+def test_linear_refuses_tensors_of_another_device():
+    x = bf16(0, 4, 128)
+    op = fql.QuantizedActivation(OnDevice.make(torch.zeros(64, dtype=torch.uint8), 0), "mxfp8", (4,), 128)
+    ws = OnDevice.make(torch.zeros(64, dtype=torch.uint8), 1)
+    for a in (x, op):
+        for name, w, args in (("weight", weight(1), {}), ("bias", weight(0), dict(bias=bf16(1, 64))),
+                              ("residual", weight(0), dict(residual=bf16(1, 4, 64))),
+                              ("out", weight(0), dict(out=bf16(1, 4, 64))),
+                              ("workspace", weight(0), dict(out=bf16(0, 4, 64), workspace=ws))):
+            with pytest.raises(fql.FQLError, match=f"{name} must be on x's device"):
+                fql.linear_fused(a, w, **args)
+    with pytest.raises(fql.FQLError, match="alpha_dev must be on x's device"):
+        fql.linear_fused(x, weight(0, "fp8", 1), out=bf16(0, 4, 64), workspace=OnDevice.make(ws.as_subclass(torch.Tensor), 0))
+
+
+def test_attention_refuses_a_workspace_of_another_device():
+    def u8(*shape):
+        return OnDevice.make(torch.zeros(shape, dtype=torch.uint8), 0)
+
+    def i32(*values):
+        return OnDevice.make(torch.tensor(values, dtype=torch.int32), 0)
+
+    cache = fql.KVCache8(u8(2, 1, 16, 64), u8(2, 1, 1, 64, 16), u8(2, 1), u8(2, 1))
+    q = bf16(0, 1, 2, 64)
+    with pytest.raises(fql.FQLError, match="workspace must be on the cache's device"):
+        fql.attention_kv8(q, cache, i32([0, 1]), i32(1), i32(0, 1), 1, out=bf16(0, 1, 2, 64),
+                          workspace=OnDevice.make(torch.zeros(1 << 20, dtype=torch.uint8), 1))
