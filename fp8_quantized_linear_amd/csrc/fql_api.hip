@@ -1127,6 +1127,21 @@ int check_attention(int batch, int Hq, int Hkv, int D, int64_t max_new, int64_t 
   return FQL_OK;
 }
 
+// Whether two of the rows of D elements at t * lt + h * lh, t < T, h < H, share an element.
+bool rows_overlap(int64_t T, int64_t lt, int64_t H, int64_t lh, int64_t D) {
+  typedef __int128 wide;
+  if ((H == 1 || lh >= D) && (T == 1 || lt >= (wide)(H - 1) * lh + D)) return false;
+  if ((T == 1 || lt >= D) && (H == 1 || lh >= (wide)(T - 1) * lt + D)) return false;
+  // other strides: for each distance in heads the distances in tokens around the one that meets it
+  if (T > 1 && lt < D) return true;
+  for (int64_t dh = 1; dh < H; ++dh) {
+    const wide a = (wide)dh * lh, t0 = T > 1 ? a / lt : 0;
+    for (wide dt : {t0, t0 + 1})
+      if (dt < T && (a > dt * lt ? a - dt * lt : dt * lt - a) < D) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1293,6 +1308,7 @@ int fql_attention_kv8(const fql_kv_cache* cache, const fql_kv_batch* batch, cons
     if (int r = check_attention(b.B, q_heads, c.heads, c.D, b.max_new, max_len, window, &plan)) return r;
     if (!q || !out || !workspace) return fail(FQL_ERR_INVALID, "null pointer");
     if (q_ld_token < 0 || q_ld_head < 0 || o_ld_token < 0 || o_ld_head < 0) return fail(FQL_ERR_INVALID, "negative stride");
+    if (rows_overlap(b.T, o_ld_token, q_heads, o_ld_head, c.D)) return fail(FQL_ERR_INVALID, "rows of out overlap");
     if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(FQL_ERR_INVALID, "scale must be finite and > 0");
     if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return fail(FQL_ERR_INVALID, "workspace must be 256-byte aligned");
     if (b.T == 0 || b.max_new == 0) return ok();

@@ -628,7 +628,8 @@ int fql_attention_kv8_describe(int batch, int q_heads, int kv_heads, int head_di
  * them): out = sum_j p_j v_j / sum_j p_j, p_j = exp(scale * q . k_j - max).
  * Query head i reads kv head i / (q_heads / kv_heads).
  *   q, out   bf16 [tokens][q_heads][head_dim] with token and head strides.
- *            Rows that no sequence names are not written.
+ *            Rows that no sequence names are not written; rows of out must not
+ *            overlap.
  *   scale    of the scores, finite and > 0.
  *   lse      float32 [tokens][q_heads] or NULL: log sum_j exp(scale q . k_j).
  *   causal   nonzero: position p sees keys 0 .. p; zero: all lens[b] keys.

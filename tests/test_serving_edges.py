@@ -8,7 +8,7 @@ import torch
 
 import fp8_quantized_linear_amd as fql
 
-from test_serving_api import refused
+from test_serving_api import NULL, P, batch, cache, refused
 
 
 def test_capture_id_refusals():
@@ -98,3 +98,31 @@ def test_attention_refuses_a_workspace_of_another_device():
     with pytest.raises(fql.FQLError, match="workspace must be on the cache's device"):
         fql.attention_kv8(q, cache, i32([0, 1]), i32(1), i32(0, 1), 1, out=bf16(0, 1, 2, 64),
                           workspace=OnDevice.make(torch.zeros(1 << 20, dtype=torch.uint8), 1))
+
+
+# ---------------------------------------------------------------------------
+# attention's output rows and its host arguments
+# ---------------------------------------------------------------------------
+
+def attend_out(tokens, heads, ld_token, ld_head):
+    return fql.lib().fql_attention_kv8(
+        ctypes.byref(cache()), ctypes.byref(batch(tokens=tokens, max_new=min(tokens, 2))), P, heads * 64, 64, heads, 0.1, 1,
+        0, 64, P, ld_token, ld_head, NULL, P, 16, NULL)  # a workspace of 16 bytes: what passes is refused for that
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 5])
+@pytest.mark.parametrize("heads", [2, 6])
+def test_attention_refuses_output_rows_that_overlap(tokens, heads):
+    D = 64
+    for lt in (0, 1, 32, 63, 64, 65, 96, 128, 129, 160, 192, 320, 384, 400, 640):
+        for lh in (0, 1, 48, 63, 64, 65, 96, 128, 192, 320, 321, 640):
+            starts = sorted(t * lt + h * lh for t in range(tokens) for h in range(heads))
+            apart = all(b - a >= D for a, b in zip(starts, starts[1:]))
+            if apart:
+                refused(attend_out(tokens, heads, lt, lh), "workspace", code=-4)
+            else:
+                refused(attend_out(tokens, heads, lt, lh), "overlap")
+    big = 1 << 62  # no overflow on the way
+    refused(attend_out(tokens, heads, big, 64), "workspace", code=-4)
+    refused(attend_out(tokens, heads, 64 * heads, big), "workspace", code=-4)
+    refused(attend_out(tokens, heads, big, 0), "overlap")
