@@ -137,9 +137,11 @@ class QuantizedActivation:
 
 
 def _new_operand(x, fmt, scale):
+    """An operand of x's shape, without any bytes where x has no rows."""
     K = x.shape[-1]
     q = QuantizedActivation(None, fmt, x.shape[:-1], K, scale if fmt == "fp8" else None)
-    q.data = torch.empty_strided((_query("fql_operand_bytes", _format(fmt), q.M, K),), (1,), dtype=_u8, device=x.device)
+    n = _query("fql_operand_bytes", _format(fmt), q.M or 1, K)
+    q.data = torch.empty_strided((n if q.M else 0,), (1,), dtype=_u8, device=x.device)
     return q
 
 
@@ -164,7 +166,7 @@ def rms_norm_quant(x, weight, fmt, eps=1e-6, residual=None, scale=None, residual
     """h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight, quantized to fmt ("fp8", "fp8_block"
     or "mxfp8"). x, residual bf16 [..., K], weight bf16 [K]; scale: per-tensor FP8's static scale.
     Returns (codes uint8 [..., K], scales as quant_<fmt> gives them or None, h bf16 or None without a
-    residual). residual_out may be x or residual itself."""
+    residual). residual_out may be x or residual itself. No rows give empty outputs."""
     f = _format(fmt)
     xp, M, K, ld, rp, ldr, wp, h, hp, ldh = _norm_args(x, weight, residual, residual_out)
     dev = x.device
@@ -176,8 +178,12 @@ def rms_norm_quant(x, weight, fmt, eps=1e-6, residual=None, scale=None, residual
         scales = _new(x.shape[:-1] + (K // 128,), _f32, dev)
     if scales is not None:
         sp = scales.data_ptr()
-    _check(lib().fql_rms_norm_quant(f, xp, M, K, ld, rp, ldr, wp, eps, _scale_arg(fmt, scale), codes.data_ptr(), sp,
-                                    hp, ldh, _stream(dev.index)))
+    s = _scale_arg(fmt, scale)
+    if M == 0:
+        _query("fql_operand_bytes", f, 1, K)  # refuses what any other call on this K would
+    else:
+        _check(lib().fql_rms_norm_quant(f, xp, M, K, ld, rp, ldr, wp, eps, s, codes.data_ptr(), sp, hp, ldh,
+                                        _stream(dev.index)))
     return codes, scales, h
 
 
@@ -188,8 +194,9 @@ def rms_norm_operand(x, weight, fmt, eps=1e-6, residual=None, scale=None, residu
     xp, M, K, ld, rp, ldr, wp, h, hp, ldh = _norm_args(x, weight, residual, residual_out)
     s = _scale_arg(fmt, scale)
     q = _new_operand(x, fmt, s)
-    _check(lib().fql_rms_norm_operand(f, xp, M, K, ld, rp, ldr, wp, eps, s, q.data.data_ptr(), q.data.numel(), hp, ldh,
-                                      _stream(x.device.index)))
+    if M > 0:
+        _check(lib().fql_rms_norm_operand(f, xp, M, K, ld, rp, ldr, wp, eps, s, q.data.data_ptr(), q.data.numel(), hp,
+                                          ldh, _stream(x.device.index)))
     return q, h
 
 
@@ -199,7 +206,8 @@ def quant_operand(x, fmt, scale=None):
     xp, M, K, ld = _rows(x, "x")
     s = _scale_arg(fmt, scale)
     q = _new_operand(x, fmt, s)
-    _check(lib().fql_quant_operand(f, xp, M, K, ld, s, q.data.data_ptr(), q.data.numel(), _stream(x.device.index)))
+    if M > 0:
+        _check(lib().fql_quant_operand(f, xp, M, K, ld, s, q.data.data_ptr(), q.data.numel(), _stream(x.device.index)))
     return q
 
 
@@ -230,7 +238,8 @@ def linear_fused(x, weight, activation=None, bias=None, residual=None, alpha=Non
     x: bf16 [..., K], quantized in the call as linear_<fmt> does, or a QuantizedActivation.
     weight: MXFP4Weight, MXFP8Weight, FP8Weight or FP8BlockWeight. activation: None, "relu",
     "gelu", "gelu_tanh", "silu", or "swiglu" (rows interleaved by interleave_gate_up, output
-    [..., N/2]). bias bf16 [N]. residual: bf16 of y's shape; may be `out` itself."""
+    [..., N/2]). bias bf16 [N]. residual: bf16 of y's shape; may be `out` itself. No rows give an
+    empty output."""
     if activation not in ACTIVATIONS:
         raise FQLError(f"unknown activation {activation!r}")
     fmt = getattr(weight, "fmt", None)
@@ -264,6 +273,8 @@ def linear_fused(x, weight, activation=None, bias=None, residual=None, alpha=Non
         yp, ldy = out.data_ptr(), No
     else:
         yp, _, _, ldy = _rows(out, "out", shape, index)
+    if M == 0:
+        return out
     if workspace is None:
         workspace = _workspace(dev, _query("fql_linear_fused_workspace_bytes", FORMATS[fmt], M, N, K))
     else:

@@ -8,7 +8,7 @@ import fp8_quantized_linear_amd as fql
 from oracle import serving as S
 
 from gpu_helpers import announce
-from serving_helpers import (HALF_BF16, assert_attention, bf16, f64, i32, poison, random_cache, tables, to_device)
+from serving_helpers import (DEV, HALF_BF16, assert_attention, bf16, f64, i32, poison, random_cache, tables, to_device)
 from test_gpu_serving import FMTS, SCALE, Decoder, check_norm, layer, operand_rows
 
 pytestmark = pytest.mark.gpu
@@ -152,6 +152,33 @@ def test_the_plan_names_the_kernels_that_run(fmt, M):
     assert len(ran) == len(named), (ran, named)
     for kernel, name in zip(ran, named):
         assert f":{name}<" in kernel, (kernel, name)
+
+
+# ---------------------------------------------------------------------------
+# no tokens
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_calls_on_no_rows_give_empty_outputs(fmt):
+    """A step in which no sequence has a token: a layer goes through it as the cache's calls do."""
+    announce(f"no rows {fmt}")
+    net = Decoder(fmt)
+    h, _ = bf16(np.zeros((3, 512)))
+    cache = fql.KVCache8.empty(2, 2, 16, 64, DEV)
+    y = net(h[:0], cache, i32([[0, 1]]), i32([5]), i32([0, 0]), 1)
+    assert y.shape == (0, 512) and y.dtype is torch.bfloat16 and y.device == h.device
+    sc = 0.1 if fmt == "fp8" else None
+    codes, scales, r = fql.rms_norm_quant(h[:0], net.w1, fmt, residual=h[:0], scale=sc)
+    n = {"fp8": None, "fp8_block": 4, "mxfp8": 16}[fmt]
+    assert codes.shape == (0, 512) and r.shape == (0, 512) and (scales is None if n is None else scales.shape == (0, n))
+    assert fql.linear_fused(h.view(1, 3, 512)[:, :0], net.qkv).shape == (1, 0, 768)
+    assert fql.linear_fused(fql.quant_operand(h[:0], fmt, scale=sc), net.gu, activation="swiglu").shape == (0, 1024)
+    out = h[:0]
+    assert fql.linear_fused(h[:0], net.o, residual=out, out=out) is out
+    with pytest.raises(fql.FQLError, match="multiple"):  # what does not fit is refused all the same
+        fql.rms_norm_quant(h[:0, :500], net.w1[:500], fmt, scale=sc)
+    with pytest.raises(fql.FQLError, match="has K="):
+        fql.linear_fused(h[:0, :256], net.qkv)
 
 
 # ---------------------------------------------------------------------------
