@@ -29,6 +29,7 @@ from . import (FMT_FP8, FMT_FP8_BLOCK, FMT_MXFP4, FMT_MXFP8, FQLError, _captured
                _check, _grow_workspace, _rows_view, _size_query, _workspaces, lib)
 
 FORMATS = {"mxfp4": FMT_MXFP4, "mxfp8": FMT_MXFP8, "fp8": FMT_FP8, "fp8_block": FMT_FP8_BLOCK}
+_I32_MAX = 2 ** 31 - 1
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
 
 # A decode step's calls take a few microseconds on the GPU, so what Python does
@@ -391,11 +392,19 @@ def kv_append(cache, k, v, block_table, lens, cu_seqlens, max_new):
         _check(lib().fql_kv_append(cache._struct, b, kp, kt, kh, vp, vt, vh, _stream(cache._index)))
 
 
+def _within(value, name, lo, hi):
+    """A whole number that the library's C argument holds."""
+    value = int(value)
+    if not lo <= value <= hi:
+        raise FQLError(f"{name} must be in {lo} .. {hi}")
+    return value
+
+
 def attention_kv8_plan(batch, q_heads, kv_heads, head_dim, max_new, max_len, window=0):
     """One-line description of the launch plan of an attention_kv8 call."""
     buf = ctypes.create_string_buffer(256)
     _check(lib().fql_attention_kv8_describe(int(batch), int(q_heads), int(kv_heads), int(head_dim), int(max_new),
-                                            int(max_len), int(window), buf, 256))
+                                            int(max_len), _within(window, "window", 0, _I32_MAX), buf, 256))
     return buf.value.decode()
 
 
@@ -423,8 +432,12 @@ def attention_kv8(q, cache, block_table, lens, cu_seqlens, max_new, causal=True,
         lp = lse.data_ptr()
     b, B, cols, new = _batch(cache, block_table, lens, cu_seqlens, max_new, T)
     if T > 0:
+        if window:
+            window = _within(window, "window", 0, _I32_MAX)
         if max_len is None:
             max_len = cols * cache.block_size
+        else:
+            max_len = _within(max_len, "max_len", 1, 1 << 30)
         if workspace is None:
             workspace = _workspace(dev, _query("fql_attention_kv8_workspace_bytes", B, Hq, cache.kv_heads, D, new,
                                                max_len, window))

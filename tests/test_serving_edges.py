@@ -3,6 +3,7 @@
 import ctypes
 import types
 
+import numpy as np
 import pytest
 import torch
 
@@ -126,3 +127,30 @@ def test_attention_refuses_output_rows_that_overlap(tokens, heads):
     refused(attend_out(tokens, heads, big, 64), "workspace", code=-4)
     refused(attend_out(tokens, heads, 64 * heads, big), "workspace", code=-4)
     refused(attend_out(tokens, heads, big, 0), "overlap")
+
+
+def test_attention_host_arguments_do_not_wrap(monkeypatch):
+    """window and max_len reach the library as C integers: what those cannot hold is refused, and any
+    kind of whole number is taken."""
+    def u8(*shape):
+        return OnDevice.make(torch.zeros(shape, dtype=torch.uint8), 0)
+
+    def i32(*values):
+        return OnDevice.make(torch.tensor(values, dtype=torch.int32), 0)
+
+    c = fql.KVCache8(u8(2, 1, 16, 64), u8(2, 1, 1, 64, 16), u8(2, 1), u8(2, 1))
+    args = (bf16(0, 1, 2, 64), c, i32([0, 1]), i32(1), i32(0, 1), 1)
+    for bad in (2 ** 32, 2 ** 32 + 5, 2 ** 31, -1, -2 ** 40):
+        with pytest.raises(fql.FQLError, match="window"):
+            fql.attention_kv8(*args, out=bf16(0, 1, 2, 64), window=bad)
+        with pytest.raises(fql.FQLError, match="window"):
+            fql.attention_kv8_plan(1, 2, 1, 64, 1, 32, window=bad)
+    for bad in (0, -1, 2 ** 64 + 5, 2 ** 31):
+        with pytest.raises(fql.FQLError, match="max_len"):
+            fql.attention_kv8(*args, out=bf16(0, 1, 2, 64), max_len=bad)
+    # numpy's and torch's numbers: as far as the workspace, which is too small
+    ws = u8(4096)
+    monkeypatch.setattr(fql.serving, "_stream", lambda index: 0)
+    for number in (np.int64, torch.tensor):
+        with pytest.raises(fql.FQLError, match="workspace"):
+            fql.attention_kv8(*args, out=bf16(0, 1, 2, 64), window=number(8), max_len=number(32), workspace=ws)
