@@ -1,5 +1,7 @@
 """Edges of the 8-bit serving operators (GPU)."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -152,6 +154,20 @@ def test_the_plan_names_the_kernels_that_run(fmt, M):
     assert len(ran) == len(named), (ran, named)
     for kernel, name in zip(ran, named):
         assert f":{name}<" in kernel, (kernel, name)
+
+
+@pytest.mark.parametrize("M", [2, 80])
+def test_gelu_tail(M):
+    """The negative tail keeps its relative precision down to bf16's smallest normal values: its
+    float32 evaluation is off by at most 1e-5 (a^2 / 2 <= 84 rounded, times 2^-23), bf16 by 2^-8."""
+    announce(f"GELU tail M={M}")
+    K, N = 128, 256
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device=DEV)
+    g, _ = layer("mxfp8", np.zeros((N, K)))
+    b, z = bf16(-np.linspace(0.01, 12.9, N))
+    y = f64(fql.linear_fused(x, g, activation="gelu", bias=b))
+    want = np.array([[t / 2 * math.erfc(-t / math.sqrt(2)) for t in z]])  # 1 + erf cancels
+    assert (np.abs(y - want) <= (HALF_BF16 + 1e-5) * np.abs(want)).all()
 
 
 # ---------------------------------------------------------------------------
