@@ -20,6 +20,7 @@ and the shape [*x.shape[:-1], N].
 import ctypes
 import os
 import threading
+import weakref
 
 import torch
 
@@ -507,7 +508,7 @@ def linear_plan(M, N, K, aligned=True, transform=False, hadamard_block=0):
 
 
 _workspaces = {}  # of eager calls: (device type, index, stream) -> buffer
-_outgrown = []    # replaced ones
+_outgrown = weakref.WeakSet()  # replaced ones that something else still holds
 _captured = {}    # of a stream's newest graph capture: the same key -> (capture id, buffer)
 _COUNTER_BYTES = 64 << 10      # leading part of a workspace that has to start at zero
 _CAPTURED_BYTES = 16 << 20     # serves the layers of a step of up to a hundred tokens: one clearing a graph
@@ -533,14 +534,15 @@ def _workspace(device, nbytes):
 
 
 def _grow_workspace(key, nbytes, device):
-    """A new workspace for `key`, at least twice as large as the one it replaces: those are kept,
-    and so hold no more than the newest in all."""
+    """A new workspace for `key`, at least twice as large as the one it replaces. That one goes back to
+    the allocator, which hands it out in the order of its stream: calls in flight still have it, and
+    no graph does (a capture has a workspace of its own)."""
     old = _workspaces.get(key)
     if old is not None:
         nbytes = max(nbytes, 2 * old.numel())
     ws = new_workspace(nbytes, device)
     if old is not None:
-        _outgrown.append(old)
+        _outgrown.add(old)
     _workspaces[key] = ws
     return ws
 

@@ -2,6 +2,7 @@
 
 import ctypes
 import types
+import weakref
 
 import numpy as np
 import pytest
@@ -154,3 +155,19 @@ def test_attention_host_arguments_do_not_wrap(monkeypatch):
     for number in (np.int64, torch.tensor):
         with pytest.raises(fql.FQLError, match="workspace"):
             fql.attention_kv8(*args, out=bf16(0, 1, 2, 64), window=number(8), max_len=number(32), workspace=ws)
+
+
+def test_a_replaced_workspace_is_given_back():
+    """Growing keeps nothing of the old buffer: no graph uses an eager workspace."""
+    key, device = ("cpu", None, -1), torch.device("cpu")
+    try:
+        sizes = []
+        for need in (1 << 20, 3 << 20, 4 << 20, 1):
+            old = fql._workspaces.get(key)
+            gone = [] if old is None else [weakref.ref(old)]
+            sizes.append(fql._grow_workspace(key, need, device).numel())
+            del old
+            assert all(r() is None for r in gone)
+        assert sizes == [1 << 20, 3 << 20, 6 << 20, 12 << 20]
+    finally:
+        fql._workspaces.pop(key, None)
