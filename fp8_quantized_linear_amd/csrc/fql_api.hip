@@ -1142,6 +1142,18 @@ bool rows_overlap(int64_t T, int64_t lt, int64_t H, int64_t lh, int64_t D) {
   return false;
 }
 
+// Whether x [M][K] and y [M][N] (bf16, row strides ldx and ldy) may share an element: exact for
+// columns of one buffer, where the strides are equal.
+bool matrices_overlap(const void* x, int64_t K, int64_t ldx, const void* y, int64_t N, int64_t ldy, int64_t M) {
+  typedef __int128 wide;
+  const wide a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  const wide rx = 2 * ((wide)(M - 1) * ldx + K), ry = 2 * ((wide)(M - 1) * ldy + N);
+  if (a + rx <= b || b + ry <= a) return false;
+  if (M == 1 || ldx != ldy) return true;
+  const wide pitch = 2 * (wide)ldx, d = ((b - a) % pitch + pitch) % pitch;
+  return d < 2 * (wide)K || d + 2 * (wide)N > pitch;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1248,6 +1260,8 @@ int fql_linear_fused(int format, const void* x, int64_t M, int64_t K, int64_t ld
       return fail(FQL_ERR_INVALID, "too many output tiles for the arrival counters");
     if (plan.Mp * (plan.groups > 0 ? fql::round_up(K, 128) / 32 : 0) > ((int64_t)1 << 31) - 4096)
       return fail(FQL_ERR_INVALID, "activation too large");
+    // small M quantizes x in every workgroup, beside the ones that already write y
+    if (x && matrices_overlap(x, K, M > 1 ? ldx : K, y, Nout, ldy, M)) return fail(FQL_ERR_INVALID, "y overlaps x");
     const fql::ScEpilogue epi = {activation, static_cast<const uint16_t*>(residual), ldr};
     return hip_status(
         fql::launch_sc_linear_fused(plan, static_cast<const uint16_t*>(x), M, K, ldx, x && aligned16(x, ldx, 2), inv,

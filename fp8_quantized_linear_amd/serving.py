@@ -239,8 +239,8 @@ def linear_fused(x, weight, activation=None, bias=None, residual=None, alpha=Non
     x: bf16 [..., K], quantized in the call as linear_<fmt> does, or a QuantizedActivation.
     weight: MXFP4Weight, MXFP8Weight, FP8Weight or FP8BlockWeight. activation: None, "relu",
     "gelu", "gelu_tanh", "silu", or "swiglu" (rows interleaved by interleave_gate_up, output
-    [..., N/2]). bias bf16 [N]. residual: bf16 of y's shape; may be `out` itself. No rows give an
-    empty output."""
+    [..., N/2]). bias bf16 [N]. residual: bf16 of y's shape; may be `out` itself, `x` may not. No rows
+    give an empty output."""
     if activation not in ACTIVATIONS:
         raise FQLError(f"unknown activation {activation!r}")
     fmt = getattr(weight, "fmt", None)

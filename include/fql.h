@@ -546,6 +546,7 @@ int fql_quant_operand(int format, const void* x, int64_t M, int64_t K, int64_t l
  *              in groups of 16 gate rows followed by their 16 up rows, N is a
  *              multiple of 32, and y and residual have N / 2 columns.
  *   residual   [M][ldr] bf16 or NULL; may be y itself (same pointer, stride).
+ *   y          must not overlap x (workgroups read x while others write y).
  *   workspace  as fql_linear_<format>, of fql_linear_fused_workspace_bytes. The
  *              call has launch plans of its own, so its float32 sum over K may
  *              be in another order than fql_linear_<format>'s.

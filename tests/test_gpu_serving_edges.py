@@ -170,6 +170,23 @@ def test_gelu_tail(M):
     assert (np.abs(y - want) <= (HALF_BF16 + 1e-5) * np.abs(want)).all()
 
 
+@pytest.mark.parametrize("M", [1, 5, 40])
+def test_linear_reads_and_writes_columns_of_one_buffer(M):
+    """x and out in the same rows of one buffer, side by side in either order, do not overlap."""
+    announce(f"columns of one buffer M={M}")
+    rng = np.random.default_rng([28, M])
+    g, _ = layer("mxfp8", rng.standard_normal((64, 128)) * 0.1)
+    x, _ = bf16(rng.standard_normal((M, 128)))
+    want = fql.linear_fused(x, g)
+    for x0, y0 in ((0, 128), (64, 0)):
+        both = torch.full((M, 192), 3.0, dtype=torch.bfloat16, device=DEV)
+        both[:, x0:x0 + 128] = x
+        out = fql.linear_fused(both[:, x0:x0 + 128], g, out=both[:, y0:y0 + 64])
+        assert torch.equal(out, want) and torch.equal(both[:, x0:x0 + 128], x)
+    with pytest.raises(fql.FQLError, match="overlap"):
+        fql.linear_fused(both[:, 64:], g, out=both[:, 32:96])
+
+
 # ---------------------------------------------------------------------------
 # no tokens
 # ---------------------------------------------------------------------------

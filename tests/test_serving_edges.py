@@ -171,3 +171,20 @@ def test_a_replaced_workspace_is_given_back():
         assert sizes == [1 << 20, 3 << 20, 6 << 20, 12 << 20]
     finally:
         fql._workspaces.pop(key, None)
+
+
+@pytest.mark.parametrize("M", [1, 4, 40])
+def test_linear_refuses_an_output_that_overlaps_its_input(M):
+    """x [M, 128] and y [M, 64] at distances (in elements) and strides where they share elements."""
+    def at(offset):
+        return ctypes.c_void_p((1 << 20) + 2 * offset)
+
+    def call(y, ldx, ldy):
+        return fql.lib().fql_linear_fused(fql.FMT_MXFP8, at(0), M, 128, ldx, 0.0, NULL, ctypes.c_void_p(1 << 24), 64, 1.0, NULL,
+                                          NULL, 0, NULL, 0, at(y), ldy, ctypes.c_void_p(1 << 25), 1 << 26, NULL)
+
+    for y, ldx, ldy in ((0, 128, 64), (127, 128, 64), (-63, 128, 64), (0, 128, 128), (64, 192, 192)):
+        refused(call(y, ldx, ldy), "overlaps")
+    if M > 1:
+        for y, ldx, ldy in ((192 - 1, 192, 192), (-64, 191, 191), (128 + 1, 192, 192), (130, 192, 200), (191, 256, 64)):
+            refused(call(y, ldx, ldy), "overlaps")
