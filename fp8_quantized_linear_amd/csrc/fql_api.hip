@@ -1050,6 +1050,24 @@ int check_operand(int fmt, int64_t M, int64_t K, const void* operand, size_t byt
   return FQL_OK;
 }
 
+// Whether x [M][K] and y [M][N] (bf16, row strides ldx and ldy) may share an element: exact for
+// columns of one buffer, where the strides are equal.
+bool matrices_overlap(const void* x, int64_t K, int64_t ldx, const void* y, int64_t N, int64_t ldy, int64_t M) {
+  typedef __int128 wide;
+  const wide a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+  const wide rx = 2 * ((wide)(M - 1) * ldx + K), ry = 2 * ((wide)(M - 1) * ldy + N);
+  if (a + rx <= b || b + ry <= a) return false;
+  if (M == 1 || ldx != ldy) return true;
+  const wide pitch = 2 * (wide)ldx, d = ((b - a) % pitch + pitch) % pitch;
+  return d < 2 * (wide)K || d + 2 * (wide)N > pitch;
+}
+
+// An output that may be one of its inputs, element for element, but not overlap it otherwise.
+bool overlaps_shifted(const void* in, int64_t ld_in, const void* out, int64_t ld_out, int64_t N, int64_t M) {
+  if (!in || !out || (in == out && (M == 1 || ld_in == ld_out))) return false;
+  return matrices_overlap(in, N, ld_in, out, N, ld_out, M);
+}
+
 int rms_norm(int format, bool to_operand, const void* x, int64_t M, int64_t K, int64_t ldx, const void* residual,
              int64_t ldr, const void* weight, float eps, float scale, uint8_t* codes, void* scales,
              size_t operand_bytes, void* h_out, int64_t ldh, void* stream) {
@@ -1062,6 +1080,8 @@ int rms_norm(int format, bool to_operand, const void* x, int64_t M, int64_t K, i
   if (h_out && !residual) return fail(FQL_ERR_INVALID, "h_out needs a residual");
   if (h_out && ldh < K) return fail(FQL_ERR_INVALID, "h_out row stride %lld is smaller than K", (long long)ldh);
   if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(FQL_ERR_INVALID, "eps must be finite and >= 0");
+  if (overlaps_shifted(x, ldx, h_out, ldh, K, M) || overlaps_shifted(residual, ldr, h_out, ldh, K, M))
+    return fail(FQL_ERR_INVALID, "h_out overlaps another row or column of x or residual");
   fql::NormArgs a{};
   if (int r = inverse_scale(fmt, scale, "scale", &a.inv_scale)) return r;
   if (to_operand) {
@@ -1140,18 +1160,6 @@ bool rows_overlap(int64_t T, int64_t lt, int64_t H, int64_t lh, int64_t D) {
       if (dt < T && (a > dt * lt ? a - dt * lt : dt * lt - a) < D) return true;
   }
   return false;
-}
-
-// Whether x [M][K] and y [M][N] (bf16, row strides ldx and ldy) may share an element: exact for
-// columns of one buffer, where the strides are equal.
-bool matrices_overlap(const void* x, int64_t K, int64_t ldx, const void* y, int64_t N, int64_t ldy, int64_t M) {
-  typedef __int128 wide;
-  const wide a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-  const wide rx = 2 * ((wide)(M - 1) * ldx + K), ry = 2 * ((wide)(M - 1) * ldy + N);
-  if (a + rx <= b || b + ry <= a) return false;
-  if (M == 1 || ldx != ldy) return true;
-  const wide pitch = 2 * (wide)ldx, d = ((b - a) % pitch + pitch) % pitch;
-  return d < 2 * (wide)K || d + 2 * (wide)N > pitch;
 }
 
 }  // namespace
@@ -1261,6 +1269,7 @@ int fql_linear_fused(int format, const void* x, int64_t M, int64_t K, int64_t ld
     if (plan.Mp * (plan.groups > 0 ? fql::round_up(K, 128) / 32 : 0) > ((int64_t)1 << 31) - 4096)
       return fail(FQL_ERR_INVALID, "activation too large");
     // small M quantizes x in every workgroup, beside the ones that already write y
+    if (overlaps_shifted(residual, ldr, y, ldy, Nout, M)) return fail(FQL_ERR_INVALID, "y overlaps another row or column of residual");
     if (x && matrices_overlap(x, K, M > 1 ? ldx : K, y, Nout, ldy, M)) return fail(FQL_ERR_INVALID, "y overlaps x");
     const fql::ScEpilogue epi = {activation, static_cast<const uint16_t*>(residual), ldr};
     return hip_status(

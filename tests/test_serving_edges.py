@@ -10,7 +10,7 @@ import torch
 
 import fp8_quantized_linear_amd as fql
 
-from test_serving_api import NULL, P, batch, cache, refused
+from test_serving_api import FP8, NULL, P, batch, cache, linear, norm, refused
 
 
 def test_capture_id_refusals():
@@ -188,3 +188,20 @@ def test_linear_refuses_an_output_that_overlaps_its_input(M):
     if M > 1:
         for y, ldx, ldy in ((192 - 1, 192, 192), (-64, 191, 191), (128 + 1, 192, 192), (130, 192, 200), (191, 256, 64)):
             refused(call(y, ldx, ldy), "overlaps")
+
+
+def test_outputs_that_are_an_input_shifted_are_refused():
+    """h_out may be x or residual itself and y may be residual itself, not a neighbouring row or column of it."""
+    def at(offset):
+        return ctypes.c_void_p((1 << 20) + 2 * offset)
+
+    far = ctypes.c_void_p(1 << 28)
+    for h, ldh in ((1, 256), (256, 256), (-256, 256), (0, 257), (300, 512), (255, 511)):
+        for args in (dict(x=at(0), res=far), dict(x=far, res=at(0))):
+            refused(norm(**args, h=at(h), ldh=ldh), "h_out overlaps")
+    for y, ldy in ((1, 64), (64, 64), (-64, 64), (0, 65), (80, 128)):
+        refused(linear(x=far, res=at(0), ldr=64, y=at(y), ldy=ldy), "y overlaps")
+    # itself, as far as the next check
+    for args in (dict(x=at(0), res=far), dict(x=far, res=at(0)), dict(x=at(0), res=at(0))):
+        refused(norm(**args, h=at(0), fmt=FP8, scale=0.0), "scale")
+    refused(linear(x=at(0), ldx=256, res=at(0), ldr=64, y=at(0)), "y overlaps x")
