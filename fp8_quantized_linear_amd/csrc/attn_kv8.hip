@@ -8,7 +8,10 @@
 // scales (powers of two) go into the scores and the weights p in float32.
 // Scores, running maximum, running sum and output accumulators are float32;
 // p (times its block's value scale, exact) is rounded to bf16 for the second
-// product, the sum takes it unrounded.
+// product, which is how the matrix cores take it at full rate; the sum takes it
+// unrounded. Against 64 bits the outputs are then off by 0.0019 to 0.0023 of their
+// norm, where float32 weights give 0.0016 to 0.0017, most of it the output's own
+// rounding.
 //
 // Both products use one trick to keep p in registers. The first computes
 // S^T = K Q^T, so a lane holds scores of one query row (its column) and of
@@ -320,7 +323,9 @@ __device__ void put_nan_rows(const AttnArgs& a, const PagedCache& c, const Paged
 // per wave is always in flight and no barrier is in the loop.
 //
 // Bound by memory: 64 sequences of up to 16384 tokens, 64 query and 8 kv heads
-// of 128 channels: 1.34 GB in 257 us, 5.2 TB/s (a large copy: 5.0). One
+// of 128 channels: 1.34 GB in 246 to 259 us, 5.2 to 5.4 TB/s (a large copy: 5.0, a
+// bare read: 6.6). Part of the distance is the end, where the longest sequences
+// run alone: 64 equal ones of 16384 reach 5.6 (head_dim 64 5.2, 256 5.8). One
 // sequence of 1000 tokens is a chain of dependent accesses (lengths, table,
 // keys, values, partial results, arrival, join): 8.9 us for 2 MB.
 //
@@ -615,10 +620,11 @@ __global__ __launch_bounds__(64 * stream_waves(D, NC)) void attn_kv8_stream_kern
 // Bound by the issue of vector instructions beside the matrix ones: a wave's 32
 // products of a tile take 1024 cycles, its 32 exponentials 512 and the rest of
 // the softmax, widening and addressing 500 to 740. 8192 causal tokens, 32 query
-// and 8 kv heads of 128 channels: 570 us, 965 TFLOP/s (a large bf16 matrix
-// product: 1140); four prompts of up to 2048 tokens 99 us, 725 TFLOP/s, the
-// starts and ends of their short workgroups being the rest; head_dim 64 630
-// TFLOP/s (per product the softmax weighs twice), 256 565 (one workgroup a CU).
+// and 8 kv heads of 128 channels: 570 to 640 us by the card and its clock, 860
+// to 965 TFLOP/s (a large bf16 matrix product: 1140); four prompts of up to 2048
+// tokens 99 us, 725 TFLOP/s, the starts and ends of their short workgroups being
+// the rest; head_dim 64 630 to 700 TFLOP/s (per product the softmax weighs twice),
+// 256 700 (one workgroup a CU).
 // Tried at this size and slower: scales folded into the widening (640 us), the
 // softmax interleaved with the products by hand, waves with raised priority.
 template <int D, int NW>
@@ -982,7 +988,9 @@ AttnPlan plan_attention(int B, int Hq, int Hkv, int D, int64_t max_new, int64_t 
     }
   } else {
     // many rows: four rounds of workgroups (sequences differ in length), of at
-    // least 2048 keys. 512 and 274 new tokens on 32768 and 17579, 64 heads: 1.03
+    // least 2048 keys, which was measured where the tiles fill the card: with few
+    // tiles shorter ranges would use more of it (8 tokens, 64 heads, on 4096 keys
+    // 58 us in two ranges; 4 tokens, in the other kernel, 19). 512 and 274 new tokens on 32768 and 17579, 64 heads: 1.03
     // ms whole, 1.00 in two ranges, 0.85 in four, 0.82 in eight; 512 each on
     // 32768: 1.14 in two and four, 1.17 in eight, 1.26 in ranges of 2048.
     splits = std::max<int64_t>(1, std::min<int64_t>((2048 + tiles - 1) / tiles, span / 2048));

@@ -202,10 +202,12 @@ __device__ __forceinline__ void finish_vec(const NormArgs& a, int64_t m, int64_t
 // thread). STREAM: rows too long for that read x and the residual twice.
 //
 // Bound by memory where there are many rows: 8192 x 5120 block FP8 with a
-// residual moves 294 MB in 58 us, 5.1 TB/s, what a large copy reaches. Few rows
-// are one dependent chain (load, reduce, barrier, encode): one row of 4096 takes
-// 3.7 us, 333 x 5120 MXFP8 7.1 us (1.7 TB/s; two vectors a thread, so that one
-// row's chain is short and its loads are all in flight at once).
+// residual moves 294 MB in 54 to 58 us, 5.1 TB/s, what a large copy reaches (with
+// the exact codes MXFP8 takes 60.5 us, FP8 61 to 67; into the operand, whose 16-byte
+// pieces L2 joins, block FP8 63.5, FP8 65, MXFP8 70). Few rows are one dependent
+// chain (load, reduce, barrier, encode): one row of 4096 takes 3.8 us, 333 x 5120
+// MXFP8 7.9 us (two vectors a thread, so that one row's chain is short and its
+// loads are all in flight at once).
 template <int F, bool OP, int I, bool WAVE, bool STREAM>
 __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, const NormFlags f) {
   __shared__ double red[16];
@@ -290,7 +292,7 @@ __global__ __launch_bounds__(1024) void rms_norm_quant_kernel(const NormArgs a, 
   };
   // Block FP8, whose codes are those of a float32 y, sums in float32 and again in
   // float64 where the squares leave float32's range (float64 at once takes 8192 x
-  // 5120 from 55.5 to 57.5 us).
+  // 5120 from 56 to 57.5 us).
   std::conditional_t<F == SC_FP8_BLOCK, float, double> rinv;
   if constexpr (F == SC_FP8_BLOCK) {
     const float ss = squares(0.0f, red32);

@@ -585,9 +585,11 @@ typedef struct {
  * first of n new tokens has position lens[b] - n. Row b of block_table names
  * the blocks of the sequence in order. The arrays are device memory that the
  * host does not read: row ranges are clamped to `tokens`, lengths to the
- * table's capacity, tokens at negative positions are ignored, and a block
- * number outside the cache is never followed (its tokens are not written, and
- * attention takes them as absent).
+ * table's capacity, and a block number outside the cache is never followed (its
+ * tokens are not written, and attention takes them as absent). New tokens at
+ * negative positions (more new ones than lens[b]) are not written; in
+ * attention they see no key under a causal mask, and like any other all
+ * lens[b] keys without one.
  */
 typedef struct {
   const int32_t* block_table; /* [batch][ld_table], table_cols <= ld_table columns used */
