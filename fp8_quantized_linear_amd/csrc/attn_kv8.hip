@@ -990,8 +990,8 @@ AttnPlan plan_attention(int B, int Hq, int Hkv, int D, int64_t max_new, int64_t 
     // many rows: four rounds of workgroups (sequences differ in length), of at
     // least 2048 keys, which was measured where the tiles fill the card: with few
     // tiles shorter ranges would use more of it (8 tokens, 64 heads, on 4096 keys
-    // 58 us in two ranges; 4 tokens, in the other kernel, 19). 512 and 274 new tokens on 32768 and 17579, 64 heads: 1.03
-    // ms whole, 1.00 in two ranges, 0.85 in four, 0.82 in eight; 512 each on
+    // 58 us in two ranges; 4 tokens, in the other kernel, 19). 512 and 274 new
+    // tokens on 32768 and 17579, 64 heads: 1.03 ms whole, 1.00 in two ranges, 0.85 in four, 0.82 in eight; 512 each on
     // 32768: 1.14 in two and four, 1.17 in eight, 1.26 in ranges of 2048.
     splits = std::max<int64_t>(1, std::min<int64_t>((2048 + tiles - 1) / tiles, span / 2048));
   }

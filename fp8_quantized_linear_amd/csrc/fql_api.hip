@@ -1268,8 +1268,9 @@ int fql_linear_fused(int format, const void* x, int64_t M, int64_t K, int64_t ld
       return fail(FQL_ERR_INVALID, "too many output tiles for the arrival counters");
     if (plan.Mp * (plan.groups > 0 ? fql::round_up(K, 128) / 32 : 0) > ((int64_t)1 << 31) - 4096)
       return fail(FQL_ERR_INVALID, "activation too large");
+    if (overlaps_shifted(residual, ldr, y, ldy, Nout, M))
+      return fail(FQL_ERR_INVALID, "y overlaps another row or column of residual");
     // small M quantizes x in every workgroup, beside the ones that already write y
-    if (overlaps_shifted(residual, ldr, y, ldy, Nout, M)) return fail(FQL_ERR_INVALID, "y overlaps another row or column of residual");
     if (x && matrices_overlap(x, K, M > 1 ? ldx : K, y, Nout, ldy, M)) return fail(FQL_ERR_INVALID, "y overlaps x");
     const fql::ScEpilogue epi = {activation, static_cast<const uint16_t*>(residual), ldr};
     return hip_status(

@@ -10,9 +10,9 @@
 // Roundings: h is rounded to bf16 only where it is stored; the norm and the
 // quantizer take the unrounded float32 sum. The sum of squares and the row's
 // factor 1 / sqrt(..) are float64 (block FP8: float32 while they stay well inside
-// its range), y is float32. Where the codes of FP8 and MXFP8 could differ for a y off by its
-// rounding, they are made again from float64 (exact_codes): an MXFP8 code
-// carries one rounding, its own, an FP8 code that of fl32(1 / scale) besides.
+// its range), y is float32. Where the codes of FP8 and MXFP8 could differ for a
+// y off by its rounding, they are made again from float64 (exact_codes): an MXFP8
+// code carries one rounding, its own, an FP8 code that of fl32(1 / scale) besides.
 // The codes of block FP8 are those of the float32 y over the float32 scale.
 //
 // A y that is not a number (a NaN or infinity in its row, 0 / 0 in an all-zero
