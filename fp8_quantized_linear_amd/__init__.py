@@ -65,6 +65,11 @@ __all__ = [
     "pack_weight_fp8_block",
     "linear_fp8_block",
     "FP8BlockWeight",
+    "quant_int8",
+    "quant_int8_weight",
+    "pack_weight_int8",
+    "linear_int8",
+    "INT8Weight",
     "fp8_scale_from_amax",
     "linear_sc_plan",
     "linear_sc_workspace_bytes",
@@ -101,6 +106,7 @@ FMT_MXFP4 = 2
 FMT_MXFP8 = 3
 FMT_FP8 = 4
 FMT_FP8_BLOCK = 5
+FMT_INT8 = 6
 
 _c_int, _c_i64, _c_f32, _c_vp, _c_sz = (ctypes.c_int, ctypes.c_int64, ctypes.c_float,
                                          ctypes.c_void_p, ctypes.c_size_t)
@@ -146,6 +152,14 @@ SIGNATURES = {
     "fql_linear_fp8_block_describe": (_c_int, [_c_i64, _c_i64, _c_i64, ctypes.c_char_p, _c_sz]),
     "fql_linear_fp8_block": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_f32, _c_vp,
                                       _c_vp, _c_i64, _c_vp, _c_sz, _c_vp]),
+    "fql_quant_int8": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
+    "fql_quant_int8_f32": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
+    "fql_packed_int8_bytes": (_c_int, [_c_i64, _c_i64, ctypes.POINTER(_c_sz)]),
+    "fql_pack_weight_int8": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_sz, _c_vp]),
+    "fql_linear_int8_workspace_bytes": (_c_int, [_c_i64, _c_i64, _c_i64, ctypes.POINTER(_c_sz)]),
+    "fql_linear_int8_describe": (_c_int, [_c_i64, _c_i64, _c_i64, ctypes.c_char_p, _c_sz]),
+    "fql_linear_int8": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_i64, _c_f32, _c_vp,
+                                 _c_vp, _c_i64, _c_vp, _c_sz, _c_vp]),
     "fql_transform_bf16": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_int, _c_vp, _c_i64,
                                     _c_vp]),
     "fql_quant_nvfp4_transform": (_c_int, [_c_vp, _c_i64, _c_i64, _c_i64, _c_f32, _c_vp, _c_int,
@@ -738,10 +752,10 @@ def quant_nvfp4_dynamic(x, T=None, hadamard_block=0):
 
 
 # ---------------------------------------------------------------------------
-# scaled-MFMA formats: MXFP4, MXFP8 (E8M0 per 32), per-tensor FP8, block FP8
+# scaled-MFMA formats: MXFP4, MXFP8 (E8M0 per 32), per-tensor FP8, block FP8; INT8
 # ---------------------------------------------------------------------------
 
-_SC = {"mxfp4": "mxfp4", "mxfp8": "mxfp8", "fp8": "fp8", "fp8_block": "fp8_block"}
+_SC = {"mxfp4": "mxfp4", "mxfp8": "mxfp8", "fp8": "fp8", "fp8_block": "fp8_block", "int8": "int8"}
 
 
 def _fn(name):
@@ -765,12 +779,15 @@ def _quant_sc(fmt, x, name, dtype, fn, scale=None, weight_tiles=False):
     x2, ld = _rows_view(x, name)
     M, K = x2.shape
     lead = tuple(x.shape[:-1])
-    codes = torch.empty(_sc_codes_shape(fmt, lead, K), dtype=torch.uint8, device=x.device)
+    codes = torch.empty(_sc_codes_shape(fmt, lead, K), dtype=torch.int8 if fmt == "int8" else torch.uint8,
+                        device=x.device)
     if fmt in ("mxfp4", "mxfp8"):
         scales = torch.empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
     elif fmt == "fp8_block":
         shape = (M // 128, K // 128) if weight_tiles else lead + (K // 128,)
         scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+    elif fmt == "int8":
+        scales = torch.empty(lead, dtype=torch.float32, device=x.device)
     else:
         scales = None
     if fmt == "fp8":
@@ -819,6 +836,16 @@ def quant_fp8_block_weight(w):
                      weight_tiles=True)
 
 
+def quant_int8(x):
+    """INT8 of bf16 x [..., K], one scale a token: (codes int8 [..., K], scales float32 [...])."""
+    return _quant_sc("int8", x, "x", torch.bfloat16, _fn("fql_quant_int8"))
+
+
+def quant_int8_weight(w):
+    """INT8 of float32 weights w [N, K], one scale a channel: (codes int8 [N, K], scales float32 [N])."""
+    return _quant_sc("int8", w, "w", torch.float32, _fn("fql_quant_int8_f32"))
+
+
 def fp8_scale_from_amax(amax_value):
     """The per-tensor FP8 calibration scale fl32(amax / 448) (1 when that is 0), from
     the library (host-side)."""
@@ -839,6 +866,8 @@ def _pack_sc(fmt, codes, scales, out):
         raise FQLError("scales must be [N, K/32]")
     if fmt == "fp8_block" and (tuple(scales.shape) != (N // 128, K // 128) or scales.dtype != torch.float32):
         raise FQLError("scales must be float32 [N/128, K/128]")
+    if fmt == "int8" and (codes.dtype != torch.int8 or tuple(scales.shape) != (N,) or scales.dtype != torch.float32):
+        raise FQLError("codes must be int8 [N, K] and scales float32 [N]")
     nbytes = _size_query(f"fql_packed_{fmt}_bytes", N, K)
     if out is None:
         out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
@@ -869,6 +898,11 @@ def pack_weight_fp8(codes, out=None):
 def pack_weight_fp8_block(codes, scales, out=None):
     """Re-lay block FP8 weight (codes [N, K], float32 scales [N/128, K/128]) for the GEMM."""
     return _pack_sc("fp8_block", codes, scales, out)[0]
+
+
+def pack_weight_int8(codes, scales, out=None):
+    """Re-lay canonical INT8 weight (codes int8 [N, K], float32 scales [N]) for the GEMM."""
+    return _pack_sc("int8", codes, scales, out)[0]
 
 
 class _ScWeight:
@@ -912,6 +946,16 @@ class FP8BlockWeight(_ScWeight):
     def from_float(cls, w):
         codes, scales = quant_fp8_block_weight(w)
         return cls(pack_weight_fp8_block(codes, scales), w.shape[0], w.shape[1])
+
+
+class INT8Weight(_ScWeight):
+    """A packed INT8 weight [N, K] with one scale a channel (inside the blob)."""
+    fmt = "int8"
+
+    @classmethod
+    def from_float(cls, w):
+        codes, scales = quant_int8_weight(w)
+        return cls(pack_weight_int8(codes, scales), w.shape[0], w.shape[1])
 
 
 class FP8Weight(_ScWeight):
@@ -1023,6 +1067,11 @@ def linear_fp8_block(x, weight, alpha=1.0, bias=None, out=None, workspace=None):
     return _linear_sc("fp8_block", x, weight, alpha, bias, out, workspace)
 
 
+def linear_int8(x, weight, alpha=1.0, bias=None, out=None, workspace=None):
+    """y = bf16(alpha * s_x s_w (int8(x) @ W_q^T) + bias), s_x a token's scale, s_w a channel's."""
+    return _linear_sc("int8", x, weight, alpha, bias, out, workspace)
+
+
 # ---------------------------------------------------------------------------
 # warmup
 # ---------------------------------------------------------------------------
@@ -1038,7 +1087,7 @@ def warmup(layers, token_counts, device=None):
     """Run every distinct (format, N, K, M) linear call once on zeros.
 
     `layers` holds packed weights (NVFP4Weight, MXFP4Weight, MXFP8Weight,
-    FP8Weight, FP8BlockWeight); layers with the same format and shape are
+    FP8Weight, FP8BlockWeight, INT8Weight); layers with the same format and shape are
     warmed once (the B12X write-up dedupes warmup layers by signature). This loads
     the kernels' code objects and leaves the per-stream workspace sized for
     the largest call, so later calls (and graph captures) allocate nothing.
@@ -1056,7 +1105,7 @@ def warmup(layers, token_counts, device=None):
             dev = device or w.packed.device
             x = torch.zeros((int(M), w.K), dtype=torch.bfloat16, device=dev)
             fn = {"nvfp4": linear_nvfp4, "mxfp4": linear_mxfp4, "mxfp8": linear_mxfp8,
-                  "fp8": linear_fp8, "fp8_block": linear_fp8_block}[fmt]
+                  "fp8": linear_fp8, "fp8_block": linear_fp8_block, "int8": linear_int8}[fmt]
             fn(x, w)
             calls += 1
     return calls

@@ -208,6 +208,11 @@ int fql_can_implement(int format, int64_t N, int64_t K, int hadamard_block, char
     if (N < 128 || N % 128 != 0) why = "N must be a positive multiple of 128 (weight group 128 x 128)";
     else if (K < 128 || K % 128 != 0) why = "K must be a positive multiple of 128 (activation group 1 x 128)";
     else if (hadamard_block != 0) why = "this format takes no rotation (hadamard_block must be 0)";
+  } else if (format == FQL_FMT_INT8) {
+    if (N < 1) why = "N must be >= 1";
+    else if (K < 32 || K % 32 != 0) why = "K must be a positive multiple of 32";
+    else if (K > fql::kInt8MaxK) why = "K must be at most 131072 (32-bit sums)";
+    else if (hadamard_block != 0) why = "this format takes no rotation (hadamard_block must be 0)";
   } else {
     why = "unknown format";
   }
@@ -691,10 +696,11 @@ int fql_linear_nvfp4_dynamic(const void* x, int64_t M, int64_t K, int64_t ldx, c
 namespace {
 
 const char* sc_name(int fmt) {
-  return fmt == fql::SC_MXFP4 ? "MXFP4" : fmt == fql::SC_MXFP8 ? "MXFP8" : fmt == fql::SC_FP8 ? "FP8" : "block FP8";
+  return fmt == fql::SC_MXFP4 ? "MXFP4" : fmt == fql::SC_MXFP8 ? "MXFP8" : fmt == fql::SC_FP8 ? "FP8"
+         : fmt == fql::SC_INT8 ? "INT8" : "block FP8";
 }
 
-// K granularity: 32 (MX block; per-tensor FP8 follows the same operand
+// K granularity: 32 (MX block; per-tensor FP8 and INT8 follow the same operand
 // granularity) or 128 (block FP8 group).
 int64_t sc_kmult(int fmt) { return fmt == fql::SC_FP8_BLOCK ? 128 : 32; }
 
@@ -708,6 +714,9 @@ int check_sc_shape(int fmt, int64_t rows, int64_t K, int64_t ld, const char* row
     return fail(FQL_ERR_INVALID, "block FP8 needs N a multiple of 128 (got %lld)", (long long)rows);
   if (ld < K) return fail(FQL_ERR_INVALID, "row stride %lld is smaller than K %lld", (long long)ld, (long long)K);
   if (K > (int64_t)1 << 24 || rows > (int64_t)1 << 24) return fail(FQL_ERR_INVALID, "dimension too large");
+  if (fmt == fql::SC_INT8 && K > fql::kInt8MaxK)
+    return fail(FQL_ERR_INVALID, "INT8 needs K <= %lld for its 32-bit sums (got %lld)", (long long)fql::kInt8MaxK,
+                (long long)K);
   if (rows * (fql::round_up(K, 128) / 32) > ((int64_t)1 << 31) - 4096)
     return fail(FQL_ERR_INVALID, "too many 32-element blocks");
   return FQL_OK;
@@ -718,8 +727,10 @@ int sc_quant(int fmt, bool f32_input, bool weight_tiles, const void* x, int64_t 
   if (int r = check_sc_shape(fmt, rows, K, ld, weight_tiles ? "N" : "M", weight_tiles)) return r;
   if (!x || !codes || (fmt != fql::SC_FP8 && !scales)) return fail(FQL_ERR_INVALID, "null pointer");
   if (reinterpret_cast<uintptr_t>(codes) % 4 != 0 ||
-      (fmt == fql::SC_FP8_BLOCK && reinterpret_cast<uintptr_t>(scales) % 4 != 0))
+      ((fmt == fql::SC_FP8_BLOCK || fmt == fql::SC_INT8) && reinterpret_cast<uintptr_t>(scales) % 4 != 0))
     return fail(FQL_ERR_INVALID, "codes (and float scales) must be 4-byte aligned");
+  if (fmt == fql::SC_INT8 && reinterpret_cast<uintptr_t>(codes) % 8 != 0)
+    return fail(FQL_ERR_INVALID, "INT8 codes must be 8-byte aligned");
   float inv = 0.0f;
   if (fmt == fql::SC_FP8) {
     if (int r = check_scale(scale, "scale")) return r;
@@ -746,7 +757,7 @@ int sc_pack(int fmt, const uint8_t* codes, const void* scales, int64_t N, int64_
     return fail(FQL_ERR_INVALID, "packed buffer holds %zu bytes, %zu needed", packed_bytes, need);
   if (reinterpret_cast<uintptr_t>(packed) % 16 != 0 || reinterpret_cast<uintptr_t>(codes) % 16 != 0)
     return fail(FQL_ERR_INVALID, "codes and the packed buffer must be 16-byte aligned");
-  if (fmt == fql::SC_FP8_BLOCK && reinterpret_cast<uintptr_t>(scales) % 4 != 0)
+  if ((fmt == fql::SC_FP8_BLOCK || fmt == fql::SC_INT8) && reinterpret_cast<uintptr_t>(scales) % 4 != 0)
     return fail(FQL_ERR_INVALID, "scales must be 4-byte aligned");
   return hip_status(fql::launch_sc_pack(fmt, codes, scales, N, K, static_cast<uint8_t*>(packed),
                                         static_cast<hipStream_t>(stream)),
@@ -930,6 +941,30 @@ int fql_linear_fp8_block(const void* x, int64_t M, int64_t K, int64_t ldx, const
                    workspace, workspace_bytes, stream);
 }
 
+// INT8
+int fql_quant_int8(const void* x, int64_t M, int64_t K, int64_t ldx, int8_t* codes, float* scales, void* stream) {
+  return sc_quant(fql::SC_INT8, false, false, x, M, K, ldx, 0.0f, reinterpret_cast<uint8_t*>(codes), scales, stream);
+}
+int fql_quant_int8_f32(const float* w, int64_t N, int64_t K, int64_t ldw, int8_t* codes, float* scales, void* stream) {
+  return sc_quant(fql::SC_INT8, true, false, w, N, K, ldw, 0.0f, reinterpret_cast<uint8_t*>(codes), scales, stream);
+}
+int fql_packed_int8_bytes(int64_t N, int64_t K, size_t* bytes) { return sc_packed_bytes(fql::SC_INT8, N, K, bytes); }
+int fql_pack_weight_int8(const int8_t* codes, const float* scales, int64_t N, int64_t K, void* packed,
+                         size_t packed_bytes, void* stream) {
+  return sc_pack(fql::SC_INT8, reinterpret_cast<const uint8_t*>(codes), scales, N, K, packed, packed_bytes, stream);
+}
+int fql_linear_int8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+  return sc_workspace_bytes(fql::SC_INT8, M, N, K, bytes);
+}
+int fql_linear_int8_describe(int64_t M, int64_t N, int64_t K, char* buf, size_t buf_len) {
+  return sc_describe(fql::SC_INT8, M, N, K, buf, buf_len);
+}
+int fql_linear_int8(const void* x, int64_t M, int64_t K, int64_t ldx, const void* w_packed, int64_t N, float alpha,
+                    const void* bias, void* y, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  return sc_linear(fql::SC_INT8, x, M, K, ldx, 1.0f, w_packed, N, alpha, bias, y, ldy, workspace, workspace_bytes,
+                   stream);
+}
+
 }  // extern "C"
 // ---- linear call without allocation: a static scratch buffer per device ------
 //
@@ -1029,6 +1064,7 @@ int sc_format(int format, bool fp4) {
     case FQL_FMT_MXFP8: return fql::SC_MXFP8;
     case FQL_FMT_FP8: return fql::SC_FP8;
     case FQL_FMT_FP8_BLOCK: return fql::SC_FP8_BLOCK;
+    case FQL_FMT_INT8: return fql::SC_INT8;
     default: return -1;
   }
 }
@@ -1072,7 +1108,9 @@ int rms_norm(int format, bool to_operand, const void* x, int64_t M, int64_t K, i
              int64_t ldr, const void* weight, float eps, float scale, uint8_t* codes, void* scales,
              size_t operand_bytes, void* h_out, int64_t ldh, void* stream) {
   const int fmt = sc_format(format, false);
-  if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no 8-bit norm output (MXFP8, FP8, block FP8 have)", format);
+  if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no 8-bit norm output (MXFP8, FP8, block FP8, INT8 have)", format);
+  if (fmt == fql::SC_INT8 && !to_operand)
+    return fail(FQL_ERR_UNSUPPORTED, "format %d: the INT8 norm is written as an operand only", format);
   if (int r = check_sc_shape(fmt, M, K, ldx, "M", false)) return r;
   if (!x || !weight || !codes || (!to_operand && fmt != fql::SC_FP8 && !scales))
     return fail(FQL_ERR_INVALID, "null pointer");
@@ -1215,7 +1253,7 @@ int fql_quant_operand(int format, const void* x, int64_t M, int64_t K, int64_t l
 int fql_linear_fused_workspace_bytes(int format, int64_t M, int64_t N, int64_t K, size_t* bytes) {
   return guarded([&] {
     const int fmt = sc_format(format, true);
-    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no fused epilogue (MXFP4, MXFP8, FP8, block FP8 have)", format);
+    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no fused epilogue (MXFP4, MXFP8, FP8, block FP8, INT8 have)", format);
     if (!bytes) return fail(FQL_ERR_INVALID, "null pointer");
     if (int r = check_sc_shape(fmt, M, K, K, "M", false)) return r;
     if (int r = check_sc_shape(fmt, N, K, K, "N", true)) return r;
@@ -1227,7 +1265,7 @@ int fql_linear_fused_workspace_bytes(int format, int64_t M, int64_t N, int64_t K
 int fql_linear_fused_describe(int format, int64_t M, int64_t N, int64_t K, char* buf, size_t buf_len) {
   return guarded([&] {
     const int fmt = sc_format(format, true);
-    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no fused epilogue (MXFP4, MXFP8, FP8, block FP8 have)", format);
+    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no fused epilogue (MXFP4, MXFP8, FP8, block FP8, INT8 have)", format);
     if (int r = check_sc_shape(fmt, M, K, K, "M", false)) return r;
     if (int r = check_sc_shape(fmt, N, K, K, "N", true)) return r;
     write_reason(buf, buf_len, fql::describe_sc_plan(fql::plan_sc_fused(fmt, M, N, K)));
@@ -1241,7 +1279,7 @@ int fql_linear_fused(int format, const void* x, int64_t M, int64_t K, int64_t ld
                      void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&] {
     const int fmt = sc_format(format, true);
-    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no fused epilogue (MXFP4, MXFP8, FP8, block FP8 have)", format);
+    if (fmt < 0) return fail(FQL_ERR_UNSUPPORTED, "format %d has no fused epilogue (MXFP4, MXFP8, FP8, block FP8, INT8 have)", format);
     if (int r = check_sc_shape(fmt, M, K, x ? ldx : K, "M", false)) return r;
     if (int r = check_sc_shape(fmt, N, K, K, "N", true)) return r;
     if (activation < FQL_ACT_NONE || activation > FQL_ACT_SWIGLU) return fail(FQL_ERR_INVALID, "unknown activation %d", activation);

@@ -197,8 +197,8 @@ hipError_t launch_linear_gemm(const GemmPlan& p, const uint8_t* packed, int64_t 
                               float alpha, const uint16_t* bias, uint16_t* y, int64_t ldy,
                               uint8_t* workspace, hipStream_t st, const LinearExtras* ex = nullptr);
 
-// ---- scaled-MFMA formats: MXFP4, MXFP8, per-tensor FP8, block FP8 ---------
-// All four run on v_mfma_scale_f32_16x16x128_f8f6f4 (one instruction per
+// ---- scaled-MFMA formats: MXFP4, MXFP8, per-tensor FP8, block FP8; INT8 ---
+// The first four run on v_mfma_scale_f32_16x16x128_f8f6f4 (one instruction per
 // 16x16 output tile and 128-deep "chunk" of K). Operand layout, shared by the
 // quantized activation (workspace) and the packed weight; rows padded to 16,
 // K to 128:
@@ -210,7 +210,12 @@ hipError_t launch_linear_gemm(const GemmPlan& p, const uint8_t* packed, int64_t 
 //     (the MFMA takes the scale of row r, block j from lane 16j + r).
 //   block-FP8 activation row scales (float32) [quads][KC][row 64].
 //   block-FP8 weight scales (float32) [N/128][KC], after the weight codes.
-enum ScFmt { SC_MXFP4 = 0, SC_MXFP8 = 1, SC_FP8 = 2, SC_FP8_BLOCK = 3 };
+//   INT8 (v_mfma_i32_16x16x64_i8, one instruction a half): two's complement
+//     codes in the FP8 layout, then one float32 scale a row, [rows_p], of the
+//     activation (per token) and of the weight (per channel; 0 past N).
+enum ScFmt { SC_MXFP4 = 0, SC_MXFP8 = 1, SC_FP8 = 2, SC_FP8_BLOCK = 3, SC_INT8 = 4 };
+// INT8's 32-bit sum over K holds 128 * 127 * K < 2^31 (a weight's code may be -128).
+constexpr int64_t kInt8MaxK = 131072;
 
 struct ScDims {
   int64_t rows_p, Kp, KC, quads, code_bytes, scale_bytes;
@@ -246,6 +251,13 @@ std::string describe_sc_plan(const ScPlan& p);
 hipError_t launch_sc_quant(int fmt, bool f32_input, bool weight_tiles, const void* x, int64_t rows,
                            int64_t K, int64_t ld, float inv_scale, uint8_t* codes, void* scales,
                            hipStream_t st);
+// INT8 rows (K % 32 == 0, K <= kInt8MaxK): s = fl32(max|v| / 127), codes
+// rint(fl32(v * fl32(1 / s))). A row that holds a NaN or an infinity has scale
+// NaN (its codes say nothing), which makes its outputs NaN. `operand`: codes in
+// the operand layout (rows past `rows` are not written, columns past K are
+// zeros), else [rows][K].
+hipError_t launch_int8_quant(bool f32_input, bool operand, const void* x, int64_t rows, int64_t K, int64_t ld,
+                             uint8_t* codes, float* scales, hipStream_t st);
 // Canonical weight -> packed operand layout.
 hipError_t launch_sc_pack(int fmt, const uint8_t* codes, const void* scales, int64_t N, int64_t K,
                           uint8_t* packed, hipStream_t st);

@@ -39,6 +39,8 @@ struct NormArgs {
   int64_t ldh;
 };
 hipError_t launch_rms_norm_quant(int fmt, bool operand, const NormArgs& a, hipStream_t st);
+// INT8, as an operand (scales: float32, one a row)
+hipError_t launch_rms_norm_int8(const NormArgs& a, hipStream_t st);
 
 // ---- linear layer with a fused epilogue --------------------------------------
 // y = bf16(act(alpha * acc + bias) + residual). kActSwiglu: the N columns come

@@ -408,6 +408,7 @@ __global__ __launch_bounds__(256) void sc_quant_operand_kernel(const uint16_t* _
 
 hipError_t launch_quant_operand(int fmt, const uint16_t* x, int64_t M, int64_t K, int64_t ldx, bool aligned,
                                 float inv_scale, uint8_t* codes, void* scales, hipStream_t st) {
+  if (fmt == SC_INT8) return launch_int8_quant(false, true, x, M, K, ldx, codes, static_cast<float*>(scales), st);
   const int64_t KC = (K + 127) / 128, waves = (M + 15) / 16 * KC;
   const unsigned grid = (unsigned)((waves + 3) / 4);
 #define FQL_Q(F)                                                                                                   \
@@ -421,6 +422,7 @@ hipError_t launch_quant_operand(int fmt, const uint16_t* x, int64_t M, int64_t K
 }
 
 hipError_t launch_rms_norm_quant(int fmt, bool operand, const NormArgs& a, hipStream_t st) {
+  if (fmt == SC_INT8) return operand ? launch_rms_norm_int8(a, st) : hipErrorInvalidValue;
 #define FQL_F(F) \
   if (fmt == F) return operand ? launch_t<F, true>(a, st) : launch_t<F, false>(a, st);
   FQL_F(SC_FP8) FQL_F(SC_FP8_BLOCK) FQL_F(SC_MXFP8)

@@ -1,5 +1,5 @@
-// GEMM of the scaled-MFMA formats (MXFP4, MXFP8, per-tensor FP8, block FP8)
-// on gfx950, plus the launch planner and the linear-layer launcher.
+// GEMM of the scaled-MFMA formats (MXFP4, MXFP8, per-tensor FP8, block FP8) and
+// of INT8 on gfx950, plus the launch planner and the linear-layer launcher.
 //
 // One v_mfma_scale_f32_16x16x128_f8f6f4 computes a 16x16 output tile over a
 // 128-deep chunk of K from the operands exactly as they sit in memory: E2M1 or
@@ -8,7 +8,10 @@
 // dequantized. Per-tensor FP8 passes the unit scale and applies alpha in the
 // epilogue; block FP8 computes each chunk into a fresh accumulator and adds
 // it with the product of the row's and the column block's float32 scales
-// (the per-128-group promotion).
+// (the per-128-group promotion). INT8 runs two v_mfma_i32_16x16x64_i8 a chunk into
+// 32-bit integers and multiplies them by the row's and the column's scale at the
+// end (a range of K that is joined with others: before the join, which is in
+// float32).
 //
 // Workgroup: NW = WM x WN waves; wave (wm, wn) owns MTW x NTW output tiles of
 // 16x16, so the workgroup tile is (WM*MTW*16) x (WN*NTW*16). The activation
@@ -33,6 +36,7 @@
 namespace fql {
 
 typedef int int8v __attribute__((ext_vector_type(8)));
+typedef int int4v __attribute__((ext_vector_type(4)));
 
 ScDims sc_dims(int fmt, int64_t rows, int64_t K, bool weight) {
   ScDims d;
@@ -42,6 +46,7 @@ ScDims sc_dims(int fmt, int64_t rows, int64_t K, bool weight) {
   d.quads = (d.rows_p + 63) / 64;
   d.code_bytes = fmt == SC_MXFP4 ? d.rows_p * d.Kp / 2 : d.rows_p * d.Kp;
   if (fmt == SC_MXFP4 || fmt == SC_MXFP8) d.scale_bytes = d.quads * d.KC * 256;
+  else if (fmt == SC_INT8) d.scale_bytes = round_up(d.rows_p * 4, 256);
   else if (fmt == SC_FP8_BLOCK) d.scale_bytes = weight ? round_up((rows / 128) * d.KC * 4, 256) : d.quads * d.KC * 256;
   else d.scale_bytes = 0;
   return d;
@@ -53,7 +58,41 @@ struct ScTraits {
   static constexpr int FMT = F == SC_MXFP4 ? 4 : 0;          // MFMA operand format (E2M1 / E4M3)
   static constexpr bool MX = F == SC_MXFP4 || F == SC_MXFP8;  // E8M0 scales in the operands
   static constexpr bool BLOCK = F == SC_FP8_BLOCK;
+  static constexpr bool INT = F == SC_INT8;
 };
+
+// INT8: one 16x16 tile over a 128-deep chunk. The 32-bit sums travel as the bits
+// of the float accumulators.
+__device__ __forceinline__ float4v mfma_int8(const int8v& a, const int8v& b, const float4v& c) {
+  int4v s = __builtin_bit_cast(int4v, c);
+  s = __builtin_amdgcn_mfma_i32_16x16x64_i8(int4v{a[0], a[1], a[2], a[3]}, int4v{b[0], b[1], b[2], b[3]}, s, 0, 0, 0);
+  s = __builtin_amdgcn_mfma_i32_16x16x64_i8(int4v{a[4], a[5], a[6], a[7]}, int4v{b[4], b[5], b[6], b[7]}, s, 0, 0, 0);
+  return __builtin_bit_cast(float4v, s);
+}
+// Four rows' sums of one column as float32 (rounded above 2^24) times the scales.
+__device__ __forceinline__ float4v int8_scaled(const float4v& acc, const float4v& row, float col) {
+  const int4v s = __builtin_bit_cast(int4v, acc);
+  return float4v{(float)s[0] * (row[0] * col), (float)s[1] * (row[1] * col), (float)s[2] * (row[2] * col),
+                 (float)s[3] * (row[3] * col)};
+}
+
+// The sum of two fragments of one format.
+template <int F>
+__device__ __forceinline__ float4v add_acc(const float4v& a, const float4v& b) {
+  if (F == SC_INT8) return __builtin_bit_cast(float4v, __builtin_bit_cast(int4v, a) + __builtin_bit_cast(int4v, b));
+  return a + b;
+}
+// The scales of rows m .. m + 3: kept as they are (rows past M have a place), or
+// (FQ) as the bits of the rows' largest |v|.
+template <int FQ>
+__device__ __forceinline__ float4v int8_rows(const void* scales, int m, int M) {
+  float4v row;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    row[i] = FQ ? int8_scale(static_cast<const uint32_t*>(scales)[m + i < M ? m + i : 0])
+                : static_cast<const float*>(scales)[m + i];
+  return row;
+}
 
 template <int F, int WM, int WN, int MTW, int NTW>
 struct ScStage {
@@ -423,6 +462,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_sc_kernel(
             const float4v z = float4v{0.f, 0.f, 0.f, 0.f};
             const float4v part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[nt], z, 0, 0, 0, 127, 0, 127);
             acc[mt][nt] += part * s4;
+          } else if constexpr (T::INT) {
+            acc[mt][nt] = mfma_int8(a, b[nt], acc[mt][nt]);
           } else {
             acc[mt][nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[nt], acc[mt][nt], T::FMT,
                                                                            T::FMT, 0, sa, 0, sb[nt]);
@@ -458,6 +499,23 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_sc_kernel(
     }
   }
   wait_vmcnt<0>();  // no LDS load may still be in flight when the workgroup ends
+  if constexpr (T::INT) {
+    // rows up to the padded M and columns up to the padded N have a scale's place;
+    // what rows past M hold is not stored
+    const float* const xs = reinterpret_cast<const float*>(xscales) + m0 + wm * MTW * 16 + 4 * (lane >> 4);
+    float col[NTW];
+#pragma unroll
+    for (int nt = 0; nt < NTW; ++nt) {
+      const int n = n0 + (wn * NTW + nt) * 16 + (lane & 15);
+      col[nt] = n < ntiles_w * 16 ? reinterpret_cast<const float*>(wscales)[n] : 0.0f;
+    }
+#pragma unroll
+    for (int mt = 0; mt < MTW; ++mt) {
+      const float4v row = *reinterpret_cast<const float4v*>(xs + mt * 16);
+#pragma unroll
+      for (int nt = 0; nt < NTW; ++nt) acc[mt][nt] = int8_scaled(acc[mt][nt], row, col[nt]);
+    }
+  }
 
   // a whole tile goes out through the ring's LDS when the staged tile fits it
   // (and its 16-byte pieces divide evenly among the threads)
@@ -596,6 +654,23 @@ __global__ __launch_bounds__(64 * W) void gemv_sc_kernel(
   auto quantize_activation = [&]() {
     const int64_t nblk = KC * 4;              // 32-blocks per row of the padded operand
     const int64_t total = (int64_t)M * nblk;  // rows >= M are never stored: not quantized
+    if constexpr (T::INT) {
+      // a row's scale needs all of it: the largest |v| of the rows first, its bits kept in place of the scales
+      uint32_t* const top = const_cast<uint32_t*>(xsd);
+      for (int m = tid; m < M; m += 64 * W) top[m] = 0u;
+      __syncthreads();
+      for (int64_t i = tid; i < total; i += 64 * W) {
+        const int64_t m = i / nblk, b = i - m * nblk;
+        if (b * 32 >= K) continue;
+        float v[32];
+        load32(x + m * ldx + b * 32, aligned != 0, v);
+        uint32_t a = 0u;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) a = amax_bits(v[j], a);
+        atomicMax(&top[m], a);
+      }
+      __syncthreads();
+    }
     for (int64_t base = 0; base < total; base += 64 * W) {
       // consecutive lanes take consecutive blocks of a row, so the four blocks
       // of a 128-group (block FP8) sit in lanes l, l^1, l^2, l^3
@@ -610,7 +685,13 @@ __global__ __launch_bounds__(64 * W) void gemv_sc_kernel(
         for (int j = 0; j < 32; ++j) v[j] = 0.0f;
       uint32_t w[8], sbyte = 0;
       float gs = 0.0f;
-      quant_block32<F>(v, valid, inv_scale, w, sbyte, gs);
+      if constexpr (T::INT) {
+        const float r = safe_reciprocal(int8_scale(xsd[m]));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = int8x4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], r);
+      } else {
+        quant_block32<F>(v, valid, inv_scale, w, sbyte, gs);
+      }
       if (inside) {
         if (!valid) {
 #pragma unroll
@@ -729,6 +810,8 @@ __global__ __launch_bounds__(64 * W) void gemv_sc_kernel(
           const float4v z = float4v{0.f, 0.f, 0.f, 0.f};
           const float4v part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[nt], z, 0, 0, 0, 127, 0, 127);
           acc[mt][nt] += part * s4;
+        } else if constexpr (T::INT) {
+          acc[mt][nt] = mfma_int8(a, b[nt], acc[mt][nt]);
         } else {
           acc[mt][nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[nt], acc[mt][nt], T::FMT,
                                                                          T::FMT, 0, sa, 0, sb[nt]);
@@ -780,8 +863,15 @@ __global__ __launch_bounds__(64 * W) void gemv_sc_kernel(
       float4v a = red[0][f][lane], b = red[0][f + 1][lane];
 #pragma unroll
       for (int w = 1; w < W; ++w) {
-        a += red[w][f][lane];
-        b += red[w][f + 1][lane];
+        a = add_acc<F>(a, red[w][f][lane]);
+        b = add_acc<F>(b, red[w][f + 1][lane]);
+      }
+      if constexpr (T::INT) {
+        const int m = (f / NT) * 16 + 4 * (lane >> 4), n = (int)((tile0 + f % NT) * 16) + (lane & 15);
+        const float* const ws = reinterpret_cast<const float*>(wscales);
+        const float4v row = int8_rows<FQ>(FQ ? static_cast<const void*>(xsd) : xscales, m, M);
+        a = int8_scaled(a, row, n < ntiles_w * 16 ? ws[n] : 0.0f);
+        b = int8_scaled(b, row, n + 16 < ntiles_w * 16 ? ws[n + 16] : 0.0f);
       }
       o.emit_pair(a, b, (f / NT) * 16 + 4 * (lane >> 4), (int)((tile0 + f % NT) * 16) + (lane & 15));
     }
@@ -792,9 +882,14 @@ __global__ __launch_bounds__(64 * W) void gemv_sc_kernel(
     if (f % W != wave) continue;
     float4v sum = red[0][f][lane];
 #pragma unroll
-    for (int w = 1; w < W; ++w) sum += red[w][f][lane];
+    for (int w = 1; w < W; ++w) sum = add_acc<F>(sum, red[w][f][lane]);
     const int n_col = (int)((tile0 + f % NT) * 16) + (lane & 15);
     if (n_col >= N) continue;
+    if constexpr (T::INT) {
+      const float4v row =
+          int8_rows<FQ>(FQ ? static_cast<const void*>(xsd) : xscales, (f / NT) * 16 + 4 * (lane >> 4), M);
+      sum = int8_scaled(sum, row, reinterpret_cast<const float*>(wscales)[n_col]);
+    }
     const float bv = bias ? bf16_bits_to_f32(bias[n_col]) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -817,13 +912,14 @@ __global__ __launch_bounds__(64 * W) void gemv_sc_kernel(
 #define FQL_SC_CONFIGS_FP4(X, F) FQL_SC_CONFIGS_ANY(X, F) X(F, 2, 4, 8, 4, 4)
 #define FQL_SC_CONFIGS_ALL(X) \
   FQL_SC_CONFIGS_FP4(X, SC_MXFP4) FQL_SC_CONFIGS_ANY(X, SC_MXFP8) FQL_SC_CONFIGS_ANY(X, SC_FP8) \
-  FQL_SC_CONFIGS_ANY(X, SC_FP8_BLOCK)
+  FQL_SC_CONFIGS_ANY(X, SC_FP8_BLOCK) FQL_SC_CONFIGS_ANY(X, SC_INT8)
 
 // Configurations of the fused-epilogue calls alone (see plan_sc_fused), 8-bit
 // formats: 64 x 64, 128 x 64 and 128 x 128 tiles, the latter two on 8 waves.
 #define FQL_SCX_CONFIGS(X, F) X(F, 2, 2, 2, 2, 4) X(F, 4, 2, 2, 2, 4) X(F, 2, 4, 4, 2, 4)
 #define FQL_SCX_CONFIGS_ALL(X) \
-  FQL_SCX_CONFIGS(X, SC_MXFP8) FQL_SCX_CONFIGS(X, SC_FP8) FQL_SCX_CONFIGS(X, SC_FP8_BLOCK)
+  FQL_SCX_CONFIGS(X, SC_MXFP8) FQL_SCX_CONFIGS(X, SC_FP8) FQL_SCX_CONFIGS(X, SC_FP8_BLOCK) \
+  FQL_SCX_CONFIGS(X, SC_INT8)
 
 // (W, MT, NT, D) GEMV configurations built: 4 waves, one row tile with four
 // (FP4) or two (8-bit) column tiles, two row tiles with two column tiles.
@@ -831,12 +927,13 @@ __global__ __launch_bounds__(64 * W) void gemv_sc_kernel(
 #define FQL_SCV_CONFIGS_FP8(X, F) X(F, 4, 1, 2, 3) X(F, 4, 2, 2, 3)
 #define FQL_SCV_CONFIGS_ALL(X) \
   FQL_SCV_CONFIGS_FP4(X, SC_MXFP4) FQL_SCV_CONFIGS_FP8(X, SC_MXFP8) FQL_SCV_CONFIGS_FP8(X, SC_FP8) \
-  FQL_SCV_CONFIGS_FP8(X, SC_FP8_BLOCK)
+  FQL_SCV_CONFIGS_FP8(X, SC_FP8_BLOCK) FQL_SCV_CONFIGS_FP8(X, SC_INT8)
 
 // The GEMV configurations also built with the activation quantized in the
 // workgroup (FQ = 1): the one-row-tile decode defaults.
 #define FQL_SCV_FUSED_CONFIGS_ALL(X) \
-  X(SC_MXFP4, 4, 1, 4, 3) X(SC_MXFP8, 4, 1, 2, 3) X(SC_FP8, 4, 1, 2, 3) X(SC_FP8_BLOCK, 4, 1, 2, 3)
+  X(SC_MXFP4, 4, 1, 4, 3) X(SC_MXFP8, 4, 1, 2, 3) X(SC_FP8, 4, 1, 2, 3) X(SC_FP8_BLOCK, 4, 1, 2, 3) \
+  X(SC_INT8, 4, 1, 2, 3)
 
 template <int F, int W, int MT, int NT, int D>
 static constexpr bool scv_config_fits() {
@@ -856,7 +953,8 @@ static bool scv_config_built(int fmt, int w, int mt, int nt, int d) {
 // and the weight ring do not fit in 160 KiB together.
 static int64_t scv_fused_lds(int fmt, int w, int mt, int nt, int d, int64_t KC, int64_t M) {
   const int H = fmt == SC_MXFP4 ? 1 : 2;
-  const int64_t dyn = KC * M * (H * 64 + 16);  // codes, then scales, rows 0 .. M-1
+  // codes, then scales, rows 0 .. M-1
+  const int64_t dyn = fmt == SC_INT8 ? KC * M * H * 64 + round_up(M * 4, 16) : KC * M * (H * 64 + 16);
 #define FQL_X(F0, A, B, C, E)                                                                     \
   if (fmt == F0 && w == A && mt == B && nt == C && d == E)                                         \
     return (int64_t)sizeof(ScvStage<F0, B, C, 1>) * A * E + dyn <= 160 * 1024 ? dyn : 0;
@@ -882,7 +980,7 @@ static bool sc_config_built(int fmt, int wm, int wn, int mtw, int ntw, int st) {
 }
 
 static const char* sc_fmt_name(int f) {
-  return f == SC_MXFP4 ? "mxfp4" : f == SC_MXFP8 ? "mxfp8" : f == SC_FP8 ? "fp8" : "fp8_block";
+  return f == SC_MXFP4 ? "mxfp4" : f == SC_MXFP8 ? "mxfp8" : f == SC_FP8 ? "fp8" : f == SC_INT8 ? "int8" : "fp8_block";
 }
 
 ScPlan plan_sc_gemm(int fmt, int64_t M, int64_t N, int64_t K) {
@@ -1061,14 +1159,15 @@ ScPlan plan_sc_fused(int fmt, int64_t M, int64_t N, int64_t K) {
 
 std::string describe_sc_plan(const ScPlan& p) {
   char b[240];
+  const char* const quant = p.fmt == SC_INT8 ? "int8_row_kernel" : "sc_quant_operand_kernel";
   if (p.kind == 1 && p.fq) {
     std::snprintf(b, sizeof(b), "gemv_sc_kernel<%s,W=%d,MT=%d,NT=%d,D=%d,FQ=1> grid=%lld splits=1",
                   sc_fmt_name(p.fmt), p.wn, p.mtw, p.ntw, p.st, (long long)p.groups);
     return std::string(b);
   }
   if (p.kind == 1) {
-    std::snprintf(b, sizeof(b), "sc_quant_operand_kernel<%s> + gemv_sc_kernel<%s,W=%d,MT=%d,NT=%d,D=%d> grid=%lld splits=1",
-                  sc_fmt_name(p.fmt), sc_fmt_name(p.fmt), p.wn, p.mtw, p.ntw, p.st, (long long)p.groups);
+    std::snprintf(b, sizeof(b), "%s<%s> + gemv_sc_kernel<%s,W=%d,MT=%d,NT=%d,D=%d> grid=%lld splits=1",
+                  quant, sc_fmt_name(p.fmt), sc_fmt_name(p.fmt), p.wn, p.mtw, p.ntw, p.st, (long long)p.groups);
     return std::string(b);
   }
   // whole tiles first; a split tail reads "tail=<tiles>x<splits>"
@@ -1076,8 +1175,8 @@ std::string describe_sc_plan(const ScPlan& p) {
   const std::string extra =
       tail ? " tail=" + std::to_string(p.groups - p.dp_groups) + "x" + std::to_string(p.splits) : "";
   std::snprintf(b, sizeof(b),
-                "sc_quant_operand_kernel<%s> + gemm_sc_kernel<%s,WM=%d,WN=%d,MTW=%d,NTW=%d,ST=%d> grid=%lld splits=%d%s",
-                sc_fmt_name(p.fmt), sc_fmt_name(p.fmt), p.wm, p.wn, p.mtw, p.ntw, p.st,
+                "%s<%s> + gemm_sc_kernel<%s,WM=%d,WN=%d,MTW=%d,NTW=%d,ST=%d> grid=%lld splits=%d%s",
+                quant, sc_fmt_name(p.fmt), sc_fmt_name(p.fmt), p.wm, p.wn, p.mtw, p.ntw, p.st,
                 (long long)(p.dp_groups + (p.groups - p.dp_groups) * p.splits), tail ? 1 : p.splits,
                 extra.c_str());
   return std::string(b);

@@ -81,6 +81,25 @@ __device__ __forceinline__ void encode_fp8x32(const float v[32], float f, uint32
     w[j] = fp8x4(v[4 * j] * f, v[4 * j + 1] * f, v[4 * j + 2] * f, v[4 * j + 3] * f);
 }
 
+// INT8: the scale of a row from the bits of its largest |v| as an unsigned
+// number, which orders NaN above infinity above all finite values.
+__device__ __forceinline__ uint32_t amax_bits(float v, uint32_t a) {
+  const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+  return b > a ? b : a;
+}
+__device__ __forceinline__ float int8_scale(uint32_t amax) {
+  return amax >= 0x7F800000u ? __builtin_nanf("") : __uint_as_float(amax) / 127.0f;
+}
+// Four codes rint(fl32(v * r)) as bytes. |v * r| <= 127.01, and adding 1.5 * 2^23
+// rounds to a whole number (ties to even) whose low byte is the code.
+__device__ __forceinline__ uint32_t int8x4(float a, float b, float c, float d, float r) {
+#pragma clang fp contract(off)
+  const float magic = 12582912.0f;
+  const uint32_t u0 = __float_as_uint(a * r + magic), u1 = __float_as_uint(b * r + magic);
+  const uint32_t u2 = __float_as_uint(c * r + magic), u3 = __float_as_uint(d * r + magic);
+  return __builtin_amdgcn_perm(u1, u0, 0x0C0C0400u) | __builtin_amdgcn_perm(u3, u2, 0x04000C0Cu);
+}
+
 // 2^-e as a float32 for e in [-127, 126].
 __device__ __forceinline__ float pow2_neg(int e) { return __uint_as_float((uint32_t)(127 - e) << 23); }
 

@@ -101,6 +101,8 @@ hipError_t launch_sc_quant(int fmt, bool f32_input, bool weight_tiles, const voi
                            hipStream_t st) {
   const uintptr_t xa = reinterpret_cast<uintptr_t>(x);
   const bool aligned = xa % 16 == 0 && (ld * (f32_input ? 4 : 2)) % 16 == 0;
+  if (fmt == SC_INT8)
+    return launch_int8_quant(f32_input, false, x, rows, K, ld, codes, static_cast<float*>(scales), st);
   if (fmt == SC_FP8_BLOCK && weight_tiles) {
     if (!f32_input) return hipErrorInvalidValue;
     const int64_t tiles = (rows / 128) * (K / 128);
@@ -180,6 +182,7 @@ __global__ __launch_bounds__(256) void sc_quant_operand_kernel(
 hipError_t launch_sc_quant_operand(int fmt, const uint16_t* x, int64_t M, int64_t K, int64_t ldx,
                                    bool aligned, float inv_scale, int64_t Mp, uint8_t* codes,
                                    void* scales, hipStream_t st) {
+  if (fmt == SC_INT8) return launch_int8_quant(false, true, x, M, K, ldx, codes, static_cast<float*>(scales), st);
   const int64_t Kp = round_up(K, 128);
   const int64_t total = Mp * (Kp / 32);
   const unsigned grid = (unsigned)((total + 255) / 256);
@@ -240,10 +243,11 @@ __global__ __launch_bounds__(256) void sc_pack_mx_scales_kernel(const uint8_t* _
   out[i] = d;
 }
 
-__global__ __launch_bounds__(256) void copy_f32_kernel(const float* __restrict__ src, int64_t n,
+// n floats, then zeros up to `total`
+__global__ __launch_bounds__(256) void copy_f32_kernel(const float* __restrict__ src, int64_t n, int64_t total,
                                                        float* __restrict__ dst) {
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i < n) dst[i] = src[i];
+  if (i < total) dst[i] = i < n ? src[i] : 0.0f;
 }
 
 hipError_t launch_sc_pack(int fmt, const uint8_t* codes, const void* scales, int64_t N, int64_t K,
@@ -267,7 +271,13 @@ hipError_t launch_sc_pack(int fmt, const uint8_t* codes, const void* scales, int
   if (fmt == SC_FP8_BLOCK) {  // [N/128][K/128] floats, already the packed order (K % 128 == 0)
     const int64_t n = (N / 128) * d.KC;
     copy_f32_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(
-        static_cast<const float*>(scales), n, reinterpret_cast<float*>(packed + d.code_bytes));
+        static_cast<const float*>(scales), n, n, reinterpret_cast<float*>(packed + d.code_bytes));
+    return hipGetLastError();
+  }
+  if (fmt == SC_INT8) {  // [N] floats, zeros up to the padded rows
+    const int64_t n = d.scale_bytes / 4;
+    copy_f32_kernel<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(
+        static_cast<const float*>(scales), N, n, reinterpret_cast<float*>(packed + d.code_bytes));
     return hipGetLastError();
   }
   return hipSuccess;

@@ -25,10 +25,10 @@ import struct
 
 import torch
 
-from . import (FMT_FP8, FMT_FP8_BLOCK, FMT_MXFP4, FMT_MXFP8, FQLError, _captured, _captured_workspace, _capturing,
-               _check, _grow_workspace, _rows_view, _size_query, _workspaces, lib)
+from . import (FMT_FP8, FMT_FP8_BLOCK, FMT_INT8, FMT_MXFP4, FMT_MXFP8, FQLError, _captured, _captured_workspace,
+               _capturing, _check, _grow_workspace, _rows_view, _size_query, _workspaces, lib)
 
-FORMATS = {"mxfp4": FMT_MXFP4, "mxfp8": FMT_MXFP8, "fp8": FMT_FP8, "fp8_block": FMT_FP8_BLOCK}
+FORMATS = {"mxfp4": FMT_MXFP4, "mxfp8": FMT_MXFP8, "fp8": FMT_FP8, "fp8_block": FMT_FP8_BLOCK, "int8": FMT_INT8}
 _I32_MAX = 2 ** 31 - 1
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}
 
@@ -169,6 +169,8 @@ def rms_norm_quant(x, weight, fmt, eps=1e-6, residual=None, scale=None, residual
     Returns (codes uint8 [..., K], scales as quant_<fmt> gives them or None, h bf16 or None without a
     residual). residual_out may be x or residual itself. No rows give empty outputs."""
     f = _format(fmt)
+    if fmt == "int8":
+        raise FQLError("unknown format 'int8' (its norm is written as an operand: rms_norm_operand)")
     xp, M, K, ld, rp, ldr, wp, h, hp, ldh = _norm_args(x, weight, residual, residual_out)
     dev = x.device
     codes = _new(x.shape, _u8, dev)
@@ -189,8 +191,8 @@ def rms_norm_quant(x, weight, fmt, eps=1e-6, residual=None, scale=None, residual
 
 
 def rms_norm_operand(x, weight, fmt, eps=1e-6, residual=None, scale=None, residual_out=None):
-    """rms_norm_quant with the quantized activation as a QuantizedActivation for linear_fused;
-    returns (activation, h or None)."""
+    """rms_norm_quant (also "int8") with the quantized activation as a QuantizedActivation for
+    linear_fused; returns (activation, h or None)."""
     f = _format(fmt)
     xp, M, K, ld, rp, ldr, wp, h, hp, ldh = _norm_args(x, weight, residual, residual_out)
     s = _scale_arg(fmt, scale)
@@ -237,7 +239,7 @@ def linear_fused(x, weight, activation=None, bias=None, residual=None, alpha=Non
     """y = bf16(act(alpha * x_q @ W_q^T + bias) + residual), rounded once.
 
     x: bf16 [..., K], quantized in the call as linear_<fmt> does, or a QuantizedActivation.
-    weight: MXFP4Weight, MXFP8Weight, FP8Weight or FP8BlockWeight. activation: None, "relu",
+    weight: MXFP4Weight, MXFP8Weight, FP8Weight, FP8BlockWeight or INT8Weight. activation: None, "relu",
     "gelu", "gelu_tanh", "silu", or "swiglu" (rows interleaved by interleave_gate_up, output
     [..., N/2]). bias bf16 [N]. residual: bf16 of y's shape; may be `out` itself, `x` may not. No rows
     give an empty output."""
@@ -245,7 +247,7 @@ def linear_fused(x, weight, activation=None, bias=None, residual=None, alpha=Non
         raise FQLError(f"unknown activation {activation!r}")
     fmt = getattr(weight, "fmt", None)
     if fmt not in FORMATS:
-        raise FQLError("linear_fused takes MXFP4, MXFP8, FP8 and block FP8 weights")
+        raise FQLError("linear_fused takes MXFP4, MXFP8, FP8, block FP8 and INT8 weights")
     N, K = weight.N, weight.K
     xp = op = ld = 0
     if isinstance(x, QuantizedActivation):

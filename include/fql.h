@@ -53,6 +53,7 @@ extern "C" {
 #define FQL_FMT_MXFP8 3
 #define FQL_FMT_FP8 4       /* per-tensor FP8 */
 #define FQL_FMT_FP8_BLOCK 5 /* block FP8: 1 x 128 activation, 128 x 128 weight groups */
+#define FQL_FMT_INT8 6      /* 8-bit integers, one scale a token and one a channel */
 
 /* Library version (major*10000 + minor*100 + patch). */
 int fql_version(void);
@@ -76,7 +77,8 @@ int fql_is_supported(int device, char* reason, size_t reason_len);
  * K % 32 == 0, N >= 1, K >= 32 and hadamard_block == 0. Block FP8 needs N and
  * K multiples of 128 (the B12X write-up's can_implement: activation group
  * (1, 128), weight group (128, 128), 128-aligned features) and
- * hadamard_block == 0. N and K are at most 2^24.
+ * hadamard_block == 0. INT8 needs K % 32 == 0, 32 <= K <= 131072 (the 32-bit
+ * sum over K), N >= 1 and hadamard_block == 0. N and K are at most 2^24.
  */
 int fql_can_implement(int format, int64_t N, int64_t K, int hadamard_block, char* reason,
                       size_t reason_len);
@@ -485,9 +487,35 @@ int fql_linear_fp8_block(const void* x, int64_t M, int64_t K, int64_t ldx, const
                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * INT8: two's complement codes with one float32 scale a token and one a weight
+ * channel. Per row: s = fl32(max|v| / 127), q = rint(fl32(v * fl32(1 / s))), ties
+ * to even (s = 0: q = 0). A row that holds a NaN or an infinity gets scale NaN,
+ * which makes its outputs NaN; its codes say nothing. Codes [rows][K], 8-byte
+ * aligned; scales float [rows]. A weight's codes may be any int8, -128 included.
+ * The sum over K is exact in 32-bit integers (K <= 131072); where a launch plan
+ * splits K, the ranges' sums are scaled and joined in float32.
+ * ------------------------------------------------------------------------- */
+int fql_quant_int8(const void* x, int64_t M, int64_t K, int64_t ldx, int8_t* codes, float* scales,
+                   void* stream);
+int fql_quant_int8_f32(const float* w, int64_t N, int64_t K, int64_t ldw, int8_t* codes,
+                       float* scales, void* stream);
+int fql_packed_int8_bytes(int64_t N, int64_t K, size_t* bytes);
+/* codes [N][K] (16-byte aligned), scales [N] -> packed operand order. */
+int fql_pack_weight_int8(const int8_t* codes, const float* scales, int64_t N, int64_t K,
+                         void* packed, size_t packed_bytes, void* stream);
+int fql_linear_int8_workspace_bytes(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int fql_linear_int8_describe(int64_t M, int64_t N, int64_t K, char* buf, size_t buf_len);
+/* y = bf16(alpha * s_x s_w (x_q @ w_q^T) + bias), x quantized as fql_quant_int8;
+ * arguments as fql_linear_mxfp4, alpha normally 1. */
+int fql_linear_int8(const void* x, int64_t M, int64_t K, int64_t ldx, const void* w_packed,
+                    int64_t N, float alpha, const void* bias, void* y, int64_t ldy,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * 8-bit serving operators: what stands between the 8-bit linear layers of a
  * decoder. `format` is FQL_FMT_FP8, FQL_FMT_FP8_BLOCK or FQL_FMT_MXFP8 (the
- * fused linear call also takes FQL_FMT_MXFP4).
+ * calls on operands also take FQL_FMT_INT8, the fused linear call and
+ * fql_quant_operand FQL_FMT_MXFP4 besides).
  * ------------------------------------------------------------------------- */
 
 /*
@@ -515,7 +543,8 @@ int fql_rms_norm_quant(int format, const void* x, int64_t M, int64_t K, int64_t 
 int fql_operand_bytes(int format, int64_t M, int64_t K, size_t* bytes);
 
 /* fql_rms_norm_quant with the codes and scales written as an operand
- * (256-byte aligned, at least fql_operand_bytes). */
+ * (256-byte aligned, at least fql_operand_bytes). Also INT8 (fql_quant_int8 on the
+ * float32 y; a row with a y that is not a number gets scale NaN). */
 int fql_rms_norm_operand(int format, const void* x, int64_t M, int64_t K, int64_t ldx,
                          const void* residual, int64_t ldr, const void* weight, float eps,
                          float scale, void* operand, size_t operand_bytes, void* h_out, int64_t ldh,
