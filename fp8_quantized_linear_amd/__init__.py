@@ -96,6 +96,7 @@ __all__ = [
     "kv_append",
     "attention_kv8",
     "attention_kv8_plan",
+    "route_experts",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -218,6 +219,8 @@ SIGNATURES = {
     "fql_attention_kv8": (_c_int, [_c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_f32,
                                    _c_int, _c_int, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp,
                                    _c_sz, _c_vp]),
+    "fql_route_experts": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_int,
+                                   _c_int, _c_int, _c_int, _c_f32, _c_vp, _c_vp, _c_vp]),
 }
 
 PLAN_OVERRIDES = {"nvfp4": 0, "sc_gemm": 1, "sc_gemv": 2}  # FQL_PLAN_NVFP4, _SC_GEMM, _SC_GEMV
@@ -1111,7 +1114,8 @@ def warmup(layers, token_counts, device=None):
     return calls
 
 
-from . import serving  # noqa: E402
+from . import experts, serving  # noqa: E402
+from .experts import route_experts  # noqa: E402
 from .serving import (KVCache8, QuantizedActivation, attention_kv8, attention_kv8_plan,  # noqa: E402
                       interleave_gate_up, kv_append, linear_fused, linear_fused_plan, quant_operand,
                       rms_norm_operand, rms_norm_quant)

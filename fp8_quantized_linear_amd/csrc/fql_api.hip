@@ -15,6 +15,7 @@
 #include <string>
 
 #include "../../include/fql.h"
+#include "fql_experts.h"
 #include "fql_internal.h"
 #include "fql_serving.h"
 
@@ -1392,6 +1393,57 @@ int fql_attention_kv8(const fql_kv_cache* cache, const fql_kv_batch* batch, cons
     return hip_status(fql::launch_attention(plan, a, c, b, static_cast<uint8_t*>(workspace),
                                             static_cast<hipStream_t>(stream)),
                       "attention launch");
+  });
+}
+
+}  // extern "C"
+
+// ---- mixture of experts --------------------------------------------------------
+
+extern "C" {
+
+int fql_route_experts(int logits_type, const void* logits, int64_t T, int64_t E, int64_t ld, int score,
+                      const float* bias, int groups, int top_groups, int k, int renormalize, float scale,
+                      float* weights, int32_t* experts, void* stream) {
+  return guarded([&] {
+    if (logits_type != FQL_TYPE_BF16 && logits_type != FQL_TYPE_F32)
+      return fail(FQL_ERR_UNSUPPORTED, "logits must be bf16 or float32 (got type %d)", logits_type);
+    if (score != FQL_SCORE_SOFTMAX && score != FQL_SCORE_SIGMOID) return fail(FQL_ERR_INVALID, "unknown score %d", score);
+    if (T < 0 || T > (int64_t)1 << 30) return fail(FQL_ERR_INVALID, "T must be in 0 .. 2^30 (got %lld)", (long long)T);
+    if (E < 1 || E > fql::kRouteMaxExperts)
+      return fail(FQL_ERR_UNSUPPORTED, "experts must be in 1 .. %d (got %lld)", fql::kRouteMaxExperts, (long long)E);
+    if (ld < E) return fail(FQL_ERR_INVALID, "row stride %lld is smaller than the %lld experts", (long long)ld, (long long)E);
+    if (groups < 1 || groups > fql::kRouteMaxGroups || E % groups != 0)
+      return fail(FQL_ERR_INVALID, "groups must divide the experts, %d at most (got %d of %lld)", fql::kRouteMaxGroups,
+                  groups, (long long)E);
+    if (top_groups < 1 || top_groups > groups)
+      return fail(FQL_ERR_INVALID, "top_groups must be in 1 .. %d (got %d)", groups, top_groups);
+    if (k < 1 || k > fql::kRouteMaxChosen || k > E / groups * top_groups)
+      return fail(FQL_ERR_INVALID, "k must be in 1 .. %lld (got %d)",
+                  (long long)std::min<int64_t>(fql::kRouteMaxChosen, E / groups * top_groups), k);
+    if (!std::isfinite(scale)) return fail(FQL_ERR_INVALID, "scale must be finite");
+    if (T == 0) return ok();
+    if (!logits || !weights || !experts) return fail(FQL_ERR_INVALID, "null pointer");
+    const uintptr_t unit = logits_type == FQL_TYPE_BF16 ? 2 : 4;
+    if (reinterpret_cast<uintptr_t>(logits) % unit != 0 || reinterpret_cast<uintptr_t>(bias) % 4 != 0 ||
+        reinterpret_cast<uintptr_t>(weights) % 4 != 0 || reinterpret_cast<uintptr_t>(experts) % 4 != 0)
+      return fail(FQL_ERR_INVALID, "pointers must be aligned to their elements");
+    fql::RouteArgs a{};
+    a.logits = logits;
+    a.T = T;
+    a.ld = ld;
+    a.E = (int)E;
+    a.k = k;
+    a.bias = bias;
+    a.softmax = score == FQL_SCORE_SOFTMAX;
+    a.groups = groups;
+    a.top_groups = top_groups;
+    a.renormalize = renormalize != 0;
+    a.scale = scale;
+    a.weights = weights;
+    a.experts = experts;
+    return hip_status(fql::launch_route(logits_type == FQL_TYPE_F32, a, static_cast<hipStream_t>(stream)),
+                      "route launch");
   });
 }
 

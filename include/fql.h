@@ -674,6 +674,38 @@ int fql_attention_kv8(const fql_kv_cache* cache, const fql_kv_batch* batch, cons
                       int window, int64_t max_len, void* out, int64_t o_ld_token, int64_t o_ld_head,
                       float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Mixture of experts: the routing of tokens to experts and the chosen experts'
+ * feed forward.
+ * ------------------------------------------------------------------------- */
+#define FQL_TYPE_BF16 1
+#define FQL_TYPE_F32 2
+#define FQL_SCORE_SOFTMAX 1
+#define FQL_SCORE_SIGMOID 2
+
+/*
+ * Scores of a router's logits and the choice of k experts a token:
+ *   s = softmax over the token's available experts, or 1 / (1 + e^-logit);
+ *   c = s + bias, without a bias the logit;
+ *   the k experts of the largest c, best first, ties to the lowest index;
+ *   weight = s, divided by the sum of the chosen s with `renormalize` (0 where
+ *   that sum is 0), times `scale`.
+ * An expert is available where its logit is neither NaN nor -inf; it is not
+ * chosen where its bias is NaN or -inf. A logit of +inf counts as the largest
+ * finite float32. Places that no expert fills get expert -1 and weight 0.
+ * With top_groups < groups only the experts of the token's best top_groups groups
+ * (of E / groups neighbours) can be chosen: a group's score is the sum of its two
+ * largest c (s without a bias), of the one where it has one. Scores are computed in
+ * float64.
+ *   logits   [T][ld], FQL_TYPE_BF16 or FQL_TYPE_F32; E <= 1024. T = 0 does nothing.
+ *   bias     [E] float32 or NULL.
+ *   groups   divides E, at most 64.   k <= 64, k <= top_groups * (E / groups).
+ *   weights  [T][k] float32, experts [T][k] int32.
+ */
+int fql_route_experts(int logits_type, const void* logits, int64_t T, int64_t E, int64_t ld, int score,
+                      const float* bias, int groups, int top_groups, int k, int renormalize,
+                      float scale, float* weights, int32_t* experts, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

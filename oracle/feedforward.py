@@ -6,7 +6,7 @@ INT8     per row: s = fl32(max |v| / 127), r = fl32(1 / s) (0 when s = 0, the la
          finite float32 when it overflows), q = rint(fl32(v r)), ties to even; a row
          with a value that is not finite has scale NaN.
 Route    an expert is available where its logit is neither NaN nor -inf (+inf counts
-         as the largest finite float32). s = softmax over the available experts or the
+         as the largest finite float32), and can be chosen where its bias is neither, either. s = softmax over the available experts or the
          sigmoid. c = s + bias, without a bias the logit. Groups of neighbours: a
          group's score is the sum of its two largest c (s without a bias) over available
          experts, a lone one counting alone; only the best `top_groups` groups that have
@@ -59,6 +59,7 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, renorma
         else:
             s = {e: 1 / (1 + math.exp(-z[e])) if z[e] > -700 else math.exp(max(z[e], -800)) for e in free}
         c = {e: s[e] + float(bias[e]) if bias is not None else z[e] for e in free}
+        free = [e for e in free if c[e] > -np.inf]  # not where c is NaN
         if groups > 1:
             n = E // groups
             by = c if bias is not None else s
