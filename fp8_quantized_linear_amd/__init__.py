@@ -97,6 +97,9 @@ __all__ = [
     "attention_kv8",
     "attention_kv8_plan",
     "route_experts",
+    "ExpertWeight",
+    "experts_fused",
+    "experts_fused_plan",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -221,6 +224,12 @@ SIGNATURES = {
                                    _c_sz, _c_vp]),
     "fql_route_experts": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_int,
                                    _c_int, _c_int, _c_int, _c_f32, _c_vp, _c_vp, _c_vp]),
+    "fql_experts_workspace_bytes": (_c_int, [_c_int, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_i64,
+                                             _c_int, ctypes.POINTER(_c_sz)]),
+    "fql_experts_describe": (_c_int, [_c_int, _c_i64, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_int,
+                                      ctypes.c_char_p, _c_sz]),
+    "fql_experts_fused": (_c_int, [_c_int, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_int, _c_vp,
+                                   _c_vp, _c_int, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_sz, _c_vp]),
 }
 
 PLAN_OVERRIDES = {"nvfp4": 0, "sc_gemm": 1, "sc_gemv": 2}  # FQL_PLAN_NVFP4, _SC_GEMM, _SC_GEMV
@@ -1115,7 +1124,7 @@ def warmup(layers, token_counts, device=None):
 
 
 from . import experts, serving  # noqa: E402
-from .experts import route_experts  # noqa: E402
+from .experts import ExpertWeight, experts_fused, experts_fused_plan, route_experts  # noqa: E402
 from .serving import (KVCache8, QuantizedActivation, attention_kv8, attention_kv8_plan,  # noqa: E402
                       interleave_gate_up, kv_append, linear_fused, linear_fused_plan, quant_operand,
                       rms_norm_operand, rms_norm_quant)

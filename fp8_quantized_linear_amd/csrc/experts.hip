@@ -1,0 +1,746 @@
+// The chosen experts' feed forward (gfx950): y_t = residual_t + sum_j w_tj
+// down_e(act(up_e(x_t))), e = experts_tj, in the formats of the scaled-MFMA linear
+// layers and INT8.
+//
+//   prepare   pairs (token, place) counted and placed by expert; x quantized, by token
+//   product   up: rows gathered by the sorted order, activation, float32
+//   quantize  the inner activation, from float32
+//   product   down: bf16 rows in sorted order
+//   combine   y_t = residual_t + the k rows of token t times their weights, float32
+//
+// A product's workgroup computes one tile of one expert: rows of its range of the
+// sorted order, columns of its weight. An expert's row tiles that share columns are
+// neighbours in the order of the workgroups, and every XCD takes a contiguous part
+// of that order, so that a weight comes from HBM once and its row tiles share it in
+// L2. The grid is the upper bound of tiles, known on the host; workgroups past the
+// true number end at once.
+#include <algorithm>
+#include <cstddef>
+#include <cstdio>
+
+#include "fql_device.h"
+#include "fql_experts.h"
+#include "fql_gemm.h"
+#include "sc_epilogue.h"
+#include "sc_quant.h"
+
+namespace fql {
+
+namespace {
+
+typedef int int8v __attribute__((ext_vector_type(8)));
+typedef int int4v __attribute__((ext_vector_type(4)));
+
+// One expert's part of a pass: its first row tile, their number, its first row
+// and the number of its rows.
+struct ExpertRange {
+  int tile0, tiles, row0, rows;
+};
+
+// Metadata of a pass in the workspace.
+struct Meta {
+  int* total_tiles;     // [0]
+  ExpertRange* ranges;  // [E]
+  int* tile_expert;     // [max_tiles]
+  int* row_pair;        // [pairs] pair t * k + j of a sorted row
+  int* pair_row;        // [pairs] its inverse; -1: the pair has no expert
+};
+constexpr int64_t meta_bytes(int64_t pairs, int64_t max_tiles) {
+  return 64 + (int64_t)kMaxExperts * (int64_t)sizeof(ExpertRange) + 4 * (max_tiles + 2 * pairs);
+}
+Meta meta_at(uint8_t* p, int64_t pairs, int64_t max_tiles) {
+  Meta m;
+  m.total_tiles = reinterpret_cast<int*>(p);
+  m.ranges = reinterpret_cast<ExpertRange*>(p + 64);
+  m.tile_expert = reinterpret_cast<int*>(m.ranges + kMaxExperts);
+  m.row_pair = m.tile_expert + max_tiles;
+  m.pair_row = m.row_pair + pairs;
+  return m;
+}
+
+// ---------------------------------------------------------------------------
+// sorting and quantizing
+// ---------------------------------------------------------------------------
+
+constexpr int kPrepThreads = 512;
+
+// Counts the pairs of every expert, lays out their rows and tiles, places them.
+// The order of an expert's rows is that of the atomics: no result depends on it
+// (a product's row depends on its own activation row only).
+__device__ __forceinline__ void sort_pairs(const int32_t* __restrict__ experts, int64_t pairs, int E, int tile_rows,
+                                           const Meta& m) {
+  __shared__ int count[kMaxExperts], row_at[kMaxExperts];
+  __shared__ int part_rows[kPrepThreads / 64], part_tiles[kPrepThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int e = tid; e < E; e += kPrepThreads) count[e] = 0;
+  __syncthreads();
+  for (int64_t i = tid; i < pairs; i += kPrepThreads) {
+    const int e = experts[i];
+    if (e >= 0 && e < E) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  // exclusive sums of rows and tiles over the experts, two experts a thread
+  static_assert(kMaxExperts <= 2 * kPrepThreads, "experts a thread");
+  int c[2], t[2];
+  int rows = 0, tiles = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = 2 * tid + j;
+    c[j] = e < E ? count[e] : 0;
+    t[j] = (c[j] + tile_rows - 1) / tile_rows;
+    rows += c[j];
+    tiles += t[j];
+  }
+  int rs = rows, ts = tiles;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int r1 = __shfl_up(rs, o), t1 = __shfl_up(ts, o);
+    if (lane >= o) {
+      rs += r1;
+      ts += t1;
+    }
+  }
+  if (lane == 63) {
+    part_rows[wave] = rs;
+    part_tiles[wave] = ts;
+  }
+  __syncthreads();
+  int row0 = rs - rows, tile0 = ts - tiles, all = 0;
+  for (int w = 0; w < kPrepThreads / 64; ++w) {
+    if (w < wave) {
+      row0 += part_rows[w];
+      tile0 += part_tiles[w];
+    }
+    all += part_tiles[w];
+  }
+  if (tid == 0) m.total_tiles[0] = all;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int e = 2 * tid + j;
+    if (e < E) {
+      m.ranges[e] = ExpertRange{tile0, t[j], row0, c[j]};
+      row_at[e] = row0;
+      for (int i = 0; i < t[j]; ++i) m.tile_expert[tile0 + i] = e;
+      row0 += c[j];
+      tile0 += t[j];
+    }
+  }
+  __syncthreads();
+  for (int64_t i = tid; i < pairs; i += kPrepThreads) {
+    const int e = experts[i];
+    int r = -1;
+    if (e >= 0 && e < E) {
+      r = atomicAdd(&row_at[e], 1);
+      m.row_pair[r] = (int)i;
+    }
+    m.pair_row[i] = r;
+  }
+}
+
+struct QuantArgs {
+  const void* x;  // bf16 or float32 [rows][ld]
+  int64_t rows, K, ld;
+  bool aligned;
+  float inv_scale;
+  ExpertRows out;
+  uint8_t* codes;
+  uint8_t* scales;
+};
+
+// Rows into the products' layout: a thread takes 32-blocks, the four of a chunk in
+// neighbouring lanes; INT8, whose scale needs the whole row first, takes a row a
+// workgroup. `unit` counts workgroups.
+template <int F, typename X>
+__device__ __forceinline__ void quant_rows(const QuantArgs& a, int64_t unit) {
+  const int64_t nblk = a.out.ld_codes / (F == SC_MXFP4 ? 16 : 32);
+  auto store = [&](int64_t m, int64_t b, const uint32_t* w) {
+    uint8_t* const dst = a.codes + m * a.out.ld_codes;
+    if (F == SC_MXFP4) {
+      *reinterpret_cast<uint4v*>(dst + b * 16) = uint4v{w[0], w[1], w[2], w[3]};
+    } else {
+      *reinterpret_cast<uint4v*>(dst + b * 32) = uint4v{w[0], w[1], w[2], w[3]};
+      *reinterpret_cast<uint4v*>(dst + b * 32 + 16) = uint4v{w[4], w[5], w[6], w[7]};
+    }
+  };
+  auto load = [&](int64_t m, int64_t b, float v[32]) {
+    if (b * 32 < a.K) load32(static_cast<const X*>(a.x) + m * a.ld + b * 32, a.aligned, v);
+    else
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+  };
+  if constexpr (F == SC_INT8) {
+    __shared__ uint32_t tops[kPrepThreads / 64];
+    const int64_t m = unit;
+    uint32_t top = 0u;
+    for (int64_t b = threadIdx.x; b < nblk; b += kPrepThreads) {
+      float v[32];
+      load(m, b, v);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) top = amax_bits(v[j], top);
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+      const uint32_t u = (uint32_t)__shfl_xor((int)top, o);
+      top = u > top ? u : top;
+    }
+    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPrepThreads / 64; ++i) top = tops[i] > top ? tops[i] : top;
+    const float s = int8_scale(top), r = safe_reciprocal(s);
+    if (threadIdx.x == 0) *reinterpret_cast<float*>(a.scales + m * a.out.ld_scales) = s;
+    for (int64_t b = threadIdx.x; b < nblk; b += kPrepThreads) {
+      float v[32];
+      load(m, b, v);
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = int8x4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], r);
+      store(m, b, w);
+    }
+  } else {
+    const int64_t i = unit * kPrepThreads + threadIdx.x;
+    const bool inside = i < a.rows * nblk;
+    const int64_t m = inside ? i / nblk : 0, b = inside ? i - m * nblk : 0;
+    const bool valid = inside && b * 32 < a.K;
+    float v[32];
+    if (inside) load(m, b, v);
+    else
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+    uint32_t w[8], sb = 0;
+    float gs = 0.0f;
+    quant_block32<F>(v, valid, a.inv_scale, w, sb, gs);
+    if (!inside) return;
+    if (!valid) {  // columns past K
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = 0u;
+      sb = 0u;
+    }
+    store(m, b, w);
+    if (F == SC_MXFP4 || F == SC_MXFP8) a.scales[m * a.out.ld_scales + b] = (uint8_t)sb;
+    if (F == SC_FP8_BLOCK && (b & 3) == 0) *reinterpret_cast<float*>(a.scales + m * a.out.ld_scales + b) = gs;
+  }
+}
+
+int64_t quant_units(int fmt, const QuantArgs& a) {
+  if (fmt == SC_INT8) return a.rows;
+  const int64_t nblk = a.out.ld_codes / (fmt == SC_MXFP4 ? 16 : 32);
+  return (a.rows * nblk + kPrepThreads - 1) / kPrepThreads;
+}
+
+// Workgroup 0 sorts while the others quantize.
+template <int F>
+__global__ __launch_bounds__(kPrepThreads) void experts_prepare_kernel(const int32_t* __restrict__ experts,
+                                                                       int64_t pairs, int E, int tile_rows, Meta m,
+                                                                       QuantArgs q) {
+  if (blockIdx.x == 0) sort_pairs(experts, pairs, E, tile_rows, m);
+  else quant_rows<F, uint16_t>(q, (int64_t)blockIdx.x - 1);
+}
+
+template <int F>
+__global__ __launch_bounds__(kPrepThreads) void experts_quant_kernel(QuantArgs q) {
+  quant_rows<F, float>(q, blockIdx.x);
+}
+
+// ---------------------------------------------------------------------------
+// the products
+// ---------------------------------------------------------------------------
+
+template <int F>
+struct Traits {
+  static constexpr int H = F == SC_MXFP4 ? 1 : 2;
+  static constexpr int FMT = F == SC_MXFP4 ? 4 : 0;
+  static constexpr bool MX = F == SC_MXFP4 || F == SC_MXFP8;
+  static constexpr bool BLOCK = F == SC_FP8_BLOCK;
+  static constexpr bool INT = F == SC_INT8;
+};
+
+struct ProductArgs {
+  const uint8_t* codes;  // activation rows
+  const uint8_t* scales;
+  ExpertRows rows;
+  const uint8_t* packed;  // weights
+  int64_t stride, code_bytes;
+  int N, ntiles_w, ngroups;
+  int64_t quads_w, KC;
+  const float* alpha;    // [E] or null
+  const uint16_t* bias;  // [E][N] or null
+  int act;               // up
+  void* out;             // up: float32 [row][ld_out]; down: bf16 [row][ld_out]
+  int64_t ld_out;
+  int pairs, k;
+};
+
+// LDS of one 128-deep chunk. Activation tiles: 16 rows of 128 (MXFP4: 64) bytes as
+// they lie in memory, their 16-byte pieces exchanged (piece p of row r in place p ^
+// swizzle(r)) so that the 16 lanes that read one piece of all rows spread over the
+// banks. Weight tiles: the packed order, lane by lane.
+template <int F, int WM, int WN, int MTW, int NTW>
+struct Stage {
+  static constexpr int H = Traits<F>::H;
+  static constexpr int TA = WM * MTW, TB = WN * NTW;
+  static constexpr int QA = (TA + 3) / 4, QB = TB / 4;
+  static constexpr int NBS = (TB * 16 + 127) / 128;
+  static constexpr int SA = Traits<F>::MX || Traits<F>::BLOCK ? QA : 0;
+  static constexpr int SB = Traits<F>::MX ? QB : (Traits<F>::BLOCK ? NBS : 0);
+  uint4v a[TA][H][64];
+  uint4v b[TB][H][64];
+  uint32_t as[SA > 0 ? SA : 1][64];
+  uint32_t bs[SB > 0 ? SB : 1][64];
+};
+
+template <int F>
+__device__ __forceinline__ int swizzle(int r) {
+  return F == SC_MXFP4 ? (r >> 2) & 3 : (r >> 1) & 7;
+}
+
+template <int F, int WM, int WN, int MTW, int NTW, int ST, bool UP>
+__global__ __launch_bounds__(64 * WM * WN) void experts_product_kernel(const ProductArgs g, const Meta meta) {
+  typedef Traits<F> T;
+  typedef Stage<F, WM, WN, MTW, NTW> Stg;
+  constexpr int NW = WM * WN, H = T::H, TA = Stg::TA, TB = Stg::TB, R = TA * 16;
+  constexpr int NA = TA * H, NB = TB * H, SA = Stg::SA, SB = Stg::SB;
+  constexpr int ITEMS = NA + NB + SA + SB;
+  constexpr int L = (ITEMS + NW - 1) / NW;
+  constexpr int P = MTW * NTW;
+  constexpr int CHUNK = 1024 * H;
+  constexpr int PIECES = F == SC_MXFP4 ? 4 : 8;  // 16-byte pieces of a row's chunk
+  static_assert(ST >= 3 && L * (ST - 2) <= 63, "ring");
+  static_assert(TB % 4 == 0 && NTW % 2 == 0, "weight tiles come in quads, columns in pairs");
+  static_assert(!T::BLOCK || (NTW * 16 <= 128 && 128 % (NTW * 16) == 0), "a wave's columns in one block");
+  __shared__ Stg stage[ST];
+
+  // this workgroup's tile
+  const int total = meta.total_tiles[0] * g.ngroups;
+  const int bid = blockIdx.x;
+  if (bid >= total) return;
+  const int xcd = bid & 7, q8 = total >> 3, r8 = total & 7;
+  const int logical = xcd * q8 + (xcd < r8 ? xcd : r8) + (bid >> 3);
+  const int expert = meta.tile_expert[logical / g.ngroups];
+  const ExpertRange er = meta.ranges[expert];
+  const int within = logical - er.tile0 * g.ngroups;
+  const int row_tile = within % er.tiles, ngroup = within / er.tiles;
+  const int row0 = er.row0 + row_tile * R;                             // first sorted row
+  const int rows = er.rows - row_tile * R < R ? er.rows - row_tile * R : R;  // at least 1
+  const int b_tile0 = ngroup * TB;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const uint8_t* const wcodes = g.packed + expert * g.stride;
+  const uint8_t* const wscales = wcodes + g.code_bytes;
+  // the activation row of tile row r; rows past the range take its last one
+  auto source_row = [&](int r) -> uint32_t {
+    const int s = row0 + (r < rows ? r : rows - 1);
+    return (uint32_t)(UP ? meta.row_pair[s] / g.k : s);
+  };
+
+  // this wave's share of a stage (item e = wave + NW j): source, chunk stride, place,
+  // and the lane's offset
+  const uint8_t* it_src[L];
+  uint32_t it_stride[L], it_lds[L], it_voff[L];
+  bool it_wide[L];
+#pragma unroll
+  for (int j = 0; j < L; ++j) {
+    int e = wave + NW * j;
+    e = e < ITEMS ? e : ITEMS - 1;
+    it_wide[j] = e < NA + NB;
+    if (e < NA) {
+      const int t = e / H, h = e % H;
+      const int r = h * 8 + lane / PIECES;  // row of the tile (MXFP4: h = 0, 16 rows)
+      const int p = (lane % PIECES) ^ swizzle<F>(r);
+      it_src[j] = g.codes;
+      it_voff[j] = source_row(t * 16 + r) * (uint32_t)g.rows.ld_codes + (uint32_t)p * 16u;
+      it_stride[j] = PIECES * 16;
+      it_lds[j] = (uint32_t)offsetof(Stg, a) + (t * H + h) * 1024;
+    } else if (e < NA + NB) {
+      const int t = (e - NA) / H, h = (e - NA) % H;
+      const int64_t gt = b_tile0 + t < g.ntiles_w ? b_tile0 + t : 0;  // past N: tile 0, never stored
+      it_src[j] = wcodes + gt * g.KC * CHUNK + h * 1024;
+      it_voff[j] = (uint32_t)lane * 16u;
+      it_stride[j] = CHUNK;
+      it_lds[j] = (uint32_t)offsetof(Stg, b) + (t * H + h) * 1024;
+    } else if (e < NA + NB + SA) {
+      const int q = e - NA - NB;
+      it_src[j] = g.scales;
+      it_voff[j] = source_row(q * 64 + lane < R ? q * 64 + lane : R - 1) * (uint32_t)g.rows.ld_scales;
+      it_stride[j] = 4;
+      it_lds[j] = (uint32_t)offsetof(Stg, as) + q * 256;
+    } else {
+      const int q = e - NA - NB - SA;
+      it_lds[j] = (uint32_t)offsetof(Stg, bs) + q * 256;
+      if (T::MX) {
+        const int64_t gq = b_tile0 / 4 + q < g.quads_w ? b_tile0 / 4 + q : 0;
+        it_src[j] = wscales + gq * g.KC * 256;
+        it_voff[j] = (uint32_t)lane * 4u;
+        it_stride[j] = 256;
+      } else {  // block FP8: the column block's scale in all 64 places
+        int64_t nb = (b_tile0 * 16) / 128 + q;
+        nb = nb < (int64_t)g.ntiles_w * 16 / 128 ? nb : 0;
+        it_src[j] = wscales + nb * g.KC * 4;
+        it_voff[j] = 0u;
+        it_stride[j] = 4;
+      }
+    }
+  }
+  auto issue_item = [&](Stg& sg, uint32_t c, int j) {
+    const uint32_t lds = lds_offset(&sg) + it_lds[j];
+    const uint8_t* const src = it_src[j] + (uint64_t)c * it_stride[j];
+    if (NW * j + NW <= NA + NB) lds_load16(src, it_voff[j], lds);
+    else if (NW * j >= NA + NB) lds_load4(src, it_voff[j], lds);
+    else if (it_wide[j]) lds_load16(src, it_voff[j], lds);
+    else lds_load4(src, it_voff[j], lds);
+  };
+
+  float4v acc[MTW][NTW];
+#pragma unroll
+  for (int mt = 0; mt < MTW; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < NTW; ++nt) acc[mt][nt] = float4v{0.f, 0.f, 0.f, 0.f};
+
+  const int fr = lane & 15, kg = lane >> 4;
+  uint32_t a_off[H];  // the lane's piece of half h within a tile, in 16-byte units
+#pragma unroll
+  for (int h = 0; h < H; ++h) a_off[h] = fr * PIECES + ((4 * h + kg) ^ swizzle<F>(fr));
+
+  auto compute = [&](const Stg& sg, Stg& refill, uint32_t rc) {
+    int8v b[NTW];
+    int sb[NTW];
+#pragma unroll
+    for (int nt = 0; nt < NTW; ++nt) {
+      const int t = wn * NTW + nt;
+      const uint4v q0 = sg.b[t][0][lane];
+      if (H == 1) {
+        b[nt] = int8v{(int)q0.x, (int)q0.y, (int)q0.z, (int)q0.w, 0, 0, 0, 0};
+      } else {
+        const uint4v q1 = sg.b[t][H - 1][lane];
+        b[nt] = int8v{(int)q0.x, (int)q0.y, (int)q0.z, (int)q0.w, (int)q1.x, (int)q1.y, (int)q1.z, (int)q1.w};
+      }
+      sb[nt] = T::MX ? (int)((sg.bs[t / 4][lane] >> (8 * (t % 4))) & 0xFFu) : 127;
+    }
+    float swv = 0.0f;
+    if (T::BLOCK) swv = __uint_as_float(sg.bs[(wn * NTW * 16) / 128][0]);
+    int p = 0;
+#pragma unroll
+    for (int mt = 0; mt < MTW; ++mt) {
+      const int t = wm * MTW + mt;
+      const uint4v* const at = &sg.a[t][0][0];
+      const uint4v q0 = at[a_off[0]];
+      int8v a;
+      if (H == 1) {
+        a = int8v{(int)q0.x, (int)q0.y, (int)q0.z, (int)q0.w, 0, 0, 0, 0};
+      } else {
+        const uint4v q1 = at[a_off[H - 1]];
+        a = int8v{(int)q0.x, (int)q0.y, (int)q0.z, (int)q0.w, (int)q1.x, (int)q1.y, (int)q1.z, (int)q1.w};
+      }
+      int sa = 127;
+      if (T::MX) sa = (int)((sg.as[t / 4][(t % 4) * 16 + fr] >> (8 * kg)) & 0xFFu);
+      float4v s4 = float4v{0.f, 0.f, 0.f, 0.f};
+      if (T::BLOCK) {
+        const float* rs = reinterpret_cast<const float*>(&sg.as[t / 4][0]) + 16 * (t % 4) + 4 * kg;
+        s4 = float4v{rs[0] * swv, rs[1] * swv, rs[2] * swv, rs[3] * swv};
+      }
+#pragma unroll
+      for (int nt = 0; nt < NTW; ++nt) {
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+          if ((j * P) / L == p) issue_item(refill, rc, j);
+        if constexpr (T::BLOCK) {
+          const float4v z = float4v{0.f, 0.f, 0.f, 0.f};
+          const float4v part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[nt], z, 0, 0, 0, 127, 0, 127);
+          acc[mt][nt] += part * s4;
+        } else if constexpr (T::INT) {
+          int4v s = __builtin_bit_cast(int4v, acc[mt][nt]);
+          s = __builtin_amdgcn_mfma_i32_16x16x64_i8(int4v{a[0], a[1], a[2], a[3]},
+                                                    int4v{b[nt][0], b[nt][1], b[nt][2], b[nt][3]}, s, 0, 0, 0);
+          s = __builtin_amdgcn_mfma_i32_16x16x64_i8(int4v{a[4], a[5], a[6], a[7]},
+                                                    int4v{b[nt][4], b[nt][5], b[nt][6], b[nt][7]}, s, 0, 0, 0);
+          acc[mt][nt] = __builtin_bit_cast(float4v, s);
+        } else {
+          acc[mt][nt] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[nt], acc[mt][nt], T::FMT, T::FMT, 0, sa,
+                                                                         0, sb[nt]);
+        }
+        ++p;
+      }
+    }
+  };
+
+  // Ring: chunk i lives in stage i % ST. Before computing chunk i a wave waits for
+  // its own loads of chunk i, passes the barrier (everyone's have landed and
+  // everyone has finished chunk i - 1), then refills stage (i - 1) % ST with chunk i
+  // + ST - 1 while computing (past the end: the last chunk again).
+  const int nch = (int)g.KC;
+#pragma unroll
+  for (int p0 = 0; p0 < ST - 1; ++p0)
+#pragma unroll
+    for (int j = 0; j < L; ++j) issue_item(stage[p0], p0 < nch ? p0 : nch - 1, j);
+  for (int i0 = 0; i0 < nch; i0 += ST) {
+#pragma unroll
+    for (int j = 0; j < ST; ++j) {
+      if (i0 + j < nch) {
+        wait_vmcnt<L * (ST - 2)>();
+        stage_barrier();
+        const int rc = i0 + j + ST - 1;
+        compute(stage[j], stage[(j + ST - 1) % ST], rc < nch ? rc : nch - 1);
+      }
+    }
+  }
+  wait_vmcnt<0>();  // no LDS load may still be in flight when the workgroup ends
+
+  const float alpha = g.alpha != nullptr ? g.alpha[expert] : 1.0f;
+  const uint16_t* const bias = g.bias != nullptr ? g.bias + (int64_t)expert * g.N : nullptr;
+  const int n0 = b_tile0 * 16;
+  if constexpr (T::INT) {
+#pragma unroll
+    for (int mt = 0; mt < MTW; ++mt) {
+      float4v row;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        row[i] = *reinterpret_cast<const float*>(
+            g.scales + (int64_t)source_row((wm * MTW + mt) * 16 + 4 * kg + i) * g.rows.ld_scales);
+#pragma unroll
+      for (int nt = 0; nt < NTW; ++nt) {
+        const int n = n0 + (wn * NTW + nt) * 16 + fr;
+        const float col = n < g.ntiles_w * 16 ? reinterpret_cast<const float*>(wscales)[n] : 0.0f;
+        const int4v s = __builtin_bit_cast(int4v, acc[mt][nt]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[mt][nt][i] = (float)s[i] * (row[i] * col);
+      }
+    }
+  }
+  if constexpr (UP) {
+    const EpiOut o = {rows, g.N, alpha, bias, ScEpilogue{g.act, nullptr, 0}, nullptr, 0};
+    float* const h = static_cast<float*>(g.out) + (int64_t)row0 * g.ld_out;
+    auto put = [&](const float4v& v, int m, int n, int n_end) {
+      if (n >= n_end) return;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (m + i < rows) h[(int64_t)(m + i) * g.ld_out + n] = v[i];
+    };
+#pragma unroll
+    for (int mt = 0; mt < MTW; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NTW; nt += 2) {
+        const int m = (wm * MTW + mt) * 16 + 4 * kg, n = n0 + (wn * NTW + nt) * 16 + fr;
+        if (o.gated()) {
+          put(o.gate(acc[mt][nt], acc[mt][nt + 1], n), m, (n >> 5) * 16 + (n & 15), n < g.N ? g.N / 2 : 0);
+        } else {
+          put(o.plain(acc[mt][nt], n), m, n, g.N);
+          put(o.plain(acc[mt][nt + 1], n + 16), m, n + 16, g.N);
+        }
+      }
+  } else {
+    uint16_t* const d = static_cast<uint16_t*>(g.out) + (int64_t)row0 * g.ld_out;
+    constexpr bool kStaged = sizeof(stage) >= (size_t)R * StagedPitch<TB * 16>::P * 2 &&
+                             (R * TB * 16 / 8) % (64 * NW) == 0;
+    static_assert(kStaged, "the output tile goes through the ring");
+    __syncthreads();  // every wave's loads have landed: the ring is free
+    write_tile16_staged<MTW, NTW, WM, WN>(acc, rows, g.N, 0, n0, wm, wn, alpha, bias, d, g.ld_out,
+                                          reinterpret_cast<uint16_t*>(&stage[0]));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// combine
+// ---------------------------------------------------------------------------
+
+// y_t = bf16(residual_t + sum_j w_tj d_row(t, j)), eight columns a thread. The
+// products' rows are bf16 (one rounding of 2^-9 each, as a linear layer's output
+// has; float32 rows would double this kernel's and the down product's traffic);
+// their sum is float32.
+__global__ __launch_bounds__(256) void experts_combine_kernel(const uint16_t* __restrict__ d, int64_t ldd, int64_t T,
+                                                              int64_t N, const float* __restrict__ weights,
+                                                              const int* __restrict__ pair_row, int k,
+                                                              const uint16_t* residual, int64_t ldr, uint16_t* y,
+                                                              int64_t ldy, bool vec) {
+  const int64_t nv = (N + 7) / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= T * nv) return;
+  const int64_t t = i / nv, n = (i - t * nv) * 8;
+  const bool whole = n + 8 <= N && vec;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  if (residual != nullptr) {
+    const uint16_t* const r = residual + t * ldr + n;
+    if (whole) {
+      const uint4v u = *reinterpret_cast<const uint4v*>(r);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[2 * j] = __uint_as_float(u[j] << 16);
+        sum[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] = n + j < N ? bf16_bits_to_f32(r[j]) : 0.0f;
+    }
+  }
+  for (int p = 0; p < k; ++p) {
+    const int row = pair_row[t * k + p];
+    if (row < 0) continue;
+    const float w = weights[t * k + p];
+    const uint4v u = *reinterpret_cast<const uint4v*>(d + (int64_t)row * ldd + n);  // rows padded to 8 columns
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sum[2 * j] = __builtin_fmaf(w, __uint_as_float(u[j] << 16), sum[2 * j]);
+      sum[2 * j + 1] = __builtin_fmaf(w, __uint_as_float(u[j] & 0xFFFF0000u), sum[2 * j + 1]);
+    }
+  }
+  uint16_t* const out = y + t * ldy + n;
+  if (whole) {
+    uint4v u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) u[j] = f32_to_bf16_bits(sum[2 * j]) | (f32_to_bf16_bits(sum[2 * j + 1]) << 16);
+    *reinterpret_cast<uint4v*>(out) = u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (n + j < N) out[j] = (uint16_t)f32_to_bf16_bits(sum[j]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// configurations, plan, launcher
+// ---------------------------------------------------------------------------
+
+// (WM, WN, MTW, NTW, ST): row tiles of 16, 64, 128 and 256, 128 columns.
+#define FQL_EXPERT_CONFIGS(X) X(1, 4, 1, 2, 4) X(1, 4, 4, 2, 4) X(2, 2, 4, 4, 3) X(4, 2, 4, 4, 3)
+
+template <int F, bool UP>
+hipError_t launch_product(const ExpertsPlan& p, const ProductArgs& g, const Meta& m, hipStream_t st) {
+  const unsigned grid = (unsigned)(p.max_tiles * g.ngroups);
+#define FQL_X(A, B, C, D, S)                                                                       \
+  if (p.wm == A && p.wn == B && p.mtw == C && p.ntw == D && p.st == S) {                            \
+    experts_product_kernel<F, A, B, C, D, S, UP><<<grid, 64 * A * B, 0, st>>>(g, m);                \
+    return hipGetLastError();                                                                       \
+  }
+  FQL_EXPERT_CONFIGS(FQL_X)
+#undef FQL_X
+  return hipErrorInvalidValue;
+}
+
+ProductArgs product_args(const ExpertsPlan& p, const ExpertWeights& w, const uint8_t* codes, const uint8_t* scales) {
+  const ScDims d = sc_dims(p.fmt, w.N, w.K, true);
+  ProductArgs g{};
+  g.codes = codes;
+  g.scales = scales;
+  g.rows = expert_rows(p.fmt, w.K);
+  g.packed = w.packed;
+  g.stride = w.stride;
+  g.code_bytes = d.code_bytes;
+  g.N = (int)w.N;
+  g.ntiles_w = (int)(d.rows_p / 16);
+  const int64_t cols = 16 * p.wn * p.ntw;
+  g.ngroups = (int)((w.N + cols - 1) / cols);
+  g.quads_w = d.quads;
+  g.KC = d.KC;
+  g.alpha = w.alpha;
+  g.bias = w.bias;
+  return g;
+}
+
+template <int F>
+hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspace, hipStream_t st) {
+  uint8_t* at = workspace + p.counter_bytes;
+  auto take = [&](int64_t bytes) {
+    uint8_t* const r = at;
+    at += bytes;
+    return r;
+  };
+  uint8_t* const meta = take(p.meta_bytes);
+  uint8_t* const xc = take(p.xcode_bytes);
+  uint8_t* const xs = take(p.xscale_bytes);
+  uint8_t* const h = take(p.h_bytes);
+  uint8_t* const hc = take(p.hcode_bytes);
+  uint8_t* const hs = take(p.hscale_bytes);
+  uint8_t* const d = take(p.d_bytes);
+  const Meta m = meta_at(meta, p.pairs, p.max_tiles);
+  const int tile_rows = 16 * p.wm * p.mtw;
+  for (int64_t t0 = 0; t0 < a.T; t0 += p.tokens) {
+    const int64_t T = std::min(p.tokens, a.T - t0), pairs = T * a.k;
+    QuantArgs q{a.x + t0 * a.ldx, T, a.up.K, a.ldx, a.aligned, a.up.inv_scale, expert_rows(F, a.up.K), xc, xs};
+    experts_prepare_kernel<F><<<(unsigned)(1 + quant_units(F, q)), kPrepThreads, 0, st>>>(
+        a.experts + t0 * a.k, pairs, a.E, tile_rows, m, q);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    ProductArgs g = product_args(p, a.up, xc, xs);
+    g.act = a.act;
+    g.out = h;
+    g.ld_out = round_up(a.I, 4);
+    g.pairs = (int)pairs;
+    g.k = a.k;
+    e = launch_product<F, true>(p, g, m, st);
+    if (e != hipSuccess) return e;
+    q = QuantArgs{h, pairs, a.I, round_up(a.I, 4), true, a.down.inv_scale, expert_rows(F, a.I), hc, hs};
+    experts_quant_kernel<F><<<(unsigned)quant_units(F, q), kPrepThreads, 0, st>>>(q);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    g = product_args(p, a.down, hc, hs);
+    g.out = d;
+    g.ld_out = round_up(a.down.N, 8);
+    g.pairs = (int)pairs;
+    g.k = a.k;
+    e = launch_product<F, false>(p, g, m, st);
+    if (e != hipSuccess) return e;
+    uint16_t* const y = a.y + t0 * a.ldy;
+    const uint16_t* const r = a.residual != nullptr ? a.residual + t0 * a.ldr : nullptr;
+    auto whole = [](const void* ptr, int64_t ld) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0; };
+    const bool vec = whole(a.y, a.ldy) && (r == nullptr || whole(a.residual, a.ldr));
+    const int64_t items = T * ((a.down.N + 7) / 8);
+    experts_combine_kernel<<<(unsigned)((items + 255) / 256), 256, 0, st>>>(
+        reinterpret_cast<const uint16_t*>(d), round_up(a.down.N, 8), T, a.down.N, a.weights + t0 * a.k, m.pair_row, a.k,
+        r, a.ldr, y, a.ldy, vec);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+ExpertsPlan plan_experts(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, int64_t N, int64_t I, int64_t Ho) {
+  ExpertsPlan p{};
+  p.fmt = fmt;
+  // a pass's activations lie within 32-bit offsets and 1 GiB of workspace
+  const ExpertRows xr = expert_rows(fmt, H), hr = expert_rows(fmt, I);
+  const int64_t per_token = xr.ld_codes + xr.ld_scales + k * (hr.ld_codes + hr.ld_scales + 4 * round_up(I, 4) + 2 * round_up(Ho, 8));
+  p.tokens = std::max<int64_t>(1, std::min<int64_t>(T, ((int64_t)1 << 30) / per_token));
+  p.pairs = p.tokens * k;
+  // rows of a tile by the mean of an expert's rows
+  const int64_t mean = p.pairs / E;
+  p.wn = 4; p.st = 4; p.wm = 1; p.ntw = 2;
+  if (mean >= 192) { p.wm = 4; p.wn = 2; p.mtw = 4; p.ntw = 4; p.st = 3; }
+  else if (mean >= 96) { p.wm = 2; p.wn = 2; p.mtw = 4; p.ntw = 4; p.st = 3; }
+  else if (mean >= 16) p.mtw = 4;
+  else p.mtw = 1;
+  const int64_t R = 16 * p.wm * p.mtw;
+  p.max_tiles = std::min(p.pairs, p.pairs / R + std::min(E, p.pairs));
+  p.counter_bytes = 64 * 1024;
+  p.meta_bytes = round_up(meta_bytes(p.pairs, p.max_tiles), 256);
+  p.xcode_bytes = round_up(p.tokens * xr.ld_codes, 256);
+  p.xscale_bytes = round_up(p.tokens * xr.ld_scales, 256);
+  p.h_bytes = round_up(p.pairs * 4 * round_up(I, 4), 256);
+  p.hcode_bytes = round_up(p.pairs * hr.ld_codes, 256);
+  p.hscale_bytes = round_up(p.pairs * hr.ld_scales, 256);
+  p.d_bytes = round_up(p.pairs * 2 * round_up(Ho, 8), 256);
+  p.total_bytes = p.counter_bytes + p.meta_bytes + p.xcode_bytes + p.xscale_bytes + p.h_bytes + p.hcode_bytes +
+                  p.hscale_bytes + p.d_bytes;
+  return p;
+}
+
+std::string describe_experts(const ExpertsPlan& p) {
+  char b[200];
+  std::snprintf(b, sizeof(b), "experts_product_kernel<WM=%d,WN=%d,MTW=%d,NTW=%d,ST=%d> tokens=%lld tiles<=%lld", p.wm,
+                p.wn, p.mtw, p.ntw, p.st, (long long)p.tokens, (long long)p.max_tiles);
+  return std::string(b);
+}
+
+hipError_t launch_experts(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspace, hipStream_t st) {
+#define FQL_F(F) \
+  if (p.fmt == F) return launch_t<F>(p, a, workspace, st);
+  FQL_F(SC_MXFP4) FQL_F(SC_MXFP8) FQL_F(SC_FP8) FQL_F(SC_FP8_BLOCK) FQL_F(SC_INT8)
+#undef FQL_F
+  return hipErrorInvalidValue;
+}
+
+}  // namespace fql

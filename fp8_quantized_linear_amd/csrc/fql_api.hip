@@ -1400,6 +1400,45 @@ int fql_attention_kv8(const fql_kv_cache* cache, const fql_kv_batch* batch, cons
 
 // ---- mixture of experts --------------------------------------------------------
 
+namespace {
+
+// The shapes of an experts call; passed, its plan. I: columns of the inner activation.
+int check_experts(int format, int64_t T, int k, int64_t E, int64_t H, int64_t N, int64_t Ho, int activation, int64_t* I,
+                  fql::ExpertsPlan* plan) {
+  const int fmt = sc_format(format, true);
+  if (fmt < 0)
+    return fail(FQL_ERR_UNSUPPORTED, "format %d has no experts (MXFP4, MXFP8, FP8, block FP8, INT8 have)", format);
+  if (activation < FQL_ACT_NONE || activation > FQL_ACT_SWIGLU) return fail(FQL_ERR_INVALID, "unknown activation %d", activation);
+  if (E < 1 || E > fql::kMaxExperts)
+    return fail(FQL_ERR_UNSUPPORTED, "experts must be in 1 .. %d (got %lld)", fql::kMaxExperts, (long long)E);
+  if (k < 1 || k > fql::kRouteMaxChosen)
+    return fail(FQL_ERR_INVALID, "k must be in 1 .. %d (got %d)", fql::kRouteMaxChosen, k);
+  if (T < 0 || T > (int64_t)1 << 24) return fail(FQL_ERR_INVALID, "T must be in 0 .. 2^24 (got %lld)", (long long)T);
+  if (int r = check_sc_shape(fmt, N, H, H, "N", true)) return r;
+  if (activation == FQL_ACT_SWIGLU && N % 32 != 0)
+    return fail(FQL_ERR_INVALID, "a gated layer needs N a multiple of 32 (got %lld)", (long long)N);
+  *I = activation == FQL_ACT_SWIGLU ? N / 2 : N;
+  if (int r = check_sc_shape(fmt, Ho, *I, *I, "N", true)) return r;
+  if (H > 1 << 18 || N > 1 << 18 || Ho > 1 << 18) return fail(FQL_ERR_INVALID, "an expert's dimensions are at most 2^18");
+  *plan = fql::plan_experts(fmt, std::max<int64_t>(T, 1), k, E, H, N, *I, Ho);
+  return FQL_OK;
+}
+
+int check_expert_weight(const fql_expert_weight* w, int fmt, const char* name, fql::ExpertWeights* out) {
+  if (!w->packed) return fail(FQL_ERR_INVALID, "null pointer");
+  if (reinterpret_cast<uintptr_t>(w->packed) % 16 != 0 || w->stride % 16 != 0)
+    return fail(FQL_ERR_INVALID, "%s: packed weights and their stride must be 16-byte aligned", name);
+  if (w->stride < fql::sc_dims(fmt, w->N, w->K, true).total_bytes())
+    return fail(FQL_ERR_INVALID, "%s: a stride of %lld bytes is smaller than a packed weight", name, (long long)w->stride);
+  if (reinterpret_cast<uintptr_t>(w->alpha) % 4 != 0 || reinterpret_cast<uintptr_t>(w->bias) % 2 != 0)
+    return fail(FQL_ERR_INVALID, "%s: alpha and bias must be aligned to their elements", name);
+  *out = fql::ExpertWeights{static_cast<const uint8_t*>(w->packed), w->stride, w->N, w->K, 0.0f, w->alpha,
+                            static_cast<const uint16_t*>(w->bias)};
+  return inverse_scale(fmt, w->input_scale, "input_scale", &out->inv_scale);
+}
+
+}  // namespace
+
 extern "C" {
 
 int fql_route_experts(int logits_type, const void* logits, int64_t T, int64_t E, int64_t ld, int score,
@@ -1444,6 +1483,80 @@ int fql_route_experts(int logits_type, const void* logits, int64_t T, int64_t E,
     a.experts = experts;
     return hip_status(fql::launch_route(logits_type == FQL_TYPE_F32, a, static_cast<hipStream_t>(stream)),
                       "route launch");
+  });
+}
+
+int fql_experts_workspace_bytes(int format, int64_t T, int k, int64_t E, int64_t H, int64_t N, int64_t Ho, int activation,
+                                size_t* bytes) {
+  return guarded([&] {
+    if (!bytes) return fail(FQL_ERR_INVALID, "null pointer");
+    int64_t I = 0;
+    fql::ExpertsPlan plan;
+    if (int r = check_experts(format, T, k, E, H, N, Ho, activation, &I, &plan)) return r;
+    *bytes = (size_t)plan.total_bytes;
+    return ok();
+  });
+}
+
+int fql_experts_describe(int format, int64_t T, int k, int64_t E, int64_t H, int64_t N, int64_t Ho, int activation,
+                         char* buf, size_t buf_len) {
+  return guarded([&] {
+    int64_t I = 0;
+    fql::ExpertsPlan plan;
+    if (int r = check_experts(format, T, k, E, H, N, Ho, activation, &I, &plan)) return r;
+    write_reason(buf, buf_len, fql::describe_experts(plan));
+    return ok();
+  });
+}
+
+int fql_experts_fused(int format, const void* x, int64_t T, int64_t ldx, const fql_expert_weight* up,
+                      const fql_expert_weight* down, int64_t E, int activation, const float* weights,
+                      const int32_t* experts, int k, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&] {
+    if (!up || !down) return fail(FQL_ERR_INVALID, "null pointer");
+    int64_t I = 0;
+    fql::ExpertsPlan plan;
+    const int64_t H = up->K, Ho = down->N;
+    if (int r = check_experts(format, T, k, E, H, up->N, Ho, activation, &I, &plan)) return r;
+    if (down->K != I)
+      return fail(FQL_ERR_INVALID, "the down projection has K=%lld, the inner activation %lld columns", (long long)down->K,
+                  (long long)I);
+    fql::ExpertsArgs a{};
+    const int fmt = plan.fmt;
+    if (int r = check_expert_weight(up, fmt, "up", &a.up)) return r;
+    if (int r = check_expert_weight(down, fmt, "down", &a.down)) return r;
+    if (ldx < H) return fail(FQL_ERR_INVALID, "row stride %lld is smaller than H %lld", (long long)ldx, (long long)H);
+    if (ldy < Ho) return fail(FQL_ERR_INVALID, "ldy %lld is smaller than the %lld output columns", (long long)ldy, (long long)Ho);
+    if (residual && ldr < Ho)
+      return fail(FQL_ERR_INVALID, "residual row stride %lld is smaller than the %lld output columns", (long long)ldr, (long long)Ho);
+    if (T == 0) return ok();
+    if (!x || !weights || !experts || !y || !workspace) return fail(FQL_ERR_INVALID, "null pointer");
+    if (reinterpret_cast<uintptr_t>(weights) % 4 != 0 || reinterpret_cast<uintptr_t>(experts) % 4 != 0)
+      return fail(FQL_ERR_INVALID, "weights and experts must be 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return fail(FQL_ERR_INVALID, "workspace must be 256-byte aligned");
+    if (workspace_bytes < (size_t)plan.total_bytes)
+      return fail(FQL_ERR_WORKSPACE, "workspace holds %zu bytes, %lld needed", workspace_bytes, (long long)plan.total_bytes);
+    // a token's rows may be one and the same: y is written after x and residual have been read
+    if (overlaps_shifted(residual, ldr, y, ldy, Ho, T)) return fail(FQL_ERR_INVALID, "y overlaps another row or column of residual");
+    if (Ho == H ? overlaps_shifted(x, ldx, y, ldy, H, T) : matrices_overlap(x, H, T > 1 ? ldx : H, y, Ho, ldy, T))
+      return fail(FQL_ERR_INVALID, "y overlaps another row or column of x");
+    a.x = static_cast<const uint16_t*>(x);
+    a.T = T;
+    a.ldx = ldx;
+    a.aligned = aligned16(x, ldx, 2);
+    a.act = activation;
+    a.I = I;
+    a.weights = weights;
+    a.experts = experts;
+    a.k = k;
+    a.E = (int)E;
+    a.residual = static_cast<const uint16_t*>(residual);
+    a.ldr = ldr;
+    a.y = static_cast<uint16_t*>(y);
+    a.ldy = ldy;
+    return hip_status(fql::launch_experts(plan, a, static_cast<uint8_t*>(workspace), static_cast<hipStream_t>(stream)),
+                      "experts launch");
   });
 }
 

@@ -706,6 +706,50 @@ int fql_route_experts(int logits_type, const void* logits, int64_t T, int64_t E,
                       const float* bias, int groups, int top_groups, int k, int renormalize,
                       float scale, float* weights, int32_t* experts, void* stream);
 
+/* E experts' weights [N][K] of one projection, each packed by fql_pack_weight_<format>,
+ * `stride` bytes apart. */
+typedef struct {
+  const void* packed;   /* 16-byte aligned */
+  int64_t stride;       /* a multiple of 16, at least fql_packed_<format>_bytes(N, K) */
+  int64_t N, K;
+  const float* alpha;   /* device [E] or NULL (1): the experts' output scales (per-tensor FP8:
+                           fl32(input_scale * weight_scale)) */
+  const void* bias;     /* bf16 [E][N] or NULL */
+  float input_scale;    /* per-tensor FP8: the static scale of the projection's input */
+} fql_expert_weight;
+
+/*
+ * The feed forward of each token's experts, formats MXFP4, MXFP8, FP8, block FP8
+ * and INT8:
+ *   h = act(alpha_up * (x_q @ Wu_e^T) + bu_e)      float32, e = experts[t][j]
+ *   d = bf16(alpha_down * (h_q @ Wd_e^T) + bd_e)
+ *   y[t] = bf16(residual[t] + sum_j weights[t][j] * d), the sum in float32
+ * with x quantized as fql_linear_<format> quantizes its input, and the float32 h
+ * likewise. A place whose expert is outside 0 .. E - 1 adds nothing; the same expert
+ * in two places of a token counts twice.
+ *   x         [T][ldx] bf16, H = up->K columns.
+ *   up        [N][H]; activation FQL_ACT_* (FQL_ACT_SWIGLU: rows interleaved by 16
+ *             as in fql_linear_fused, N a multiple of 32).
+ *   down      [Ho][I], I = N, gated N / 2.
+ *   weights   [T][k] float32, experts [T][k] int32, k <= 64, E <= 1024.
+ *   residual  [T][ldr] bf16, Ho columns, or NULL.
+ *   y         [T][ldy]; may be residual or (Ho = H) x itself: same pointer and stride.
+ *   workspace 256-byte aligned, at least fql_experts_workspace_bytes of the same
+ *             shapes; one workspace per stream at a time. Its first 64 KiB are left
+ *             alone (a linear call's workspace serves).
+ * Dimensions are at most 2^18, T at most 2^24. T = 0 does nothing. Nothing is read
+ * back to the host.
+ */
+int fql_experts_workspace_bytes(int format, int64_t T, int k, int64_t E, int64_t H, int64_t N, int64_t Ho,
+                                int activation, size_t* bytes);
+/* One-line description of the launch plan (host-side). */
+int fql_experts_describe(int format, int64_t T, int k, int64_t E, int64_t H, int64_t N, int64_t Ho,
+                         int activation, char* buf, size_t buf_len);
+int fql_experts_fused(int format, const void* x, int64_t T, int64_t ldx, const fql_expert_weight* up,
+                      const fql_expert_weight* down, int64_t E, int activation, const float* weights,
+                      const int32_t* experts, int k, const void* residual, int64_t ldr, void* y,
+                      int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,389 @@
+"""The chosen experts' feed forward on the GPU against float64, with the inner activation's codes bounded by
+what its float32 value may be off."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_quantized_linear_amd as fql
+from oracle import feedforward as O
+from oracle import formats as F
+from oracle import fp8 as P
+from oracle import mx as X
+from oracle import serving as S
+from gpu_helpers import announce
+from serving_helpers import DEV, HALF_BF16, bf16, f64, strided
+
+pytestmark = pytest.mark.gpu
+
+FMTS = ("fp8", "fp8_block", "mxfp8", "mxfp4", "int8")
+SX, SH = 0.05, 0.03  # per-tensor FP8's static scales
+
+
+def experts_of(fmt, W, scale):
+    """(ExpertWeight, exact float64 weights) of float weights [E, N, K]."""
+    g = fql.ExpertWeight.from_float(torch.from_numpy(W.astype(np.float32)).to(DEV), fmt,
+                                    input_scale=scale if fmt == "fp8" else None)
+    exact = []
+    for e, w in enumerate(W.astype(np.float32)):
+        if fmt == "fp8":
+            s = np.float32(np.float64(np.float32(np.abs(w).max())) / 448)
+            exact.append(F.e4m3_decode(P.quant_fp8_tensor(w, s)) * float(s))
+        elif fmt == "mxfp4":
+            exact.append(X.dequant_mxfp4(*X.quant_mxfp4(w)))
+        elif fmt == "mxfp8":
+            exact.append(P.dequant_mxfp8(*P.quant_mxfp8(w)))
+        elif fmt == "int8":
+            exact.append(O.dequant_int8(*O.quant_int8(w)))
+        else:
+            exact.append(P.dequant_fp8_block_weight(*P.quant_fp8_block_weight(w)))
+    return g, np.stack(exact)
+
+
+def hat(fmt, x64, scale):
+    x32 = x64.astype(np.float32)
+    if fmt == "fp8":
+        return F.e4m3_decode(P.quant_fp8_tensor(x32, np.float32(scale))) * float(np.float32(scale))
+    if fmt == "mxfp4":
+        return X.dequant_mxfp4(*X.quant_mxfp4(x32))
+    if fmt == "mxfp8":
+        return P.dequant_mxfp8(*P.quant_mxfp8(x32))
+    if fmt == "int8":
+        return O.dequant_int8(*O.quant_int8(x32))
+    return P.dequant_fp8_block_act(*P.quant_fp8_block_act(x32))
+
+
+def code_values(fmt, v, tol, scale):
+    """(dequantized codes of v, what they may be off when v is off by tol): a quantizer is monotone, so codes
+    of a value within tol lie between those of v - tol and v + tol; a block's scale moves with its largest
+    value, which shifts its quotients by as much relatively."""
+    n = {"fp8": v.shape[1], "int8": v.shape[1], "fp8_block": 128, "mxfp8": 32, "mxfp4": 32}[fmt]
+    t, d = v.reshape(v.shape[0], -1, n), tol.reshape(v.shape[0], -1, n)
+    a = np.abs(t).max(2, keepdims=True)
+    ta = d.max(2, keepdims=True)
+    if fmt == "fp8":
+        steps = [np.full_like(a, float(np.float32(scale)))]
+    elif fmt in ("fp8_block", "int8"):
+        steps = [np.maximum(a / (448 if fmt == "fp8_block" else 127), 1e-300)]
+        d = d + np.abs(t) * (ta / np.maximum(a, 1e-300) + 2.0 ** -22)
+    else:
+        top = 8 if fmt == "mxfp8" else 2
+        steps = [np.exp2(np.clip(np.floor(np.log2(np.maximum(b, 1e-300))) - top, -127, 127))
+                 for b in (a, a - ta, a + ta)]
+
+    def grid(q):
+        q = np.clip(q, -1e30, 1e30)
+        if fmt == "int8":
+            return np.clip(np.rint(q), -127, 127)
+        q32 = q.astype(np.float32)
+        if fmt == "mxfp4":
+            return F.e2m1_decode(F.e2m1_encode(np.clip(q32, -6, 6)))
+        return F.e4m3_decode(F.e4m3_encode(np.clip(q32, -448, 448)))
+
+    mid = grid(t / steps[0]) * steps[0]
+    lo = np.min([grid((t - d) / s) * s for s in steps], 0)
+    hi = np.max([grid((t + d) / s) * s for s in steps], 0)
+    return mid.reshape(v.shape), np.maximum(hi - mid, mid - lo).reshape(v.shape)
+
+
+def reference(fmt, xh, wu, wd, weights, ids, act, bu, bd, res):
+    """(y, tolerance) of tokens xh [T, H]. Counted: the products' sums (2^-12 of the sum of magnitudes for the
+    FP8 and FP4 matrix instructions, 2^-20 for integers), the activation as in the linear layers' tests, the
+    codes of h (code_values), a bf16 rounding of each d and of y, float32 sums."""
+    rel = 2.0 ** -20 if fmt == "int8" else 2.0 ** -12
+    E = wu.shape[0]
+    y = np.zeros((xh.shape[0], wd.shape[1])) if res is None else res.copy()
+    tol = np.zeros_like(y)
+    mass = np.abs(y)
+    for e in range(E):
+        t, j = np.nonzero(ids == e)
+        if t.size == 0:
+            continue
+        z = xh[t] @ wu[e].T + (0 if bu is None else bu[e])
+        ez = rel * (np.abs(xh[t]) @ np.abs(wu[e]).T) + 2.0 ** -22 * np.abs(z)
+        h = S.activation(z, act)
+        if act == "swiglu":
+            (g, u), (eg, eu) = S.gate_up(z), S.gate_up(ez)
+            eh = 1.13 * eg * (np.abs(u) + eu) + np.abs(g) * eu
+        else:
+            eh = 1.13 * ez
+        eh = eh + 2.0 ** (-16 if act == "gelu" else -18) * np.abs(h) + 1e-30
+        hq, off = code_values(fmt, h, eh, SH)
+        d = hq @ wd[e].T + (0 if bd is None else bd[e])
+        ed = off @ np.abs(wd[e]).T + rel * (np.abs(hq) + off) @ np.abs(wd[e]).T + 2.0 ** -22 * np.abs(d)
+        ed = ed * (1 + HALF_BF16) + HALF_BF16 * np.abs(d)
+        w = weights[t, j][:, None]
+        np.add.at(y, t, w * d)
+        np.add.at(tol, t, np.abs(w) * ed)
+        np.add.at(mass, t, np.abs(w * d))
+    tol = tol + 2.0 ** -20 * mass
+    return y, tol * (1 + HALF_BF16) + HALF_BF16 * np.abs(y) + 1e-30
+
+
+def check(y, ref, tol, what):
+    d = np.abs(f64(y) - ref)
+    bad = ~(d <= tol)
+    assert not bad.any(), (what, int(bad.sum()), bad.size, np.argwhere(bad)[:4].tolist(), float(np.nanmax(d / tol)))
+    # the bounds are of the worst case; what is usual is far inside them
+    assert np.linalg.norm(d) <= 0.05 * np.linalg.norm(ref) + 1e-30, what
+
+
+class Layer:
+    def __init__(self, fmt, E, H, I, Ho=None, act="swiglu", seed=0, bias=False):
+        rng = np.random.default_rng([E, H, I, seed])
+        Ho = Ho or H
+        self.fmt, self.E, self.H, self.act = fmt, E, H, act
+        N = 2 * I if act == "swiglu" else I
+        self.up, self.wu = experts_of(fmt, rng.standard_normal((E, N, H)) * H ** -0.5, SX)
+        self.down, self.wd = experts_of(fmt, rng.standard_normal((E, Ho, I)) * I ** -0.5, SH)
+        self.bu = self.bd = self.bu64 = self.bd64 = None
+        if bias:
+            self.bu, self.bu64 = bf16(rng.standard_normal((E, N)))
+            self.bd, self.bd64 = bf16(rng.standard_normal((E, Ho)))
+
+    def __call__(self, x, w, e, **args):
+        return fql.experts_fused(x, self.up, self.down, w, e, activation=self.act, bias_up=self.bu, bias_down=self.bd,
+                                 **args)
+
+    def reference(self, x64, w64, ids, res=None):
+        return reference(self.fmt, hat(self.fmt, x64, SX), self.wu, self.wd, w64, ids, self.act, self.bu64, self.bd64, res)
+
+
+def choice(rng, T, E, k, skew=0.0):
+    """Weights and distinct experts; `skew` makes the first ones more popular."""
+    s = rng.standard_normal((T, E)) - skew * np.arange(E)
+    ids = np.argsort(-s, axis=1)[:, :k].astype(np.int32)
+    w = rng.random((T, k)).astype(np.float32) + 0.1
+    w /= w.sum(1, keepdims=True)
+    return torch.from_numpy(w).to(DEV), torch.from_numpy(ids).to(DEV), w.astype(np.float64), ids
+
+
+CASES = [(1, 4, 8, 256, 128), (5, 2, 4, 128, 384), (16, 8, 16, 384, 128), (40, 3, 5, 256, 256), (200, 2, 3, 256, 128),
+         (333, 4, 4, 128, 256), (700, 1, 2, 256, 128)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,k,E,H,I", CASES)
+def test_experts(fmt, T, k, E, H, I):
+    announce(f"experts {fmt} T={T} k={k} E={E} H={H} I={I} {fql.experts_fused_plan(fmt, T, k, E, H, 2 * I, H)}")
+    rng = np.random.default_rng([T, k, E])
+    layer = Layer(fmt, E, H, I)
+    x, x64 = bf16(rng.standard_normal((T, H)))
+    r, r64 = bf16(rng.standard_normal((T, H)))
+    w, e, w64, ids = choice(rng, T, E, k, skew=0.3)
+    y = layer(x, w, e, residual=r)
+    check(y, *layer.reference(x64, w64, ids, r64), "residual")
+    check(layer(x, w, e), *layer.reference(x64, w64, ids), "plain")
+    # out over the residual, and over x
+    rr = r.clone()
+    assert layer(x, w, e, residual=rr, out=rr) is rr and torch.equal(rr, y)
+    xx = x.clone()
+    layer(xx, w, e, residual=r, out=xx)
+    assert torch.equal(xx, y)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+def test_activations_and_biases(fmt, act):
+    for T in (3, 90):
+        announce(f"experts {fmt} {act} T={T}")
+        rng = np.random.default_rng(T)
+        layer = Layer(fmt, 3, 128, 256, act=act, bias=True)
+        x, x64 = bf16(rng.standard_normal((T, 128)))
+        w, e, w64, ids = choice(rng, T, 3, 2)
+        check(layer(x, w, e), *layer.reference(x64, w64, ids), (fmt, act))
+
+
+@pytest.mark.parametrize("fmt", ("fp8", "mxfp8", "mxfp4", "int8"))
+@pytest.mark.parametrize("T", [1, 7, 60, 400])
+def test_odd_sizes_and_strides(fmt, T):
+    """Columns that end inside a chunk or a tile, rows with gaps that stay as they are."""
+    announce(f"experts odd {fmt} T={T}")
+    rng = np.random.default_rng(T)
+    H, I, Ho, E = 96, 160, 77, 3
+    layer = Layer(fmt, E, H, I, Ho=Ho)
+    x, x64 = strided(rng.standard_normal((T, H)), H + 3, 1)
+    r, r64 = strided(rng.standard_normal((T, Ho)), Ho + 5, 3)
+    w, e, w64, ids = choice(rng, T, E, 2)
+    flat = torch.full((2 + T * (Ho + 9) + 8,), -7.0, dtype=torch.bfloat16, device=DEV)
+    out = torch.as_strided(flat, (T, Ho), (Ho + 9, 1), 2)
+    layer(x, w, e, residual=r, out=out)
+    check(out, *layer.reference(x64, w64, ids, r64), "strided")
+    gaps = flat.clone()
+    torch.as_strided(gaps, (T, Ho), (Ho + 9, 1), 2).fill_(-7.0)
+    assert (gaps == -7.0).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T", [2, 70, 600])
+def test_absent_repeated_and_lone_experts(fmt, T):
+    """Experts out of range, one expert in both places, one expert for all, none at all."""
+    announce(f"experts absent {fmt} T={T}")
+    rng = np.random.default_rng(T)
+    E, H = 6, 128
+    layer = Layer(fmt, E, H, 128)
+    x, x64 = bf16(rng.standard_normal((T, H)))
+    r, r64 = bf16(rng.standard_normal((T, H)))
+    w, _, w64, _ = choice(rng, T, E, 3)
+    for kind in ("absent", "repeated", "lone", "none"):
+        ids = rng.integers(-2, E + 2, (T, 3)).astype(np.int32)
+        if kind == "absent":
+            ids[0] = [-1, E, 2 ** 31 - 1]
+            ids[1, 0] = -2 ** 31
+        elif kind == "repeated":
+            ids[:, 1] = ids[:, 0] = rng.integers(0, E, T)
+        elif kind == "lone":
+            ids[:] = 4
+        else:
+            ids[:] = -1
+        y = layer(x, w, torch.from_numpy(ids).to(DEV), residual=r)
+        check(y, *layer.reference(x64, w64, ids, r64), kind)
+        if kind == "none":
+            assert torch.equal(y, r)
+            assert (layer(x, w, torch.from_numpy(ids).to(DEV)) == 0).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_token_does_not_reach_another(fmt):
+    """A row of NaN reaches its own output alone, and a NaN weight likewise."""
+    for T in (6, 150):
+        announce(f"experts NaN {fmt} T={T}")
+        rng = np.random.default_rng(T)
+        layer = Layer(fmt, 3, 256, 128)
+        x, _ = bf16(rng.standard_normal((T, 256)))
+        w, e, _, _ = choice(rng, T, 3, 2)
+        want = layer(x, w, e)
+        w2, x2 = w.clone(), x.clone()
+        w2[1, 0] = float("nan")
+        x2[4] = float("nan")
+        x2[2, 7] = float("inf")
+        got = layer(x2, w2, e)
+        same = [t for t in range(T) if t not in (1, 2, 4)]
+        assert torch.equal(got[same], want[same])
+        assert torch.isnan(got[1]).all()
+        if fmt == "int8":
+            assert torch.isnan(got[[2, 4]]).all()
+
+
+@pytest.mark.parametrize("fmt", ("mxfp8", "int8"))
+def test_many_experts_and_places(fmt):
+    announce(f"experts many {fmt}")
+    rng = np.random.default_rng(1)
+    E, H, T, k = 200, 64, 37, 16
+    layer = Layer(fmt, E, H, 64)
+    x, x64 = bf16(rng.standard_normal((T, H)))
+    w, e, w64, ids = choice(rng, T, E, k)
+    check(layer(x, w, e), *layer.reference(x64, w64, ids), "many")
+
+
+def test_passes_over_tokens():
+    """More tokens than one pass of the workspace takes."""
+    T, k, E, H, I = 2600, 8, 8, 128, 14336
+    plan = fql.experts_fused_plan("mxfp8", T, k, E, H, 2 * I, H)
+    announce(f"experts passes {plan}")
+    rng = np.random.default_rng(2)
+    layer = Layer("mxfp8", E, H, I)
+    x, x64 = bf16(rng.standard_normal((T, H), dtype=np.float32))
+    w, e, w64, ids = choice(rng, T, E, k)
+    y = layer(x, w, e, out=x.clone())
+    rows = np.unique(np.concatenate([[0, T - 1], rng.integers(0, T, 20), np.arange(1400, 1900, 50)]))
+    check(y[torch.from_numpy(rows).to(DEV)], *layer.reference(x64[rows], w64[rows], ids[rows]), "passes")
+    xx = x.clone()
+    layer(xx, w, e, out=xx)
+    assert torch.equal(xx, y)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_codes_and_repack(fmt):
+    announce(f"experts repack {fmt}")
+    rng = np.random.default_rng(3)
+    layer, other = Layer(fmt, 3, 128, 128), Layer(fmt, 3, 128, 128, seed=9)
+    x, x64 = bf16(rng.standard_normal((20, 128)))
+    w, e, w64, ids = choice(rng, 20, 3, 2)
+    W = torch.from_numpy(other.wd[1].astype(np.float32)).to(DEV)
+    if fmt == "fp8":
+        s = fql.fp8_scale_from_amax(W.abs().max().item())
+        layer.down.repack_(1, fql.quant_fp8_weight(W, s), s)
+    else:
+        quant = {"mxfp4": fql.quant_mxfp4_weight, "mxfp8": fql.quant_mxfp8_weight, "int8": fql.quant_int8_weight,
+                 "fp8_block": fql.quant_fp8_block_weight}[fmt]
+        layer.down.repack_(1, *quant(W))
+    layer.wd[1] = experts_of(fmt, other.wd[1:2], SH)[1][0]
+    check(layer(x, w, e), *layer.reference(x64, w64, ids), "repacked")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T", [3, 130])
+def test_graph_and_streams(fmt, T):
+    """Replays of a captured call beside eager ones, other choices each time; a call on another stream."""
+    announce(f"experts graph {fmt} T={T}")
+    rng = np.random.default_rng(4)
+    layer = Layer(fmt, 4, 256, 128)
+    x, _ = bf16(rng.standard_normal((T, 256)))
+    w, e, _, _ = choice(rng, T, 4, 2)
+    layer(x, w, e)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = layer(x, w, e)
+    for i in range(4):
+        x.copy_(bf16(rng.standard_normal((T, 256)))[0])
+        e.copy_(choice(rng, T, 4, 2)[1])
+        if i == 3:
+            e.fill_(-1)
+        graph.replay()
+        eager = layer(x, w, e)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            aside = layer(x, w, e)
+        torch.cuda.synchronize()
+        assert torch.equal(y, eager) and torch.equal(aside, eager)
+
+
+def test_no_tokens_and_leading_dimensions():
+    announce("experts shapes")
+    layer = Layer("mxfp8", 4, 128, 128)
+    rng = np.random.default_rng(5)
+    x, _ = bf16(rng.standard_normal((6, 128)))
+    w, e, _, _ = choice(rng, 6, 4, 2)
+    assert layer(x[:0], w[:0], e[:0]).shape == (0, 128)
+    y = layer(x.view(2, 3, 128), w.view(2, 3, 2), e.view(2, 3, 2))
+    assert y.shape == (2, 3, 128) and torch.equal(y.view(6, 128), layer(x, w, e))
+    one = layer(x[0], w[0], e[0])
+    assert one.shape == (128,) and torch.equal(one, layer(x[:1], w[:1], e[:1])[0])
+
+
+@pytest.mark.parametrize("fmt", ("fp8_block", "mxfp8", "int8"))
+@pytest.mark.parametrize("T", [1, 33])
+def test_decoder_feed_forward(fmt, T):
+    """The operators as a layer runs them: INT8 or dense projection, router, experts, residual stream."""
+    announce(f"feed forward {fmt} T={T}")
+    rng = np.random.default_rng([T, 6])
+    E, k, H, I = 8, 2, 256, 128
+    layer = Layer(fmt, E, H, I)
+    dense = fql.INT8Weight.from_float(torch.from_numpy(rng.standard_normal((H, H)).astype(np.float32) * H ** -0.5).to(DEV))
+    router = bf16(rng.standard_normal((E, H)) * H ** -0.5)[0]
+    norm, _ = bf16(np.ones(H))
+    h0, _ = bf16(rng.standard_normal((T, H)))
+    bias = torch.from_numpy((0.1 * rng.standard_normal(E)).astype(np.float32)).to(DEV)
+
+    def step(h0):
+        a, _ = fql.rms_norm_operand(h0, norm, "int8")
+        x = fql.linear_fused(a, dense, activation="silu")
+        logits = x @ router.t().contiguous()
+        w, e = fql.route_experts(logits, k, score="sigmoid", bias=bias, groups=4, top_groups=2, scale=2.0)
+        return x, logits, w, e, fql.experts_fused(x, layer.up, layer.down, w, e, residual=h0)
+
+    x, logits, w, e, y = step(h0)
+    w64, ids = O.route(f64(logits), k, score="sigmoid", bias=f64(bias), groups=4, top_groups=2, scale=2.0)
+    assert np.array_equal(e.cpu().numpy(), ids)
+    check(y, *layer.reference(f64(x), f64(w), ids, f64(h0)), "feed forward")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gy = step(h0)[-1]
+    for _ in range(3):
+        h0.copy_(bf16(rng.standard_normal((T, H)))[0])
+        graph.replay()
+        eager = step(h0)[-1]
+        torch.cuda.synchronize()
+        assert torch.equal(gy, eager)
