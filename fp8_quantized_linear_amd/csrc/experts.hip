@@ -20,6 +20,7 @@
 
 #include "fql_device.h"
 #include "fql_experts.h"
+#include "experts_tile.h"
 #include "fql_gemm.h"
 #include "sc_epilogue.h"
 #include "sc_quant.h"
@@ -28,23 +29,6 @@ namespace fql {
 
 namespace {
 
-typedef int int8v __attribute__((ext_vector_type(8)));
-typedef int int4v __attribute__((ext_vector_type(4)));
-
-// One expert's part of a pass: its first row tile, their number, its first row
-// and the number of its rows.
-struct ExpertRange {
-  int tile0, tiles, row0, rows;
-};
-
-// Metadata of a pass in the workspace.
-struct Meta {
-  int* total_tiles;     // [0]
-  ExpertRange* ranges;  // [E]
-  int* tile_expert;     // [max_tiles]
-  int* row_pair;        // [pairs] pair t * k + j of a sorted row
-  int* pair_row;        // [pairs] its inverse; -1: the pair has no expert
-};
 constexpr int64_t meta_bytes(int64_t pairs, int64_t max_tiles) {
   return 64 + (int64_t)kMaxExperts * (int64_t)sizeof(ExpertRange) + 4 * (max_tiles + 2 * pairs);
 }
@@ -246,31 +230,6 @@ __global__ __launch_bounds__(kPrepThreads) void experts_quant_kernel(QuantArgs q
 // the products
 // ---------------------------------------------------------------------------
 
-template <int F>
-struct Traits {
-  static constexpr int H = F == SC_MXFP4 ? 1 : 2;
-  static constexpr int FMT = F == SC_MXFP4 ? 4 : 0;
-  static constexpr bool MX = F == SC_MXFP4 || F == SC_MXFP8;
-  static constexpr bool BLOCK = F == SC_FP8_BLOCK;
-  static constexpr bool INT = F == SC_INT8;
-};
-
-struct ProductArgs {
-  const uint8_t* codes;  // activation rows
-  const uint8_t* scales;
-  ExpertRows rows;
-  const uint8_t* packed;  // weights
-  int64_t stride, code_bytes;
-  int N, ntiles_w, ngroups;
-  int64_t quads_w, KC;
-  const float* alpha;    // [E] or null
-  const uint16_t* bias;  // [E][N] or null
-  int act;               // up
-  void* out;             // up: float32 [row][ld_out]; down: bf16 [row][ld_out]
-  int64_t ld_out;
-  int pairs, k;
-};
-
 // LDS of one 128-deep chunk. Activation tiles: 16 rows of 128 (MXFP4: 64) bytes as
 // they lie in memory, their 16-byte pieces exchanged (piece p of row r in place p ^
 // swizzle(r)) so that the 16 lanes that read one piece of all rows spread over the
@@ -310,30 +269,17 @@ __global__ __launch_bounds__(64 * WM * WN) void experts_product_kernel(const Pro
   static_assert(!T::BLOCK || (NTW * 16 <= 128 && 128 % (NTW * 16) == 0), "a wave's columns in one block");
   __shared__ Stg stage[ST];
 
-  // this workgroup's tile
-  const int total = meta.total_tiles[0] * g.ngroups;
-  const int bid = blockIdx.x;
-  if (bid >= total) return;
-  const int xcd = bid & 7, q8 = total >> 3, r8 = total & 7;
-  const int logical = xcd * q8 + (xcd < r8 ? xcd : r8) + (bid >> 3);
-  const int expert = meta.tile_expert[logical / g.ngroups];
-  const ExpertRange er = meta.ranges[expert];
-  const int within = logical - er.tile0 * g.ngroups;
-  const int row_tile = within % er.tiles, ngroup = within / er.tiles;
-  const int row0 = er.row0 + row_tile * R;                             // first sorted row
-  const int rows = er.rows - row_tile * R < R ? er.rows - row_tile * R : R;  // at least 1
-  const int b_tile0 = ngroup * TB;
+  TileAt tile;
+  if (!find_tile(g, meta, R, tile)) return;
+  const int expert = tile.expert, row0 = tile.row0, rows = tile.rows;
+  const int b_tile0 = tile.ngroup * TB;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const uint8_t* const wcodes = g.packed + expert * g.stride;
   const uint8_t* const wscales = wcodes + g.code_bytes;
-  // the activation row of tile row r; rows past the range take its last one
-  auto source_row = [&](int r) -> uint32_t {
-    const int s = row0 + (r < rows ? r : rows - 1);
-    return (uint32_t)(UP ? meta.row_pair[s] / g.k : s);
-  };
+  auto source = [&](int r) { return source_row<UP>(g, meta, tile, r); };
 
   // this wave's share of a stage (item e = wave + NW j): source, chunk stride, place,
   // and the lane's offset
@@ -350,7 +296,7 @@ __global__ __launch_bounds__(64 * WM * WN) void experts_product_kernel(const Pro
       const int r = h * 8 + lane / PIECES;  // row of the tile (MXFP4: h = 0, 16 rows)
       const int p = (lane % PIECES) ^ swizzle<F>(r);
       it_src[j] = g.codes;
-      it_voff[j] = source_row(t * 16 + r) * (uint32_t)g.rows.ld_codes + (uint32_t)p * 16u;
+      it_voff[j] = source(t * 16 + r) * (uint32_t)g.rows.ld_codes + (uint32_t)p * 16u;
       it_stride[j] = PIECES * 16;
       it_lds[j] = (uint32_t)offsetof(Stg, a) + (t * H + h) * 1024;
     } else if (e < NA + NB) {
@@ -363,7 +309,7 @@ __global__ __launch_bounds__(64 * WM * WN) void experts_product_kernel(const Pro
     } else if (e < NA + NB + SA) {
       const int q = e - NA - NB;
       it_src[j] = g.scales;
-      it_voff[j] = source_row(q * 64 + lane < R ? q * 64 + lane : R - 1) * (uint32_t)g.rows.ld_scales;
+      it_voff[j] = source(q * 64 + lane < R ? q * 64 + lane : R - 1) * (uint32_t)g.rows.ld_scales;
       it_stride[j] = 4;
       it_lds[j] = (uint32_t)offsetof(Stg, as) + q * 256;
     } else {
@@ -497,7 +443,7 @@ __global__ __launch_bounds__(64 * WM * WN) void experts_product_kernel(const Pro
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         row[i] = *reinterpret_cast<const float*>(
-            g.scales + (int64_t)source_row((wm * MTW + mt) * 16 + 4 * kg + i) * g.rows.ld_scales);
+            g.scales + (int64_t)source((wm * MTW + mt) * 16 + 4 * kg + i) * g.rows.ld_scales);
 #pragma unroll
       for (int nt = 0; nt < NTW; ++nt) {
         const int n = n0 + (wn * NTW + nt) * 16 + fr;
@@ -603,19 +549,40 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(const uint16_t* __
 // configurations, plan, launcher
 // ---------------------------------------------------------------------------
 
-// (WM, WN, MTW, NTW, ST): row tiles of 16, 64, 128 and 256, 128 columns.
-#define FQL_EXPERT_CONFIGS(X) X(1, 4, 1, 2, 4) X(1, 4, 4, 2, 4) X(2, 2, 4, 4, 3) X(4, 2, 4, 4, 3)
+// (WM, WN, MTW, NTW, ST) of experts_product_kernel: row tiles of 16, 128 columns.
+#define FQL_EXPERT_CONFIGS(X) X(1, 4, 1, 2, 4)
+// (MT, ST) of experts_block_kernel: 64 and 128 rows, 256 columns.
+#define FQL_BLOCK_CONFIGS(X) X(2, 3) X(4, 3)
+// (WM, WN, MT, NT, ST) of experts_tile_kernel: 64, 128 and 256 rows, 256 columns.
+#define FQL_TILE_CONFIGS(X) X(1, 4, 2, 2, 3) X(1, 4, 4, 2, 4) X(2, 2, 4, 4, 4)
 
 template <int F, bool UP>
 hipError_t launch_product(const ExpertsPlan& p, const ProductArgs& g, const Meta& m, hipStream_t st) {
   const unsigned grid = (unsigned)(p.max_tiles * g.ngroups);
 #define FQL_X(A, B, C, D, S)                                                                       \
-  if (p.wm == A && p.wn == B && p.mtw == C && p.ntw == D && p.st == S) {                            \
+  if (!p.large && p.wm == A && p.wn == B && p.mtw == C && p.ntw == D && p.st == S) {                \
     experts_product_kernel<F, A, B, C, D, S, UP><<<grid, 64 * A * B, 0, st>>>(g, m);                \
     return hipGetLastError();                                                                       \
   }
   FQL_EXPERT_CONFIGS(FQL_X)
 #undef FQL_X
+  if constexpr (F == SC_FP8_BLOCK) {
+#define FQL_X(C, S)                                                                                     \
+  if (p.large && p.wm == 1 && p.wn == 4 && p.ntw == 2 && p.mtw == C && p.st == S) {                      \
+    experts_block_kernel<C, S, UP><<<grid, 256, TileConfig<F, 1, 4, C, 2, S>::LDS, st>>>(g, m);          \
+    return hipGetLastError();                                                                            \
+  }
+    FQL_BLOCK_CONFIGS(FQL_X)
+#undef FQL_X
+  } else {
+#define FQL_X(A, B, C, D, S)                                                                       \
+  if (p.large && p.wm == A && p.wn == B && p.mtw == C && p.ntw == D && p.st == S) {                 \
+    experts_tile_kernel<F, A, B, C, D, S, UP><<<grid, 256, 0, st>>>(g, m);                          \
+    return hipGetLastError();                                                                       \
+  }
+    FQL_TILE_CONFIGS(FQL_X)
+#undef FQL_X
+  }
   return hipErrorInvalidValue;
 }
 
@@ -630,7 +597,7 @@ ProductArgs product_args(const ExpertsPlan& p, const ExpertWeights& w, const uin
   g.code_bytes = d.code_bytes;
   g.N = (int)w.N;
   g.ntiles_w = (int)(d.rows_p / 16);
-  const int64_t cols = 16 * p.wn * p.ntw;
+  const int64_t cols = (p.large ? 32 : 16) * p.wn * p.ntw;
   g.ngroups = (int)((w.N + cols - 1) / cols);
   g.quads_w = d.quads;
   g.KC = d.KC;
@@ -655,30 +622,32 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
   uint8_t* const hs = take(p.hscale_bytes);
   uint8_t* const d = take(p.d_bytes);
   const Meta m = meta_at(meta, p.pairs, p.max_tiles);
-  const int tile_rows = 16 * p.wm * p.mtw;
   for (int64_t t0 = 0; t0 < a.T; t0 += p.tokens) {
     const int64_t T = std::min(p.tokens, a.T - t0), pairs = T * a.k;
     QuantArgs q{a.x + t0 * a.ldx, T, a.up.K, a.ldx, a.aligned, a.up.inv_scale, expert_rows(F, a.up.K), xc, xs};
     experts_prepare_kernel<F><<<(unsigned)(1 + quant_units(F, q)), kPrepThreads, 0, st>>>(
-        a.experts + t0 * a.k, pairs, a.E, tile_rows, m, q);
+        a.experts + t0 * a.k, pairs, a.E, p.rows, m, q);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     ProductArgs g = product_args(p, a.up, xc, xs);
     g.act = a.act;
-    g.out = h;
-    g.ld_out = round_up(a.I, 4);
-    g.pairs = (int)pairs;
     g.k = a.k;
+    g.hrows = expert_rows(F, a.I);
+    g.hscales = hs;
+    g.inv_scale = a.down.inv_scale;
+    g.out = p.h_quantized ? hc : h;
+    g.ld_out = round_up(a.I, 4);
     e = launch_product<F, true>(p, g, m, st);
     if (e != hipSuccess) return e;
-    q = QuantArgs{h, pairs, a.I, round_up(a.I, 4), true, a.down.inv_scale, expert_rows(F, a.I), hc, hs};
-    experts_quant_kernel<F><<<(unsigned)quant_units(F, q), kPrepThreads, 0, st>>>(q);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (!p.h_quantized) {
+      q = QuantArgs{h, pairs, a.I, round_up(a.I, 4), true, a.down.inv_scale, expert_rows(F, a.I), hc, hs};
+      experts_quant_kernel<F><<<(unsigned)quant_units(F, q), kPrepThreads, 0, st>>>(q);
+      e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
     g = product_args(p, a.down, hc, hs);
     g.out = d;
     g.ld_out = round_up(a.down.N, 8);
-    g.pairs = (int)pairs;
     g.k = a.k;
     e = launch_product<F, false>(p, g, m, st);
     if (e != hipSuccess) return e;
@@ -701,25 +670,35 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
 ExpertsPlan plan_experts(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, int64_t N, int64_t I, int64_t Ho) {
   ExpertsPlan p{};
   p.fmt = fmt;
-  // a pass's activations lie within 32-bit offsets and 1 GiB of workspace
   const ExpertRows xr = expert_rows(fmt, H), hr = expert_rows(fmt, I);
-  const int64_t per_token = xr.ld_codes + xr.ld_scales + k * (hr.ld_codes + hr.ld_scales + 4 * round_up(I, 4) + 2 * round_up(Ho, 8));
+  auto choose = [&](int64_t tokens) {
+    // rows of a tile by the mean of an expert's rows
+    const int64_t mean = tokens * k / E;
+    p.large = mean >= 24;
+    p.wm = 1; p.wn = 4; p.mtw = 1; p.ntw = 2; p.st = 4;
+    if (p.large) {
+      p.mtw = mean >= 96 ? 4 : 2;
+      p.st = fmt == SC_FP8_BLOCK || p.mtw == 2 ? 3 : 4;
+      if (mean >= 192 && fmt != SC_FP8_BLOCK) { p.wm = 2; p.wn = 2; p.ntw = 4; }
+    }
+    p.rows = (p.large ? 32 : 16) * p.wm * p.mtw;
+    p.h_quantized = p.large && fmt != SC_INT8;
+  };
+  choose(T);
+  // a pass's activations lie within 32-bit offsets and 1 GiB of workspace
+  const int64_t h_row = p.h_quantized ? 0 : 4 * round_up(I, 4);
+  const int64_t per_token = xr.ld_codes + xr.ld_scales + k * (hr.ld_codes + hr.ld_scales + h_row + 2 * round_up(Ho, 8));
   p.tokens = std::max<int64_t>(1, std::min<int64_t>(T, ((int64_t)1 << 30) / per_token));
   p.pairs = p.tokens * k;
-  // rows of a tile by the mean of an expert's rows
-  const int64_t mean = p.pairs / E;
-  p.wn = 4; p.st = 4; p.wm = 1; p.ntw = 2;
-  if (mean >= 192) { p.wm = 4; p.wn = 2; p.mtw = 4; p.ntw = 4; p.st = 3; }
-  else if (mean >= 96) { p.wm = 2; p.wn = 2; p.mtw = 4; p.ntw = 4; p.st = 3; }
-  else if (mean >= 16) p.mtw = 4;
-  else p.mtw = 1;
-  const int64_t R = 16 * p.wm * p.mtw;
-  p.max_tiles = std::min(p.pairs, p.pairs / R + std::min(E, p.pairs));
+  const bool quantized = p.h_quantized;
+  choose(p.tokens);
+  p.h_quantized = p.h_quantized && quantized;
+  p.max_tiles = std::min(p.pairs, p.pairs / p.rows + std::min(E, p.pairs));
   p.counter_bytes = 64 * 1024;
   p.meta_bytes = round_up(meta_bytes(p.pairs, p.max_tiles), 256);
   p.xcode_bytes = round_up(p.tokens * xr.ld_codes, 256);
   p.xscale_bytes = round_up(p.tokens * xr.ld_scales, 256);
-  p.h_bytes = round_up(p.pairs * 4 * round_up(I, 4), 256);
+  p.h_bytes = p.h_quantized ? 0 : round_up(p.pairs * 4 * round_up(I, 4), 256);
   p.hcode_bytes = round_up(p.pairs * hr.ld_codes, 256);
   p.hscale_bytes = round_up(p.pairs * hr.ld_scales, 256);
   p.d_bytes = round_up(p.pairs * 2 * round_up(Ho, 8), 256);
@@ -730,8 +709,9 @@ ExpertsPlan plan_experts(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, in
 
 std::string describe_experts(const ExpertsPlan& p) {
   char b[200];
-  std::snprintf(b, sizeof(b), "experts_product_kernel<WM=%d,WN=%d,MTW=%d,NTW=%d,ST=%d> tokens=%lld tiles<=%lld", p.wm,
-                p.wn, p.mtw, p.ntw, p.st, (long long)p.tokens, (long long)p.max_tiles);
+  std::snprintf(b, sizeof(b), "%s<WM=%d,WN=%d,MT=%d,NT=%d,ST=%d> rows=%d tokens=%lld tiles<=%lld",
+                !p.large ? "experts_product_kernel" : p.fmt == SC_FP8_BLOCK ? "experts_block_kernel" : "experts_tile_kernel", p.wm, p.wn, p.mtw, p.ntw, p.st, p.rows,
+                (long long)p.tokens, (long long)p.max_tiles);
   return std::string(b);
 }
 

@@ -32,7 +32,7 @@ hipError_t launch_route(bool f32, RouteArgs a, hipStream_t st);
 // chunks (ExpertRows), so that a product's row tile can take any rows:
 //   codes [row][KC * 128 B] (MXFP4: KC * 64 B), columns past K zero
 //   scales: MX [row][KC] dwords (byte j = the chunk's 32-block j), block FP8
-//   [row][KC] floats, INT8 [row] floats
+//   [row][KC] floats (KC rounded up to 4 in both), INT8 [row] floats
 // x lies so by token (the first product gathers its rows), the inner activation by
 // sorted row.
 struct ExpertRows {
@@ -40,7 +40,7 @@ struct ExpertRows {
 };
 inline ExpertRows expert_rows(int fmt, int64_t K) {
   const int64_t KC = round_up(K, 128) / 128;
-  return ExpertRows{KC * (fmt == SC_MXFP4 ? 64 : 128), fmt == SC_FP8 ? 0 : fmt == SC_INT8 ? 4 : KC * 4};
+  return ExpertRows{KC * (fmt == SC_MXFP4 ? 64 : 128), fmt == SC_FP8 ? 0 : fmt == SC_INT8 ? 4 : round_up(KC, 4) * 4};
 }
 
 constexpr int kMaxExperts = 1024;
@@ -49,7 +49,10 @@ constexpr int kMaxExperts = 1024;
 // offsets stay within 32 bits and the workspace within bounds) runs.
 struct ExpertsPlan {
   int fmt;
-  int wm, wn, mtw, ntw, st;  // product configuration, as ScPlan's
+  bool large;                // experts_tile_kernel (32 x 32 tiles), else experts_product_kernel (16 x 16)
+  int wm, wn, mtw, ntw, st;  // waves, tiles a wave, ring depth
+  int rows;                  // rows of a workgroup's tile
+  bool h_quantized;          // the first product quantizes the inner activation itself
   int64_t tokens;            // tokens a pass
   int64_t pairs;             // of a pass
   int64_t max_tiles;         // upper bound of a pass's row tiles
