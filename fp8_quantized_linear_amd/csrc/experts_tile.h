@@ -81,13 +81,13 @@ struct ProductArgs {
   float inv_scale;
 };
 
-// This workgroup's tile: expert, rows and column group.
+// A tile of a product: expert, rows and column group. An expert's row tiles of one
+// column group are neighbours in the order of tiles, and every XCD has a contiguous part
+// of that order (workgroups go to the eight XCDs in turn).
 struct TileAt {
   int expert, row0, rows, ngroup;
 };
-// An expert's row tiles of one column group are neighbours, and every XCD takes a
-// contiguous part of that order (workgroups go to the eight XCDs in turn). False past
-// the last tile.
+// This workgroup's tile; false past the last one.
 __device__ __forceinline__ bool find_tile(const ProductArgs& g, const Meta& meta, int R, TileAt& t) {
   const int total = meta.total_tiles[0] * g.ngroups;
   const int bid = blockIdx.x;
@@ -233,7 +233,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
   for (int mt = 0; mt < MT; ++mt) {
     rsc[mt] = 1.0f;
     if constexpr (T::INT) {
-      const uint32_t row = source_row<UP>(g, meta, tile, (wm * MT + mt) * 32 + (lane & 31));
+      const uint32_t row = source_row<UP>(g, meta, tile, (mt * WM + wm) * 32 + (lane & 31));
       rsc[mt] = *reinterpret_cast<const float*>(g.scales + (int64_t)row * g.rows.ld_scales);
     }
   }
@@ -265,7 +265,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
         }
       }
   };
-  // the rows of one wave row at a time through LDS
+  // the rows of one wave row at a time through LDS: row tiles pass, pass + WM, ..
   constexpr int PR = MT * 32;
   if (UP && g.act == kActSwiglu) {
     // Gated: 16 gate columns, then their 16 ups, so that registers r and r + 8 of a lane
@@ -308,7 +308,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
       // float32 rows: their scale needs all columns
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const int m = (wm * MT + mt) * 32 + (lane & 31);
+        const int m = (mt * WM + wm) * 32 + (lane & 31);
         float* const out = static_cast<float*>(g.out) + (int64_t)(tile.row0 + m) * g.ld_out + no + 4 * kb;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -354,7 +354,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const int m = (wm * MT + mt) * 32 + (lane & 31);
+        const int m = (mt * WM + wm) * 32 + (lane & 31);
         uint8_t* const dst = static_cast<uint8_t*>(g.out) + (int64_t)(tile.row0 + m) * g.hrows.ld_codes;
         uint8_t* const sc = g.hscales + (int64_t)(tile.row0 + m) * g.hrows.ld_scales;
 #pragma unroll
@@ -414,20 +414,19 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
       }
     };
     for (int pass = 0; pass < WM; ++pass) {
-      if (pass * PR >= tile.rows) break;
+      if (pass * 32 >= tile.rows) break;
       if (wm == pass) finish([&](int m, int c, const float4v& v) { *reinterpret_cast<float4v*>(z + m * pitch + c) = v; });
       __syncthreads();
-      const int rows = tile.rows - pass * PR < PR ? tile.rows - pass * PR : PR;
-      const int64_t row_at = tile.row0 + pass * PR;
+      auto row_of = [&](int m) { return ((m / 32) * WM + pass) * 32 + m % 32; };  // row of the tile
       if constexpr (T::INT) {
         // float32 rows: their scale needs all columns
-        float* const out = static_cast<float*>(g.out) + row_at * g.ld_out + no;
-        for (int i = tid; i < rows * (Co / 8); i += 256) {
+        float* const out = static_cast<float*>(g.out) + (int64_t)tile.row0 * g.ld_out + no;
+        for (int i = tid; i < PR * (Co / 8); i += 256) {
           const int m = i / (Co / 8), c = i % (Co / 8) * 8;
-          if (no + c < Nout) {  // Nout is a multiple of 32
+          if (row_of(m) < tile.rows && no + c < Nout) {  // Nout is a multiple of 32
             float v[8];
             outputs8(m, c / 8, v);
-            float* const dst = out + m * g.ld_out + c;
+            float* const dst = out + (int64_t)row_of(m) * g.ld_out + c;
             *reinterpret_cast<float4v*>(dst) = float4v{v[0], v[1], v[2], v[3]};
             *reinterpret_cast<float4v*>(dst + 4) = float4v{v[4], v[5], v[6], v[7]};
           }
@@ -435,25 +434,26 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
       } else {
         const int nb = Co / 32;  // a multiple of 4: a 128-group's blocks in neighbouring lanes
         const int64_t padded = g.hrows.ld_codes / (F == SC_MXFP4 ? 16 : 32);  // blocks of a row
-        for (int i = tid; i < (rows * nb + 255) / 256 * 256; i += 256) {
-          const bool inside = i < rows * nb;
-          const int m = inside ? i / nb : 0, b = inside ? i % nb : 0;
+        static_assert(PR * Co / 32 % 256 == 0, "whole rounds of threads");
+        for (int i = tid; i < PR * nb; i += 256) {
+          const int m = i / nb, b = i % nb;
           const int64_t at = no / 32 + b;  // block of the row
-          const bool valid = inside && no + b * 32 < Nout;
+          const bool valid = no + b * 32 < Nout;
           float v[32];
 #pragma unroll
           for (int j = 0; j < 4; ++j) outputs8(m, 4 * b + j, v + 8 * j);
           uint32_t w[8], sbyte = 0;
           float gs = 0.0f;
           quant_block32<F>(v, valid, g.inv_scale, w, sbyte, gs);
-          if (!inside || at >= padded) continue;
+          if (row_of(m) >= tile.rows || at >= padded) continue;
           if (!valid) {  // past the columns, up to the chunk: zeros
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[j] = 0u;
             sbyte = 0u;
           }
-          uint8_t* const dst = static_cast<uint8_t*>(g.out) + (row_at + m) * g.hrows.ld_codes;
-          uint8_t* const sc = g.hscales + (row_at + m) * g.hrows.ld_scales;
+          const int64_t row = tile.row0 + row_of(m);
+          uint8_t* const dst = static_cast<uint8_t*>(g.out) + row * g.hrows.ld_codes;
+          uint8_t* const sc = g.hscales + row * g.hrows.ld_scales;
           if (F == SC_MXFP4) {
             *reinterpret_cast<uint4v*>(dst + at * 16) = uint4v{w[0], w[1], w[2], w[3]};
           } else {
@@ -505,7 +505,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
           }
           swap_halves(w[0], w[2]);
           swap_halves(w[1], w[3]);
-          const int m = (wm * MT + mt) * 32 + (lane & 31), at = n0 + (wn * NT + nt) * 32 + 16 * j + 8 * kb;
+          const int m = (mt * WM + wm) * 32 + (lane & 31), at = n0 + (wn * NT + nt) * 32 + 16 * j + 8 * kb;
           if (m < tile.rows && at < (int)g.ld_out)
             *reinterpret_cast<uint4v*>(d + (int64_t)m * g.ld_out + at) = uint4v{w[0], w[1], w[2], w[3]};
         }
@@ -520,12 +520,11 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void experts_tile_kernel
   typedef TileConfig<F, WM, WN, MT, NT, ST> Cfg;
   constexpr int SUB = Cfg::SUB, PER = Cfg::PER_CHUNK, TA = Cfg::TA, TB = Cfg::TB, R = Cfg::R, L = Cfg::L;
   static_assert(!T::BLOCK && SUB == 1, "block FP8 has a kernel of its own");
-  constexpr int P = MT * NT;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Cfg::LDS];
   TileAt tile;
   if (!find_tile(g, meta, R, tile)) return;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const uint32_t lds0 = lds_offset(lds);
   const int stages = (int)g.KC * PER;
@@ -554,7 +553,7 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void experts_tile_kernel
   uint4v fa[2][MT][SUB][2], fb[2][NT][SUB][2];
   int sa[2][MT], sb[2][(NT + 1) / 2];  // MX: E8M0 words
   auto read_a = [&](int slot, int q, int mt) {
-    const uint8_t* const base = lds + slot * Cfg::STAGE + (wm * MT + mt) * 2 * SUB * 1024;
+    const uint8_t* const base = lds + slot * Cfg::STAGE + (mt * WM + wm) * 2 * SUB * 1024;
 #pragma unroll
     for (int s = 0; s < SUB; ++s) {
       fa[q][mt][s][0] = *reinterpret_cast<const uint4v*>(base + s * 1024 + a_at0);
@@ -577,7 +576,7 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void experts_tile_kernel
       if constexpr (T::MX) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
-          sa[q][mt] = (int)(*reinterpret_cast<const uint32_t*>(at + ((wm * MT + mt) * 32 + (lane & 31)) * 16 + cc * 4) >>
+          sa[q][mt] = (int)(*reinterpret_cast<const uint32_t*>(at + ((mt * WM + wm) * 32 + (lane & 31)) * 16 + cc * 4) >>
                             (8 * kb));
 #pragma unroll
         for (int np = 0; np < (NT + 1) / 2; ++np)
@@ -669,6 +668,10 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void experts_tile_kernel
   for (int mt = 0; mt < MT; ++mt) read_a(0, 0, mt);
 
   constexpr int FOUR = 4 * PER;  // stages of four chunks
+  // row tiles of this wave that hold rows: they go to the wave rows in turn, so that an
+  // expert's last rows cost what they are (in steps of 32 WM)
+  const int row_tiles = (tile.rows + 31) / 32;
+  const int used = (row_tiles - wm + WM - 1) / WM;
   auto iteration = [&](int i, int slot, int q, int h, bool first_of_four) {
     wait_vmcnt<L * (ST - 2)>();
     stage_barrier();
@@ -680,18 +683,16 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void experts_tile_kernel
     const int ni = i + 1;
     read_scales(ni / PER, PER == 2 ? (h ^ 1) : 0, q ^ 1);
     read_scales2(ni / PER, q ^ 1);
-    int p = 0;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int j = 0; j < L; ++j)
+        if ((j * MT) / L == mt) loads.stage(slot, rc, bv, j);
+      if (mt < used) {
 #pragma unroll
-        for (int j = 0; j < L; ++j)
-          if ((j * P) / L == p) loads.stage(slot, rc, bv, j);
-        mfma(q, mt, nt, h);
-        ++p;
+        for (int nt = 0; nt < NT; ++nt) mfma(q, mt, nt, h);
+        read_a(next_slot, q ^ 1, mt);
       }
-      read_a(next_slot, q ^ 1, mt);
       if (mt < NT) read_b(next_slot, q ^ 1, mt);
       __builtin_amdgcn_sched_barrier(0);
     }
