@@ -15,12 +15,14 @@
 // L2. The grid is the upper bound of tiles, known on the host; workgroups past the
 // true number end at once.
 #include <algorithm>
+#include <cmath>
 #include <cstddef>
 #include <cstdio>
 
 #include "fql_device.h"
 #include "fql_experts.h"
 #include "experts_tile.h"
+#include "experts_token.h"
 #include "fql_gemm.h"
 #include "sc_epilogue.h"
 #include "sc_quant.h"
@@ -29,17 +31,21 @@ namespace fql {
 
 namespace {
 
-constexpr int64_t meta_bytes(int64_t pairs, int64_t max_tiles) {
-  return 64 + (int64_t)kMaxExperts * (int64_t)sizeof(ExpertRange) + 4 * (max_tiles + 2 * pairs);
+constexpr int64_t meta_bytes(int64_t pairs, int64_t up_tiles, int64_t down_tiles) {
+  return 128 + 2 * (int64_t)kMaxExperts * (int64_t)sizeof(ExpertRange) + 4 * (up_tiles + down_tiles + 2 * pairs);
 }
-Meta meta_at(uint8_t* p, int64_t pairs, int64_t max_tiles) {
-  Meta m;
-  m.total_tiles = reinterpret_cast<int*>(p);
-  m.ranges = reinterpret_cast<ExpertRange*>(p + 64);
-  m.tile_expert = reinterpret_cast<int*>(m.ranges + kMaxExperts);
-  m.row_pair = m.tile_expert + max_tiles;
-  m.pair_row = m.row_pair + pairs;
-  return m;
+void meta_at(uint8_t* p, int64_t pairs, int64_t up_tiles, int64_t down_tiles, Meta (&m)[2]) {
+  const int64_t tiles[2] = {up_tiles, down_tiles};
+  ExpertRange* const ranges = reinterpret_cast<ExpertRange*>(p + 128);
+  int* at = reinterpret_cast<int*>(ranges + 2 * kMaxExperts);
+  for (int i = 0; i < 2; ++i) {
+    m[i].total_tiles = reinterpret_cast<int*>(p + 64 * i);
+    m[i].ranges = ranges + i * kMaxExperts;
+    m[i].tile_expert = at;
+    at += tiles[i];
+  }
+  m[0].row_pair = m[1].row_pair = at;
+  m[0].pair_row = m[1].pair_row = at + pairs;
 }
 
 // ---------------------------------------------------------------------------
@@ -54,12 +60,12 @@ constexpr int kPrepThreads = 512;
 // Each of `groups` workgroups places a part of the pairs, and counts all of them and
 // those of the parts before its own: without a wait for another workgroup. (Placing
 // is a scattered store a pair; one workgroup took 59 us for 32768 pairs.)
-__device__ __forceinline__ void sort_pairs(const int32_t* __restrict__ experts, int64_t pairs, int E, int tile_rows,
-                                           int groups, const Meta& m) {
+__device__ __forceinline__ void sort_pairs(const int32_t* __restrict__ experts, int64_t pairs, int E, int up_rows,
+                                           int down_rows, int groups, const Meta& up, const Meta& down) {
   __shared__ int count[kMaxExperts], row_at[kMaxExperts];
   const int64_t per = (pairs + groups - 1) / groups;
   const int64_t mine0 = blockIdx.x * per, mine1 = mine0 + per < pairs ? mine0 + per : pairs;
-  __shared__ int part_rows[kPrepThreads / 64], part_tiles[kPrepThreads / 64];
+  __shared__ int part_rows[kPrepThreads / 64], part_tiles[2][kPrepThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   for (int e = tid; e < E; e += kPrepThreads) count[e] = row_at[e] = 0;
   __syncthreads();
@@ -85,50 +91,62 @@ __device__ __forceinline__ void sort_pairs(const int32_t* __restrict__ experts, 
   __syncthreads();
   // exclusive sums of rows and tiles over the experts, two experts a thread
   static_assert(kMaxExperts <= 2 * kPrepThreads, "experts a thread");
-  int c[2], t[2];
-  int rows = 0, tiles = 0;
+  int c[2], t[2][2];  // rows of an expert, its tiles in each product
+  int rows = 0, tiles[2] = {0, 0};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int e = 2 * tid + j;
     c[j] = e < E ? count[e] : 0;
-    t[j] = (c[j] + tile_rows - 1) / tile_rows;
+    t[0][j] = (c[j] + up_rows - 1) / up_rows;
+    t[1][j] = (c[j] + down_rows - 1) / down_rows;
     rows += c[j];
-    tiles += t[j];
+    tiles[0] += t[0][j];
+    tiles[1] += t[1][j];
   }
-  int rs = rows, ts = tiles;
+  int rs = rows, ts[2] = {tiles[0], tiles[1]};
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int r1 = __shfl_up(rs, o), t1 = __shfl_up(ts, o);
+    const int r1 = __shfl_up(rs, o), a1 = __shfl_up(ts[0], o), b1 = __shfl_up(ts[1], o);
     if (lane >= o) {
       rs += r1;
-      ts += t1;
+      ts[0] += a1;
+      ts[1] += b1;
     }
   }
   if (lane == 63) {
     part_rows[wave] = rs;
-    part_tiles[wave] = ts;
+    part_tiles[0][wave] = ts[0];
+    part_tiles[1][wave] = ts[1];
   }
   __syncthreads();
-  int row0 = rs - rows, tile0 = ts - tiles, all = 0;
+  int row0 = rs - rows, tile0[2] = {ts[0] - tiles[0], ts[1] - tiles[1]}, all[2] = {0, 0};
   for (int w = 0; w < kPrepThreads / 64; ++w) {
     if (w < wave) {
       row0 += part_rows[w];
-      tile0 += part_tiles[w];
+      tile0[0] += part_tiles[0][w];
+      tile0[1] += part_tiles[1][w];
     }
-    all += part_tiles[w];
+    all[0] += part_tiles[0][w];
+    all[1] += part_tiles[1][w];
   }
-  if (tid == 0 && blockIdx.x == 0) m.total_tiles[0] = all;
+  if (tid == 0 && blockIdx.x == 0) {
+    up.total_tiles[0] = all[0];
+    down.total_tiles[0] = all[1];
+  }
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int e = 2 * tid + j;
     if (e < E) {
       row_at[e] += row0;
       if (blockIdx.x == 0) {
-        m.ranges[e] = ExpertRange{tile0, t[j], row0, c[j]};
-        for (int i = 0; i < t[j]; ++i) m.tile_expert[tile0 + i] = e;
+        up.ranges[e] = ExpertRange{tile0[0], t[0][j], row0, c[j]};
+        down.ranges[e] = ExpertRange{tile0[1], t[1][j], row0, c[j]};
+        for (int i = 0; i < t[0][j]; ++i) up.tile_expert[tile0[0] + i] = e;
+        for (int i = 0; i < t[1][j]; ++i) down.tile_expert[tile0[1] + i] = e;
       }
       row0 += c[j];
-      tile0 += t[j];
+      tile0[0] += t[0][j];
+      tile0[1] += t[1][j];
     }
   }
   __syncthreads();
@@ -140,8 +158,8 @@ __device__ __forceinline__ void sort_pairs(const int32_t* __restrict__ experts, 
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int64_t i = i0 + tid + (int64_t)j * kPrepThreads;
-      if (r[j] >= 0) m.row_pair[r[j]] = (int)i;
-      if (i < mine1) m.pair_row[i] = r[j];
+      if (r[j] >= 0) up.row_pair[r[j]] = (int)i;
+      if (i < mine1) up.pair_row[i] = r[j];
     }
   }
 }
@@ -240,9 +258,9 @@ int64_t quant_units(int fmt, const QuantArgs& a) {
 // The first workgroups sort while the others quantize.
 template <int F>
 __global__ __launch_bounds__(kPrepThreads) void experts_prepare_kernel(const int32_t* __restrict__ experts,
-                                                                       int64_t pairs, int E, int tile_rows, int groups,
-                                                                       Meta m, QuantArgs q) {
-  if ((int)blockIdx.x < groups) sort_pairs(experts, pairs, E, tile_rows, groups, m);
+                                                                       int64_t pairs, int E, int up_rows, int down_rows,
+                                                                       int groups, Meta up, Meta down, QuantArgs q) {
+  if ((int)blockIdx.x < groups) sort_pairs(experts, pairs, E, up_rows, down_rows, groups, up, down);
   else quant_rows<F, uint16_t>(q, (int64_t)blockIdx.x - groups);
 }
 
@@ -576,13 +594,13 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(const uint16_t* __
 
 // (WM, WN, MTW, NTW, ST) of experts_product_kernel: row tiles of 16, 128 columns.
 #define FQL_EXPERT_CONFIGS(X) X(1, 4, 1, 2, 4)
-// (MT, ST) of experts_block_kernel: 64 and 128 rows, 256 columns.
-#define FQL_BLOCK_CONFIGS(X) X(2, 3) X(4, 3)
+// (WM, MT, ST, EARLY) of experts_block_kernel: 64, 128 and 256 rows, 256 columns.
+#define FQL_BLOCK_CONFIGS(X) X(1, 2, 3, 4) X(1, 4, 3, 8) X(2, 4, 2, 4)
 // (WM, WN, MT, NT, ST) of experts_tile_kernel: 64, 128 and 256 rows, 256 columns.
 #define FQL_TILE_CONFIGS(X) X(1, 4, 2, 2, 3) X(1, 4, 4, 2, 4) X(2, 2, 4, 4, 4)
 
 template <int F, bool UP>
-hipError_t launch_product(const ExpertsPlan& p, const ProductArgs& g, const Meta& m, hipStream_t st) {
+hipError_t launch_product(const ProductPlan& p, const ProductArgs& g, const Meta& m, hipStream_t st) {
   const unsigned grid = (unsigned)(p.max_tiles * g.ngroups);
 #define FQL_X(A, B, C, D, S)                                                                       \
   if (!p.large && p.wm == A && p.wn == B && p.mtw == C && p.ntw == D && p.st == S) {                \
@@ -592,9 +610,9 @@ hipError_t launch_product(const ExpertsPlan& p, const ProductArgs& g, const Meta
   FQL_EXPERT_CONFIGS(FQL_X)
 #undef FQL_X
   if constexpr (F == SC_FP8_BLOCK) {
-#define FQL_X(C, S)                                                                                     \
-  if (p.large && p.wm == 1 && p.wn == 4 && p.ntw == 2 && p.mtw == C && p.st == S) {                      \
-    experts_block_kernel<C, S, UP><<<grid, 256, TileConfig<F, 1, 4, C, 2, S>::LDS, st>>>(g, m);          \
+#define FQL_X(A, C, S, E)                                                                                \
+  if (p.large && p.wm == A && p.wn == 4 && p.ntw == 2 && p.mtw == C && p.st == S) {                      \
+    experts_block_kernel<A, C, S, E, UP><<<grid, 256 * A, TileConfig<F, A, 4, C, 2, S>::LDS, st>>>(g, m); \
     return hipGetLastError();                                                                            \
   }
     FQL_BLOCK_CONFIGS(FQL_X)
@@ -611,19 +629,19 @@ hipError_t launch_product(const ExpertsPlan& p, const ProductArgs& g, const Meta
   return hipErrorInvalidValue;
 }
 
-ProductArgs product_args(const ExpertsPlan& p, const ExpertWeights& w, const uint8_t* codes, const uint8_t* scales) {
-  const ScDims d = sc_dims(p.fmt, w.N, w.K, true);
+ProductArgs product_args(int fmt, const ProductPlan& p, const ExpertWeights& w, const uint8_t* codes,
+                         const uint8_t* scales) {
+  const ScDims d = sc_dims(fmt, w.N, w.K, true);
   ProductArgs g{};
   g.codes = codes;
   g.scales = scales;
-  g.rows = expert_rows(p.fmt, w.K);
+  g.rows = expert_rows(fmt, w.K);
   g.packed = w.packed;
   g.stride = w.stride;
   g.code_bytes = d.code_bytes;
   g.N = (int)w.N;
   g.ntiles_w = (int)(d.rows_p / 16);
-  const int64_t cols = (p.large ? 32 : 16) * p.wn * p.ntw;
-  g.ngroups = (int)((w.N + cols - 1) / cols);
+  g.ngroups = p.cols > 0 ? (int)((w.N + p.cols - 1) / p.cols) : 0;
   g.quads_w = d.quads;
   g.KC = d.KC;
   g.alpha = w.alpha;
@@ -632,7 +650,29 @@ ProductArgs product_args(const ExpertsPlan& p, const ExpertWeights& w, const uin
 }
 
 template <int F>
+hipError_t launch_token(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspace, hipStream_t st) {
+  float* const h = reinterpret_cast<float*>(workspace + p.counter_bytes);
+  const ProductPlan none{};
+  ProductArgs g = product_args(F, none, a.up, nullptr, nullptr);
+  g.act = a.act;
+  g.k = a.k;
+  g.ld_out = round_up(a.I, 4);
+  experts_token_up_kernel<F><<<dim3((unsigned)((a.up.N + 31) / 32), (unsigned)(a.T * a.k)), 256, 0, st>>>(
+      a.x, a.ldx, a.up.inv_scale, a.up.K, a.experts, a.E, g, h);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  g = product_args(F, none, a.down, nullptr, nullptr);
+  g.k = a.k;
+  // waves without a row of their own share the others' K
+  const int parts = (int)std::min<int64_t>(std::max(1, 16 / a.k), g.KC);
+  experts_token_down_kernel<F><<<dim3((unsigned)((a.down.N + 15) / 16), (unsigned)a.T), 1024, 0, st>>>(
+      h, round_up(a.I, 4), a.down.inv_scale, a.I, a.experts, a.weights, a.E, parts, g, a.residual, a.ldr, a.y, a.ldy);
+  return hipGetLastError();
+}
+
+template <int F>
 hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspace, hipStream_t st) {
+  if (p.token) return launch_token<F>(p, a, workspace, st);
   uint8_t* at = workspace + p.counter_bytes;
   auto take = [&](int64_t bytes) {
     uint8_t* const r = at;
@@ -646,16 +686,17 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
   uint8_t* const hc = take(p.hcode_bytes);
   uint8_t* const hs = take(p.hscale_bytes);
   uint8_t* const d = take(p.d_bytes);
-  const Meta m = meta_at(meta, p.pairs, p.max_tiles);
+  Meta m[2];
+  meta_at(meta, p.pairs, p.up.max_tiles, p.down.max_tiles, m);
   for (int64_t t0 = 0; t0 < a.T; t0 += p.tokens) {
     const int64_t T = std::min(p.tokens, a.T - t0), pairs = T * a.k;
     QuantArgs q{a.x + t0 * a.ldx, T, a.up.K, a.ldx, a.aligned, a.up.inv_scale, expert_rows(F, a.up.K), xc, xs};
     const int groups = (int)std::min<int64_t>(32, (pairs + 2047) / 2048);
     experts_prepare_kernel<F><<<(unsigned)(groups + quant_units(F, q)), kPrepThreads, 0, st>>>(
-        a.experts + t0 * a.k, pairs, a.E, p.rows, groups, m, q);
+        a.experts + t0 * a.k, pairs, a.E, p.up.rows, p.down.rows, groups, m[0], m[1], q);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    ProductArgs g = product_args(p, a.up, xc, xs);
+    ProductArgs g = product_args(F, p.up, a.up, xc, xs);
     g.act = a.act;
     g.k = a.k;
     g.hrows = expert_rows(F, a.I);
@@ -663,7 +704,7 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
     g.inv_scale = a.down.inv_scale;
     g.out = p.h_quantized ? hc : h;
     g.ld_out = round_up(a.I, 4);
-    e = launch_product<F, true>(p, g, m, st);
+    e = launch_product<F, true>(p.up, g, m[0], st);
     if (e != hipSuccess) return e;
     if (!p.h_quantized) {
       q = QuantArgs{h, pairs, a.I, round_up(a.I, 4), true, a.down.inv_scale, expert_rows(F, a.I), hc, hs};
@@ -671,11 +712,11 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
       e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    g = product_args(p, a.down, hc, hs);
+    g = product_args(F, p.down, a.down, hc, hs);
     g.out = d;
     g.ld_out = round_up(a.down.N, 8);
     g.k = a.k;
-    e = launch_product<F, false>(p, g, m, st);
+    e = launch_product<F, false>(p.down, g, m[1], st);
     if (e != hipSuccess) return e;
     uint16_t* const y = a.y + t0 * a.ldy;
     const uint16_t* const r = a.residual != nullptr ? a.residual + t0 * a.ldr : nullptr;
@@ -683,7 +724,7 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
     const bool vec = whole(a.y, a.ldy) && (r == nullptr || whole(a.residual, a.ldr));
     const int64_t items = T * ((a.down.N + 7) / 8);
     experts_combine_kernel<<<(unsigned)((items + 255) / 256), 256, 0, st>>>(
-        reinterpret_cast<const uint16_t*>(d), round_up(a.down.N, 8), T, a.down.N, a.weights + t0 * a.k, m.pair_row, a.k,
+        reinterpret_cast<const uint16_t*>(d), round_up(a.down.N, 8), T, a.down.N, a.weights + t0 * a.k, m[0].pair_row, a.k,
         r, a.ldr, y, a.ldy, vec);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -693,52 +734,88 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
 
 }  // namespace
 
+// The tile of one product, N columns of a K-deep product, `pairs` rows over E experts:
+// 16 x 128 while an expert has few rows (a workgroup streams its weight columns), else
+// the tile of least time: rounds of the card's workgroups times (chunks * tc + f) us.
+// The number of row tiles is estimated with six tenths of a tile an expert for its last
+// rows.
+static ProductPlan plan_product(int fmt, int64_t pairs, int64_t E, int64_t N, int64_t K) {
+  struct Tile {
+    int wm, wn, mtw, ntw, st, resident;
+    double tc[3], f;  // MXFP4, block FP8, the others
+  };
+  static constexpr Tile tiles[] = {{1, 4, 2, 2, 3, 2, {1.00, 1.00, 1.40}, 5.0},
+                                   {1, 4, 4, 2, 4, 1, {0.85, 1.45, 1.35}, 5.0},
+                                   {2, 2, 4, 4, 4, 1, {1.04, 1.92, 1.60}, 8.0}};
+  const bool block = fmt == SC_FP8_BLOCK;
+  const int64_t KC = round_up(K, 128) / 128;
+  ProductPlan p{};
+  if (pairs / E >= 24) {
+    double best = 0.0;
+    for (const Tile& t : tiles) {
+      const int64_t R = 32 * t.wm * t.mtw;
+      const double rows = (double)pairs / (double)R + 0.6 * (double)E;
+      const int resident = block ? 1 : t.resident;
+      const double full = rows * (double)((N + 255) / 256) / (256.0 * resident);
+      const double rounds = full < 4.0 ? std::ceil(full) : full + 0.3;
+      const double cost = rounds * ((double)KC * t.tc[fmt == SC_MXFP4 ? 0 : block ? 1 : 2] + t.f);
+      if (p.large && cost >= best) continue;
+      best = cost;
+      p = ProductPlan{true, t.wm, t.wn, t.mtw, t.ntw, t.st, (int)R, 256, 0};
+      if (block) {  // experts_block_kernel's forms of them
+        p.wn = 4;
+        p.ntw = 2;
+        p.st = t.wm == 2 ? 2 : 3;
+      }
+    }
+  } else {
+    p = ProductPlan{false, 1, 4, 1, 2, 4, 16, 128, 0};
+  }
+  p.max_tiles = std::min(pairs, pairs / p.rows + std::min(E, pairs));
+  return p;
+}
+
 ExpertsPlan plan_experts(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, int64_t N, int64_t I, int64_t Ho) {
   ExpertsPlan p{};
   p.fmt = fmt;
   const ExpertRows xr = expert_rows(fmt, H), hr = expert_rows(fmt, I);
-  auto choose = [&](int64_t tokens) {
-    // rows of a tile by the mean of an expert's rows
-    const int64_t mean = tokens * k / E;
-    p.large = mean >= 24;
-    p.wm = 1; p.wn = 4; p.mtw = 1; p.ntw = 2; p.st = 4;
-    if (p.large) {
-      p.mtw = mean >= 96 ? 4 : 2;
-      p.st = fmt == SC_FP8_BLOCK || p.mtw == 2 ? 3 : 4;
-      if (mean >= 192 && fmt != SC_FP8_BLOCK) { p.wm = 2; p.wn = 2; p.ntw = 4; }
-    }
-    p.rows = (p.large ? 32 : 16) * p.wm * p.mtw;
-    p.h_quantized = p.large && fmt != SC_INT8;
-  };
-  choose(T);
   // a pass's activations lie within 32-bit offsets and 1 GiB of workspace
-  const int64_t h_row = p.h_quantized ? 0 : 4 * round_up(I, 4);
-  const int64_t per_token = xr.ld_codes + xr.ld_scales + k * (hr.ld_codes + hr.ld_scales + h_row + 2 * round_up(Ho, 8));
+  const int64_t per_token = xr.ld_codes + xr.ld_scales + k * (hr.ld_codes + hr.ld_scales + 4 * round_up(I, 4) + 2 * round_up(Ho, 8));
   p.tokens = std::max<int64_t>(1, std::min<int64_t>(T, ((int64_t)1 << 30) / per_token));
   p.pairs = p.tokens * k;
-  const bool quantized = p.h_quantized;
-  choose(p.tokens);
-  p.h_quantized = p.h_quantized && quantized;
-  p.max_tiles = std::min(p.pairs, p.pairs / p.rows + std::min(E, p.pairs));
+  p.up = plan_product(fmt, p.pairs, E, N, H);
+  p.down = plan_product(fmt, p.pairs, E, Ho, I);
+  // A few tokens, every pair for itself: two launches for five, but an expert that several
+  // tokens choose is read for each. 64 experts, 8 a token (block FP8, 2048, 1024 inner):
+  // 1 token 17 us (sorted 32), 4 tokens 37 (52), 8 tokens 63 (69), 12 tokens 89 (80); 8
+  // experts, 2 a token (FP8, 4096, 14336): 1 token 64 (93), 2 tokens 118 (127), 3 tokens
+  // 170 (159); 128 experts, 8 a token (MXFP4, 4096, 1280): 6 tokens 82 (84), 8 tokens 105 (100).
+  p.token = T == 1 || (T <= 6 && p.tokens == T && 4 * p.pairs < 3 * E);
+  p.h_quantized = !p.token && p.up.large && fmt != SC_INT8;
   p.counter_bytes = 64 * 1024;
-  p.meta_bytes = round_up(meta_bytes(p.pairs, p.max_tiles), 256);
+  p.meta_bytes = round_up(meta_bytes(p.pairs, p.up.max_tiles, p.down.max_tiles), 256);
   p.xcode_bytes = round_up(p.tokens * xr.ld_codes, 256);
   p.xscale_bytes = round_up(p.tokens * xr.ld_scales, 256);
   p.h_bytes = p.h_quantized ? 0 : round_up(p.pairs * 4 * round_up(I, 4), 256);
   p.hcode_bytes = round_up(p.pairs * hr.ld_codes, 256);
   p.hscale_bytes = round_up(p.pairs * hr.ld_scales, 256);
   p.d_bytes = round_up(p.pairs * 2 * round_up(Ho, 8), 256);
+  if (p.token) p.meta_bytes = p.xcode_bytes = p.xscale_bytes = p.hcode_bytes = p.hscale_bytes = p.d_bytes = 0;
   p.total_bytes = p.counter_bytes + p.meta_bytes + p.xcode_bytes + p.xscale_bytes + p.h_bytes + p.hcode_bytes +
                   p.hscale_bytes + p.d_bytes;
   return p;
 }
 
 std::string describe_experts(const ExpertsPlan& p) {
-  char b[200];
-  std::snprintf(b, sizeof(b), "%s<WM=%d,WN=%d,MT=%d,NT=%d,ST=%d> rows=%d tokens=%lld tiles<=%lld",
-                !p.large ? "experts_product_kernel" : p.fmt == SC_FP8_BLOCK ? "experts_block_kernel" : "experts_tile_kernel", p.wm, p.wn, p.mtw, p.ntw, p.st, p.rows,
-                (long long)p.tokens, (long long)p.max_tiles);
-  return std::string(b);
+  auto name = [&](const ProductPlan& q) {
+    char b[100];
+    std::snprintf(b, sizeof(b), "%s<WM=%d,WN=%d,MT=%d,NT=%d,ST=%d> tiles=%dx%d",
+                  !q.large ? "experts_product_kernel" : p.fmt == SC_FP8_BLOCK ? "experts_block_kernel" : "experts_tile_kernel",
+                  q.wm, q.wn, q.mtw, q.ntw, q.st, q.rows, q.cols);
+    return std::string(b);
+  };
+  if (p.token) return "experts_token_up_kernel + experts_token_down_kernel tokens=" + std::to_string(p.tokens);
+  return "up " + name(p.up) + " down " + name(p.down) + " tokens=" + std::to_string(p.tokens);
 }
 
 hipError_t launch_experts(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspace, hipStream_t st) {

@@ -37,13 +37,13 @@ typedef int int8v __attribute__((ext_vector_type(8)));
 typedef int int4v __attribute__((ext_vector_type(4)));
 typedef int int16v __attribute__((ext_vector_type(16)));
 
-// One expert's part of a pass: its first row tile, their number, its first row
-// and the number of its rows.
+// One expert's part of a pass for one of the products: its first row tile, their
+// number, its first row and the number of its rows.
 struct ExpertRange {
   int tile0, tiles, row0, rows;
 };
 
-// Metadata of a pass in the workspace.
+// Metadata of a pass in the workspace, as one of the products sees it.
 struct Meta {
   int* total_tiles;     // [0]
   ExpertRange* ranges;  // [E]
@@ -140,20 +140,22 @@ struct TileConfig {
   static constexpr int RING = ST * STAGE;
   static constexpr int OUT = MT * 32 * (C + 4) * 4;                // float32 rows of one wave row (epilogue)
   static constexpr int LDS = RING + 2 * (ASC + BSC) > OUT ? RING + 2 * (ASC + BSC) : OUT;
-  static constexpr int L = (TA + TB) * SUB / 4;                    // loads a wave and stage
-  static_assert(TA % 4 == 0 && TB % 4 == 0 && WM * WN == 4, "tiles a wave loads");
+  static constexpr int NW = WM * WN;                               // waves
+  static constexpr int L = (TA + TB) * SUB / NW;                   // loads a wave and stage
+  static_assert(TA % NW == 0 && TB % NW == 0 && NW % 4 == 0, "tiles a wave loads");
   static_assert(L * (ST - 1) <= 63, "vmcnt range");
   static_assert(LDS <= 160 * 1024, "LDS");
 };
 
-// A workgroup's loads from memory into the ring. Of a stage, wave w takes the
-// activation tiles w, w + 4, .. and the weight tiles likewise, each in SUB pieces.
+// A workgroup's loads from memory into the ring. Of a stage, wave w of NW takes the
+// activation tiles w, w + NW, .. and the weight tiles likewise, each in SUB pieces.
 template <int F, typename Cfg, bool UP>
 struct TileLoads {
   typedef Traits<F> T;
-  static constexpr int SUB = Cfg::SUB, TA = Cfg::TA, TB = Cfg::TB, L = Cfg::L, QA = Cfg::R / 64, QB = Cfg::C / 64;
-  const uint8_t *codes, *scales, *wscales, *b_src[TB / 4];
-  uint32_t a_voff[TA / 4], as_voff, lds0;
+  static constexpr int SUB = Cfg::SUB, TA = Cfg::TA, TB = Cfg::TB, L = Cfg::L, NW = Cfg::NW;
+  static constexpr int QA = Cfg::R / 64, QB = Cfg::C / 64;
+  const uint8_t *codes, *scales, *wscales, *b_src[TB / NW];
+  uint32_t a_voff[TA / NW], as_voff, lds0;
   int KC, ntiles_w, b_tile0, wave, lane;
   int64_t quads_w;
   __device__ __forceinline__ TileLoads(const ProductArgs& g, const Meta& meta, const TileAt& tile, uint32_t lds0,
@@ -163,13 +165,13 @@ struct TileLoads {
     const uint8_t* const wcodes = g.packed + tile.expert * g.stride;
     wscales = wcodes + g.code_bytes;
 #pragma unroll
-    for (int j = 0; j < TA / 4; ++j) {
+    for (int j = 0; j < TA / NW; ++j) {
       const int r = lane >> 2, p = (lane & 3) ^ ((r >> 2) & 3);
-      a_voff[j] = source_row<UP>(g, meta, tile, (wave + 4 * j) * 16 + r) * (uint32_t)g.rows.ld_codes + (uint32_t)p * 16u;
+      a_voff[j] = source_row<UP>(g, meta, tile, (wave + NW * j) * 16 + r) * (uint32_t)g.rows.ld_codes + (uint32_t)p * 16u;
     }
 #pragma unroll
-    for (int j = 0; j < TB / 4; ++j) {
-      const int t = b_tile0 + wave + 4 * j;
+    for (int j = 0; j < TB / NW; ++j) {
+      const int t = b_tile0 + wave + NW * j;
       b_src[j] = wcodes + (int64_t)(t < g.ntiles_w ? t : 0) * g.KC * (1024 * T::H);  // past N: tile 0, never stored
     }
     as_voff = 0u;
@@ -182,13 +184,13 @@ struct TileLoads {
   }
   // load j of the wave's L of a stage, into a slot of the ring
   __device__ __forceinline__ void stage(int slot, int st, uint32_t bv, int j) const {
-    if (j < TA / 4 * SUB) {
+    if (j < TA / NW * SUB) {
       const int t = j / SUB, s = j % SUB;
       lds_load16(codes + (int64_t)(st * SUB + s) * 64, a_voff[t],
-                 lds0 + slot * Cfg::STAGE + ((wave + 4 * t) * SUB + s) * 1024);
+                 lds0 + slot * Cfg::STAGE + ((wave + NW * t) * SUB + s) * 1024);
     } else {
-      const int t = (j - TA / 4 * SUB) / SUB, s = (j - TA / 4 * SUB) % SUB;
-      lds_load16(b_src[t], bv + s * 1024u, lds0 + slot * Cfg::STAGE + ((TA + wave + 4 * t) * SUB + s) * 1024);
+      const int t = (j - TA / NW * SUB) / SUB, s = (j - TA / NW * SUB) % SUB;
+      lds_load16(b_src[t], bv + s * 1024u, lds0 + slot * Cfg::STAGE + ((TA + wave + NW * t) * SUB + s) * 1024);
     }
   }
   // scales of four chunks from chunk c0 on, into buffer q
@@ -336,19 +338,19 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
         }
       if constexpr (T::BLOCK) {
         // the four blocks of a 128-group lie in as many waves (or half of them): joined through LDS
-        static_assert(WM == 1 && (WN * NP) % 4 == 0, "a group's blocks in one workgroup");
+        static_assert((WN * NP) % 4 == 0, "a group's blocks in one workgroup");
         float* const tops = reinterpret_cast<float*>(lds);  // [block][row]
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int p = 0; p < NP; ++p)
-            if (kb == 0) tops[(wn * NP + p) * R + mt * 32 + lane] = top[mt][p];
+            if (kb == 0) tops[(wn * NP + p) * R + (mt * WM + wm) * 32 + lane] = top[mt][p];
         __syncthreads();
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            const float* const t = tops + (wn * NP + p) / 4 * 4 * R + mt * 32 + (lane & 31);
+            const float* const t = tops + (wn * NP + p) / 4 * 4 * R + (mt * WM + wm) * 32 + (lane & 31);
             top[mt][p] = __builtin_fmaxf(__builtin_fmaxf(t[0], t[R]), __builtin_fmaxf(t[2 * R], t[3 * R]));
           }
       }
@@ -421,7 +423,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
       if constexpr (T::INT) {
         // float32 rows: their scale needs all columns
         float* const out = static_cast<float*>(g.out) + (int64_t)tile.row0 * g.ld_out + no;
-        for (int i = tid; i < PR * (Co / 8); i += 256) {
+        for (int i = tid; i < PR * (Co / 8); i += 64 * WM * WN) {
           const int m = i / (Co / 8), c = i % (Co / 8) * 8;
           if (row_of(m) < tile.rows && no + c < Nout) {  // Nout is a multiple of 32
             float v[8];
@@ -434,8 +436,8 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
       } else {
         const int nb = Co / 32;  // a multiple of 4: a 128-group's blocks in neighbouring lanes
         const int64_t padded = g.hrows.ld_codes / (F == SC_MXFP4 ? 16 : 32);  // blocks of a row
-        static_assert(PR * Co / 32 % 256 == 0, "whole rounds of threads");
-        for (int i = tid; i < PR * nb; i += 256) {
+        static_assert(PR * Co / 32 % (64 * WM * WN) == 0, "whole rounds of threads");
+        for (int i = tid; i < PR * nb; i += 64 * WM * WN) {
           const int m = i / nb, b = i % nb;
           const int64_t at = no / 32 + b;  // block of the row
           const bool valid = no + b * 32 < Nout;
@@ -711,18 +713,21 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void experts_tile_kernel
   finish_tile<F, WM, WN, MT, NT, UP>(g, meta, tile, acc, loads.wscales, tile.ngroup * TB * 16, lds);
 }
 
-// Block FP8: rows x 256 columns, 128 MT x 64 a wave. Every 128-deep chunk's products go
+// Block FP8: 32 MT WM rows x 256 columns, 32 MT x 64 a wave. Every 128-deep chunk's products go
 // into a fresh accumulator, which vector instructions add: from vector registers, since
 // from accumulation registers each addition would cost a move besides. That leaves 256
 // registers: 128 for the sums, 32 for the products of two tiles in turn (a tile's are
 // added while the next one's are made), 32 for the chunk's weight tiles and 32 for two
 // row tiles in turn. So operands are read one row tile ahead, and the weight tiles of
 // the next chunk behind the last products that need the old ones.
-template <int MT, int ST, bool UP>
-__global__ __launch_bounds__(256, 2) void experts_block_kernel(const ProductArgs g, const Meta meta) {
+// EARLY: a refill's loads go out in its first EARLY of P steps (a ring of two chunks
+// leaves them little more than one chunk's time).
+template <int WM, int MT, int ST, int EARLY, bool UP>
+__global__ __launch_bounds__(256 * WM, 2) void experts_block_kernel(const ProductArgs g, const Meta meta) {
   constexpr int F = SC_FP8_BLOCK, WN = 4, NT = 2;
-  typedef TileConfig<F, 1, WN, MT, NT, ST> Cfg;
+  typedef TileConfig<F, WM, WN, MT, NT, ST> Cfg;
   constexpr int TA = Cfg::TA, TB = Cfg::TB, R = Cfg::R, L = Cfg::L, P = MT * NT;
+  static_assert(EARLY >= NT && EARLY <= P, "refill steps");
   static_assert(MT % 2 == 0, "row tiles in two register sets");
   extern __shared__ __attribute__((aligned(1024))) uint8_t block_lds[];  // Cfg::LDS bytes
   uint8_t* const lds = block_lds;
@@ -730,6 +735,7 @@ __global__ __launch_bounds__(256, 2) void experts_block_kernel(const ProductArgs
   if (!find_tile(g, meta, R, tile)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
   const TileLoads<F, Cfg, UP> loads(g, meta, tile, lds_offset(lds), wave, lane);
   const int chunks = (int)g.KC;
 
@@ -749,7 +755,7 @@ __global__ __launch_bounds__(256, 2) void experts_block_kernel(const ProductArgs
   uint4v fa[2][2][2], fb[NT][2][2];  // [set or tile][piece of the chunk][16 bytes]
   float rs[MT];                      // the lane's row scales times the column block's
   auto read_a = [&](int slot, int mt) {
-    const uint8_t* const base = lds + slot * Cfg::STAGE + mt * 4096;
+    const uint8_t* const base = lds + slot * Cfg::STAGE + (mt * WM + wm) * 4096;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       fa[mt & 1][s][0] = *reinterpret_cast<const uint4v*>(base + s * 1024 + a_at0);
@@ -757,7 +763,7 @@ __global__ __launch_bounds__(256, 2) void experts_block_kernel(const ProductArgs
     }
   };
   auto read_b = [&](int slot, int nt) {
-    const uint8_t* const base = lds + slot * Cfg::STAGE + (TA + (wave * NT + nt) * 2) * 2048;
+    const uint8_t* const base = lds + slot * Cfg::STAGE + (TA + (wn * NT + nt) * 2) * 2048;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       fb[nt][s][0] = *reinterpret_cast<const uint4v*>(base + s * 1024 + b_at);
@@ -766,8 +772,8 @@ __global__ __launch_bounds__(256, 2) void experts_block_kernel(const ProductArgs
   };
   auto read_rs = [&](int c, int mt) {
     const uint8_t* const at = lds + Cfg::RING + ((c >> 2) & 1) * (Cfg::ASC + Cfg::BSC) + (c & 3) * 4;
-    rs[mt] = *reinterpret_cast<const float*>(at + (mt * 32 + (lane & 31)) * 16) *
-             *reinterpret_cast<const float*>(at + Cfg::ASC + (wave * NT * 32 / 128) * 256);
+    rs[mt] = *reinterpret_cast<const float*>(at + ((mt * WM + wm) * 32 + (lane & 31)) * 16) *
+             *reinterpret_cast<const float*>(at + Cfg::ASC + (wn * NT * 32 / 128) * 256);
   };
   auto wide = [](const uint4v& x, const uint4v& y) {
     return int8v{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
@@ -779,14 +785,15 @@ __global__ __launch_bounds__(256, 2) void experts_block_kernel(const ProductArgs
   };
   // A chunk's refill (of the slot that it leaves, with the chunk ST further on) begins in
   // its last row tile, behind the barrier after which nobody reads the slot, and goes on
-  // through the next chunk: load j at step (j P) / L of the steps counted from there.
+  // through the next chunk: load j at step (j EARLY) / L of the steps counted from there.
   auto refill = [&](int slot, int c, int step) {
     const int rc = c < chunks ? c : chunks - 1;  // past the end: the last chunk again
     const uint32_t bv = loads.b_voff(rc);
 #pragma unroll
     for (int j = 0; j < L; ++j)
-      if ((j * P) / L == step) loads.stage(slot, rc, bv, j);
+      if ((j * EARLY) / L == step) loads.stage(slot, rc, bv, j);
   };
+  const int used = ((tile.rows + 31) / 32 - wm + WM - 1) / WM;  // row tiles of this wave that hold rows
   loads.four_scales(0, 0);
 #pragma unroll
   for (int s = 0; s < ST - 1; ++s) {
@@ -822,19 +829,21 @@ __global__ __launch_bounds__(256, 2) void experts_block_kernel(const ProductArgs
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const int t = mt * NT + nt;
+        if (mt < used) {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) part[t & 1][x] = 0.0f;
+          for (int x = 0; x < 16; ++x) part[t & 1][x] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-          part[t & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(fb[nt][s][0], fb[nt][s][1]),
-                                                                        wide(fa[mt & 1][s][0], fa[mt & 1][s][1]),
-                                                                        part[t & 1], 0, 0, 0, 127, 0, 127);
+          for (int s = 0; s < 2; ++s)
+            part[t & 1] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wide(fb[nt][s][0], fb[nt][s][1]),
+                                                                          wide(fa[mt & 1][s][0], fa[mt & 1][s][1]),
+                                                                          part[t & 1], 0, 0, 0, 127, 0, 127);
+        }
         if (mt == MT - 1) refill(slot, i + ST, nt);
         else refill(before, i - 1 + ST, NT + t);
         // both products are on their way before the additions wait for the last ones
         __asm__ volatile("" : "+v"(part[t & 1]));
         __builtin_amdgcn_sched_barrier(0);
-        add_part((t + P - 1) % P);
+        if ((t + P - 1) % P / NT < used) add_part((t + P - 1) % P);
         if (t == 0) read_rs(i, MT - 1);
         if (mt == MT - 1) {
           read_b(next, nt);
@@ -852,10 +861,10 @@ __global__ __launch_bounds__(256, 2) void experts_block_kernel(const ProductArgs
     for (int u = 0; u < ST; ++u)
       if (i0 + u < chunks) chunk(i0 + u, u);
   }
-  add_part(P - 1);
+  if (MT - 1 < used) add_part(P - 1);
   wait_vmcnt<0>();  // no LDS load may still be in flight when the ring is used again
   __syncthreads();
-  finish_tile<F, 1, WN, MT, NT, UP>(g, meta, tile, acc, loads.wscales, tile.ngroup * TB * 16, lds);
+  finish_tile<F, WM, WN, MT, NT, UP>(g, meta, tile, acc, loads.wscales, tile.ngroup * TB * 16, lds);
 }
 
 }  // namespace

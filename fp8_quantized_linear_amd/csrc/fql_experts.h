@@ -45,17 +45,23 @@ inline ExpertRows expert_rows(int fmt, int64_t K) {
 
 constexpr int kMaxExperts = 1024;
 
+struct ProductPlan {
+  bool large;                // experts_tile_kernel or experts_block_kernel (32 x 32 tiles), else
+                             // experts_product_kernel (16 x 16)
+  int wm, wn, mtw, ntw, st;  // waves, tiles a wave, ring depth
+  int rows, cols;            // of a workgroup's tile
+  int64_t max_tiles;         // upper bound of a pass's row tiles
+};
+
 // What one call (or one pass of it: tokens are taken `tokens` at a time, so that
 // offsets stay within 32 bits and the workspace within bounds) runs.
 struct ExpertsPlan {
   int fmt;
-  bool large;                // experts_tile_kernel (32 x 32 tiles), else experts_product_kernel (16 x 16)
-  int wm, wn, mtw, ntw, st;  // waves, tiles a wave, ring depth
-  int rows;                  // rows of a workgroup's tile
-  bool h_quantized;          // the first product quantizes the inner activation itself
-  int64_t tokens;            // tokens a pass
-  int64_t pairs;             // of a pass
-  int64_t max_tiles;         // upper bound of a pass's row tiles
+  bool token;  // a few tokens: every pair for itself (experts_token.h), without sorting
+  ProductPlan up, down;
+  bool h_quantized;  // the first product quantizes the inner activation itself
+  int64_t tokens;    // tokens a pass
+  int64_t pairs;     // of a pass
   // workspace, in order (every size a multiple of 256)
   int64_t counter_bytes, meta_bytes, xcode_bytes, xscale_bytes, h_bytes, hcode_bytes, hscale_bytes, d_bytes, total_bytes;
 };

@@ -182,6 +182,64 @@ def test_experts(fmt, T, k, E, H, I):
     assert torch.equal(xx, y)
 
 
+FEW = [(1, 1, 1, 32, 32, 16), (1, 64, 64, 96, 160, 33), (1, 5, 9, 640, 544, 130), (2, 3, 40, 1120, 96, 77),
+       (4, 16, 96, 128, 288, 48), (6, 2, 24, 224, 1184, 256), (3, 7, 64, 2080, 128, 20)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,k,E,H,I,Ho", FEW)
+def test_a_few_tokens(fmt, T, k, E, H, I, Ho):
+    """Every pair for itself, without sorting: rows at odd addresses, columns and depths that end inside a tile
+    and a wave's chunks, absent and repeated experts, an inner activation of every kind."""
+    if fmt == "fp8_block":
+        H, I, Ho = (-(-n // 128) * 128 for n in (H, I, Ho))
+    announce(f"experts few {fmt} T={T} k={k} E={E} H={H} I={I} Ho={Ho}")
+    rng = np.random.default_rng([T, k, E, H])
+    act = ("silu", "swiglu", "none")[k % 3]
+    N = 2 * I if act == "swiglu" else I
+    assert "token_up" in fql.experts_fused_plan(fmt, T, k, E, H, N, Ho, act)
+    layer = Layer(fmt, E, H, I, Ho=Ho, act=act, bias=k % 2 == 1)
+    x, x64 = strided(rng.standard_normal((T, H)), H + 3, 1)
+    r, r64 = strided(rng.standard_normal((T, Ho)), Ho + 5, 3)
+    w, _, w64, ids = choice(rng, T, E, k)
+    check(layer(x, w, torch.from_numpy(ids).to(DEV), residual=r), *layer.reference(x64, w64, ids, r64), "all")
+    ids[0, -1] = ids[0, 0]
+    if k > 1:
+        ids[-1, 1] = E if T % 2 else -1
+    e = torch.from_numpy(ids).to(DEV)
+    y = layer(x, w, e)
+    check(y, *layer.reference(x64, w64, ids), "absent and repeated")
+    for _ in range(2):
+        assert torch.equal(layer(x, w, e), y)
+    ids[:] = -7
+    assert torch.equal(layer(x, w, torch.from_numpy(ids).to(DEV), residual=r), r)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_few_tokens_keep_to_themselves(fmt):
+    """A row of NaN and a NaN weight reach their own token alone; an unchosen expert's NaN weights reach none."""
+    announce(f"experts few NaN {fmt}")
+    rng = np.random.default_rng(3)
+    E, H = 32, 256
+    layer = Layer(fmt, E, H, 128)
+    assert "token_up" in fql.experts_fused_plan(fmt, 4, 2, E, H, 256, H)
+    x, _ = bf16(rng.standard_normal((4, H)))
+    w, e, _, ids = choice(rng, 4, E, 2)
+    want = layer(x, w, e)
+    idle = [i for i in range(E) if i not in ids][0]
+    layer.up.packed[idle] = 0xFF
+    layer.down.packed[idle] = 0xFF
+    assert torch.equal(layer(x, w, e), want)
+    w2, x2 = w.clone(), x.clone()
+    w2[1, 0] = float("nan")
+    x2[3] = float("nan")
+    got = layer(x2, w2, e)
+    assert torch.equal(got[[0, 2]], want[[0, 2]])
+    assert torch.isnan(got[1]).all()
+    if fmt == "int8":  # the other formats' quantizers saturate a NaN
+        assert torch.isnan(got[3]).all()
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu", "swiglu"])
 def test_activations_and_biases(fmt, act):
