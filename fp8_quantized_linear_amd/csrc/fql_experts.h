@@ -20,7 +20,8 @@ struct RouteArgs {
   float scale;
   float* weights;    // [T][k]
   int32_t* experts;  // [T][k]
-  int lanes_shift;   // log2 of the lanes that score one group (set by launch_route)
+  int lanes_shift;       // log2 of the lanes that score one group (set by launch_route, as the next)
+  uint32_t group_magic;  // e * group_magic >> 20 is e divided by the experts of a group
 };
 hipError_t launch_route(bool f32, RouteArgs a, hipStream_t st);
 
