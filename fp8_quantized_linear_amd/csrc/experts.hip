@@ -735,10 +735,15 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
 }  // namespace
 
 // The tile of one product, N columns of a K-deep product, `pairs` rows over E experts:
-// 16 x 128 while an expert has few rows (a workgroup streams its weight columns), else
-// the tile of least time: rounds of the card's workgroups times (chunks * tc + f) us.
-// The number of row tiles is estimated with six tenths of a tile an expert for its last
-// rows.
+// 16 x 128 while an expert has few rows, else the tile of least time: rounds of the card's
+// workgroups times (chunks * tc + f) us, with six tenths of a tile an expert for its last
+// rows. tc is measured, full tiles on the whole card; past four rounds workgroups start
+// as others end. Whole calls with 16-row tiles against 64-row ones, us: at 4 rows an expert
+// MXFP8 (64 experts, 4096, 1024 inner) 164 and 162, at 8 164 and 158, at 16 178 and 160;
+// block FP8 (32, 4096, 2048) 148 and 148, 155 and 153, 166 and 154; MXFP4 (128, 4096, 1280)
+// 211 and 209, 219 and 211, 236 and 208; FP8 (8, 4096, 14336) 257 and 279, 261 and 257, 287
+// and 263; INT8 (32, 2048, 1408; quantizes h on its own either way) 66 and 79, 68 and 80,
+// 74 and 81, at 20 rows 80 and 78.
 static ProductPlan plan_product(int fmt, int64_t pairs, int64_t E, int64_t N, int64_t K) {
   struct Tile {
     int wm, wn, mtw, ntw, st, resident;
@@ -750,7 +755,7 @@ static ProductPlan plan_product(int fmt, int64_t pairs, int64_t E, int64_t N, in
   const bool block = fmt == SC_FP8_BLOCK;
   const int64_t KC = round_up(K, 128) / 128;
   ProductPlan p{};
-  if (pairs / E >= 24) {
+  if (pairs / E >= (fmt == SC_INT8 ? 20 : 8)) {
     double best = 0.0;
     for (const Tile& t : tiles) {
       const int64_t R = 32 * t.wm * t.mtw;
