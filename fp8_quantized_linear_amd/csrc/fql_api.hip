@@ -1448,7 +1448,8 @@ int fql_route_experts(int logits_type, const void* logits, int64_t T, int64_t E,
     if (logits_type != FQL_TYPE_BF16 && logits_type != FQL_TYPE_F32)
       return fail(FQL_ERR_UNSUPPORTED, "logits must be bf16 or float32 (got type %d)", logits_type);
     if (score != FQL_SCORE_SOFTMAX && score != FQL_SCORE_SIGMOID) return fail(FQL_ERR_INVALID, "unknown score %d", score);
-    if (T < 0 || T > (int64_t)1 << 30) return fail(FQL_ERR_INVALID, "T must be in 0 .. 2^30 (got %lld)", (long long)T);
+    // a wave a token: a grid holds less than 2^32 threads
+    if (T < 0 || T > (int64_t)1 << 24) return fail(FQL_ERR_INVALID, "T must be in 0 .. 2^24 (got %lld)", (long long)T);
     if (E < 1 || E > fql::kRouteMaxExperts)
       return fail(FQL_ERR_UNSUPPORTED, "experts must be in 1 .. %d (got %lld)", fql::kRouteMaxExperts, (long long)E);
     if (ld < E) return fail(FQL_ERR_INVALID, "row stride %lld is smaller than the %lld experts", (long long)ld, (long long)E);

@@ -77,7 +77,7 @@ __global__ __launch_bounds__(1024) void int8_row_kernel(const Int8Args a) {
   __shared__ double sums[16];
   __shared__ uint32_t tops[16];
   const int t = threadIdx.x, T = blockDim.x, waves = T / 64;
-  int64_t m = blockIdx.x;
+  int64_t m = blockIdx.x + ((int64_t)blockIdx.y << 20);
   // an operand's rows are 16-byte pieces, 16 rows in a run of 256 bytes: a tile's
   // workgroups are placed on one XCD (they go to the eight in turn), whose L2 joins
   // the pieces
@@ -207,7 +207,9 @@ bool row_aligned(const void* p, int64_t ld, int64_t bytes) {
 template <typename X, bool NORM, bool OP>
 hipError_t launch_rows(const Int8Args& a, hipStream_t st) {
   const int64_t nv = OP ? (a.K + 127) / 128 * 16 : a.K / 8;
-  const unsigned rows = (unsigned)(OP ? round_up(a.M, 128) : a.M);
+  // a dimension of a grid holds less than 2^32 threads
+  const int64_t whole = OP ? round_up(a.M, 128) : a.M;
+  const dim3 rows((unsigned)std::min<int64_t>(whole, 1 << 20), (unsigned)((whole + (1 << 20) - 1) >> 20));
   // vectors a thread: two while that fills no more than a workgroup, so that a row's
   // chain is short
   const int64_t per = nv <= 1024 ? 2 : nv <= 2048 ? 4 : 8;

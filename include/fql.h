@@ -697,7 +697,7 @@ int fql_attention_kv8(const fql_kv_cache* cache, const fql_kv_batch* batch, cons
  * (of E / groups neighbours) can be chosen: a group's score is the sum of its two
  * largest c (s without a bias), of the one where it has one. Scores are computed in
  * float64.
- *   logits   [T][ld], FQL_TYPE_BF16 or FQL_TYPE_F32; E <= 1024. T = 0 does nothing.
+ *   logits   [T][ld], FQL_TYPE_BF16 or FQL_TYPE_F32; E <= 1024, T <= 2^24. T = 0 does nothing.
  *   bias     [E] float32 or NULL.
  *   groups   divides E, at most 64.   k <= 64, k <= top_groups * (E / groups).
  *   weights  [T][k] float32, experts [T][k] int32.
@@ -722,7 +722,7 @@ typedef struct {
  * The feed forward of each token's experts, formats MXFP4, MXFP8, FP8, block FP8
  * and INT8:
  *   h = act(alpha_up * (x_q @ Wu_e^T) + bu_e)      float32, e = experts[t][j]
- *   d = bf16(alpha_down * (h_q @ Wd_e^T) + bd_e)
+ *   d = alpha_down * (h_q @ Wd_e^T) + bd_e         float32 in calls of a few tokens, else bf16
  *   y[t] = bf16(residual[t] + sum_j weights[t][j] * d), the sum in float32
  * with x quantized as fql_linear_<format> quantizes its input, and the float32 h
  * likewise. A place whose expert is outside 0 .. E - 1 adds nothing; the same expert

@@ -28,6 +28,7 @@ def test_route_refusals():
     refused(route(score=3), "score")
     refused(route(T=-1), "T")
     refused(route(T=(1 << 30) + 1), "T")
+    refused(route(T=(1 << 24) + 1), "T")
     refused(route(E=0), "experts", code=-2)
     refused(route(E=1025, ld=1025), "1024", code=-2)
     refused(route(ld=63), "stride")

@@ -62,6 +62,21 @@ def test_quantizer(M, K):
     assert np.array_equal(wc.cpu().numpy(), want) and np.array_equal(wsc.cpu().numpy(), ws)
 
 
+def test_quantizer_many_rows():
+    """More rows than one dimension of the grid takes, through the codes and the packed operand."""
+    M, K, N = (1 << 20) + 133, 32, 32
+    announce(f"int8 quant {M}x{K}")
+    rng = np.random.default_rng(5)
+    x, x64 = bf16(rng.standard_normal((M, K)))
+    codes, scales = fql.quant_int8(x)
+    want, ws = O.quant_int8(x64)
+    assert np.array_equal(codes.cpu().numpy(), want) and np.array_equal(scales.cpu().numpy(), ws)
+    W, wh = weight(rng.standard_normal((N, K)))
+    some = np.r_[0:200, (1 << 20) - 130:M]
+    check(fql.linear_int8(x, W)[torch.from_numpy(some).to(DEV)], O.dequant_int8(want[some], ws[some]), wh, None, "none", None,
+          "many rows")
+
+
 def test_quantizer_extremes():
     """Zero rows, subnormal rows, ties, infinities and NaN."""
     announce("int8 quant extremes")
