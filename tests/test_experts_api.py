@@ -148,3 +148,15 @@ def test_experts_binding_refusals_without_a_gpu():
         fql.ExpertWeight("int8", torch.zeros(2, 4096, dtype=torch.uint8), 16, 128)
     with pytest.raises(fql.FQLError, match="CUDA"):
         fql.ExpertWeight.from_codes("mxfp8", torch.zeros(2, 16, 128), None)
+
+
+def test_the_gpu_tests_reach_every_tile():
+    import test_gpu_experts as G
+    for fmt in G.FMTS:
+        plans = [fql.experts_fused_plan(fmt, T, k, E, H, 2 * I, Ho) for T, k, E, H, I, Ho in G.TILES]
+        plans += [fql.experts_fused_plan(fmt, T, k, E, H, 2 * I, H) for T, k, E, H, I in G.CASES]
+        for product in ("up", "down"):
+            of = [p.split(" down ")[product == "down"] for p in plans if " down " in p]
+            for tile in ("16x128", "64x256", "128x256", "256x256"):
+                assert any(f"tiles={tile}" in p for p in of), (fmt, product, tile)
+        assert any("token" in p for p in plans)

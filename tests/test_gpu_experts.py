@@ -182,6 +182,28 @@ def test_experts(fmt, T, k, E, H, I):
     assert torch.equal(xx, y)
 
 
+# (T, k, E, H, I, Ho) at which the products take tiles of 64, 128 and 256 rows, each of the formats
+TILES = [(1500, 4, 16, 384, 256, 256), (6000, 2, 3, 384, 384, 640), (3000, 2, 8, 384, 640, 640),
+         (800, 2, 32, 384, 256, 2176), (3000, 2, 4, 384, 384, 256)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T,k,E,H,I,Ho", TILES)
+def test_tiles(fmt, T, k, E, H, I, Ho):
+    """Many tokens, an expert's rows ending anywhere in a tile; some of the rows, and every row again."""
+    announce(f"experts tiles {fmt} T={T} k={k} E={E} H={H} I={I} {fql.experts_fused_plan(fmt, T, k, E, H, 2 * I, Ho)}")
+    rng = np.random.default_rng([T, E])
+    layer = Layer(fmt, E, H, I, Ho=Ho, bias=True)
+    x, x64 = bf16(rng.standard_normal((T, H)))
+    w, e, w64, ids = choice(rng, T, E, k, skew=0.1)
+    y = layer(x, w, e)
+    rows = np.unique(np.concatenate([[0, T - 1], rng.integers(0, T, 150)]))
+    check(y[torch.from_numpy(rows).to(DEV)], *layer.reference(x64[rows], w64[rows], ids[rows]), "tiles")
+    # a token's result does not depend on where its pairs come to lie
+    order = torch.from_numpy(rng.permutation(T)).to(DEV)
+    assert torch.equal(layer(x[order].contiguous(), w[order].contiguous(), e[order].contiguous()), y[order])
+
+
 FEW = [(1, 1, 1, 32, 32, 16), (1, 64, 64, 96, 160, 33), (1, 5, 9, 640, 544, 130), (2, 3, 40, 1120, 96, 77),
        (4, 16, 96, 128, 288, 48), (6, 2, 24, 224, 1184, 256), (3, 7, 64, 2080, 128, 20)]
 
