@@ -519,13 +519,19 @@ __global__ __launch_bounds__(64 * WM * WN) void experts_product_kernel(const Pro
         }
       }
   } else {
-    uint16_t* const d = static_cast<uint16_t*>(g.out) + (int64_t)row0 * g.ld_out;
-    constexpr bool kStaged = sizeof(stage) >= (size_t)R * StagedPitch<TB * 16>::P * 2 &&
-                             (R * TB * 16 / 8) % (64 * NW) == 0;
-    static_assert(kStaged, "the output tile goes through the ring");
-    __syncthreads();  // every wave's loads have landed: the ring is free
-    write_tile16_staged<MTW, NTW, WM, WN>(acc, rows, g.N, 0, n0, wm, wn, alpha, bias, d, g.ld_out,
-                                          reinterpret_cast<uint16_t*>(&stage[0]));
+    // few rows: float32
+    const EpiOut o = {rows, g.N, alpha, bias, ScEpilogue{kActNone, nullptr, 0}, nullptr, 0};
+    float* const d = static_cast<float*>(g.out) + (int64_t)row0 * g.ld_out;
+#pragma unroll
+    for (int mt = 0; mt < MTW; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NTW; ++nt) {
+        const int m = (wm * MTW + mt) * 16 + 4 * kg, n = n0 + (wn * NTW + nt) * 16 + fr;
+        const float4v v = o.plain(acc[mt][nt], n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (m + i < rows && n < g.N) d[(int64_t)(m + i) * g.ld_out + n] = v[i];
+      }
   }
 }
 
@@ -533,11 +539,12 @@ __global__ __launch_bounds__(64 * WM * WN) void experts_product_kernel(const Pro
 // combine
 // ---------------------------------------------------------------------------
 
-// y_t = bf16(residual_t + sum_j w_tj d_row(t, j)), eight columns a thread. The
-// products' rows are bf16 (one rounding of 2^-9 each, as a linear layer's output
-// has; float32 rows would double this kernel's and the down product's traffic);
-// their sum is float32.
-__global__ __launch_bounds__(256) void experts_combine_kernel(const uint16_t* __restrict__ d, int64_t ldd, int64_t T,
+// y_t = bf16(residual_t + sum_j w_tj d_row(t, j)), eight columns a thread, the sum in
+// float32 in the order of the places. HALF: d's rows are fp16 with a factor for every 32
+// columns (finish_tile), else float32; ldd columns either way, a multiple of 32.
+template <bool HALF>
+__global__ __launch_bounds__(256) void experts_combine_kernel(const uint8_t* __restrict__ d,
+                                                              const float* __restrict__ scales, int64_t ldd, int64_t T,
                                                               int64_t N, const float* __restrict__ weights,
                                                               const int* __restrict__ pair_row, int k,
                                                               const uint16_t* residual, int64_t ldr, uint16_t* y,
@@ -568,12 +575,23 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(const uint16_t* __
     const int row = pair_row[t * k + p];
     if (row < 0) continue;
     const float w = weights[t * k + p];
-    const uint4v u = *reinterpret_cast<const uint4v*>(d + (int64_t)row * ldd + n);  // rows padded to 8 columns
+    float v[8];
+    if constexpr (HALF) {
+      const float f = scales[(int64_t)row * (ldd / 32) + n / 32];
+      const uint4v u = *reinterpret_cast<const uint4v*>(d + ((int64_t)row * ldd + n) * 2);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      sum[2 * j] = __builtin_fmaf(w, __uint_as_float(u[j] << 16), sum[2 * j]);
-      sum[2 * j + 1] = __builtin_fmaf(w, __uint_as_float(u[j] & 0xFFFF0000u), sum[2 * j + 1]);
+      for (int j = 0; j < 4; ++j) {
+        const half2v h = __builtin_bit_cast(half2v, (uint32_t)u[j]);
+        v[2 * j] = (float)h.x * f;
+        v[2 * j + 1] = (float)h.y * f;
+      }
+    } else {
+      const float4v* const f = reinterpret_cast<const float4v*>(d + ((int64_t)row * ldd + n) * 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = f[j / 4][j % 4];  // columns past N: whatever is there, not stored
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] = __builtin_fmaf(w, v[j], sum[j]);
   }
   uint16_t* const out = y + t * ldy + n;
   if (whole) {
@@ -686,6 +704,7 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
   uint8_t* const hc = take(p.hcode_bytes);
   uint8_t* const hs = take(p.hscale_bytes);
   uint8_t* const d = take(p.d_bytes);
+  float* const ds = reinterpret_cast<float*>(d + p.pairs * 2 * round_up(a.down.N, 32));  // of fp16 rows
   Meta m[2];
   meta_at(meta, p.pairs, p.up.max_tiles, p.down.max_tiles, m);
   for (int64_t t0 = 0; t0 < a.T; t0 += p.tokens) {
@@ -714,7 +733,8 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
     }
     g = product_args(F, p.down, a.down, hc, hs);
     g.out = d;
-    g.ld_out = round_up(a.down.N, 8);
+    g.out_scales = ds;
+    g.ld_out = round_up(a.down.N, 32);
     g.k = a.k;
     e = launch_product<F, false>(p.down, g, m[1], st);
     if (e != hipSuccess) return e;
@@ -723,9 +743,9 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
     auto whole = [](const void* ptr, int64_t ld) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0; };
     const bool vec = whole(a.y, a.ldy) && (r == nullptr || whole(a.residual, a.ldr));
     const int64_t items = T * ((a.down.N + 7) / 8);
-    experts_combine_kernel<<<(unsigned)((items + 255) / 256), 256, 0, st>>>(
-        reinterpret_cast<const uint16_t*>(d), round_up(a.down.N, 8), T, a.down.N, a.weights + t0 * a.k, m[0].pair_row, a.k,
-        r, a.ldr, y, a.ldy, vec);
+    const auto combine = p.down.large ? experts_combine_kernel<true> : experts_combine_kernel<false>;
+    combine<<<(unsigned)((items + 255) / 256), 256, 0, st>>>(d, ds, round_up(a.down.N, 32), T, a.down.N, a.weights + t0 * a.k,
+                                                             m[0].pair_row, a.k, r, a.ldr, y, a.ldy, vec);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -785,7 +805,7 @@ ExpertsPlan plan_experts(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, in
   p.fmt = fmt;
   const ExpertRows xr = expert_rows(fmt, H), hr = expert_rows(fmt, I);
   // a pass's activations lie within 32-bit offsets and 1 GiB of workspace
-  const int64_t per_token = xr.ld_codes + xr.ld_scales + k * (hr.ld_codes + hr.ld_scales + 4 * round_up(I, 4) + 2 * round_up(Ho, 8));
+  const int64_t per_token = xr.ld_codes + xr.ld_scales + k * (hr.ld_codes + hr.ld_scales + 4 * round_up(I, 4) + 4 * round_up(Ho, 32));
   p.tokens = std::max<int64_t>(1, std::min<int64_t>(T, ((int64_t)1 << 30) / per_token));
   p.pairs = p.tokens * k;
   p.up = plan_product(fmt, p.pairs, E, N, H);
@@ -804,7 +824,7 @@ ExpertsPlan plan_experts(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, in
   p.h_bytes = p.h_quantized ? 0 : round_up(p.pairs * 4 * round_up(I, 4), 256);
   p.hcode_bytes = round_up(p.pairs * hr.ld_codes, 256);
   p.hscale_bytes = round_up(p.pairs * hr.ld_scales, 256);
-  p.d_bytes = round_up(p.pairs * 2 * round_up(Ho, 8), 256);
+  p.d_bytes = round_up(p.pairs * round_up(Ho, 32) * (p.down.large ? 2 : 4) + (p.down.large ? p.pairs * round_up(Ho, 32) / 8 : 0), 256);
   if (p.token) p.meta_bytes = p.xcode_bytes = p.xscale_bytes = p.hcode_bytes = p.hscale_bytes = p.d_bytes = 0;
   p.total_bytes = p.counter_bytes + p.meta_bytes + p.xcode_bytes + p.xscale_bytes + p.h_bytes + p.hcode_bytes +
                   p.hscale_bytes + p.d_bytes;

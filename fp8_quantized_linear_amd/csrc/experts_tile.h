@@ -72,7 +72,8 @@ struct ProductArgs {
   const float* alpha;    // [E] or null
   const uint16_t* bias;  // [E][N] or null
   int act;               // up
-  void* out;             // up: float32 [row][ld_out], or codes (hq); down: bf16 [row][ld_out]
+  void* out;             // up: float32 [row][ld_out], or codes (hq); down: float32 or fp16 [row][ld_out]
+  float* out_scales;     // down, fp16: [row][ld_out / 32]
   int64_t ld_out;
   int k;
   // up: the inner activation quantized in the epilogue (all but INT8)
@@ -469,49 +470,89 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
       __syncthreads();
     }
   } else {
-    // bf16 rows straight from the registers: with the halves of a wave exchanged a lane has
-    // eight neighbouring columns. Rows are padded to eight columns, which may hold anything.
+    // Rows for the weighted sum, 16 bits a column: fp16, and for 32 neighbouring columns of
+    // a row a power of two that the values are divided by, so that the largest of them
+    // comes to 2^14 .. 2^15. Each is off by at most 2^-11 of itself (2^-39 of the largest
+    // where it is below 2^-28 of that): bf16 rows, of the same size, would be off by 2^-8,
+    // as much as y's own rounding again, and float32 rows would be another 268 MB each way
+    // at 4096 tokens of 8 experts and 4096 columns. Straight from the registers: with
+    // the halves of a wave exchanged a lane has eight neighbouring columns. Columns past N
+    // are zeros.
     uint16_t* const d = static_cast<uint16_t*>(g.out) + (int64_t)tile.row0 * g.ld_out;
+    float* const scales = g.out_scales + (int64_t)tile.row0 * (g.ld_out / 32);
+    const bool inside = n0 + C <= g.N;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int nb = n0 + (wn * NT + nt) * 32;
+      float b[16];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int n = n0 + (wn * NT + nt) * 32 + 16 * j + 4 * kb;
-        float b[8];
-        float4v col[2] = {{1.f, 1.f, 1.f, 1.f}, {1.f, 1.f, 1.f, 1.f}};
+      for (int e = 0; e < 16; ++e) b[e] = 0.0f;
+      if (bias != nullptr) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int ne = n + (e & 3) + 2 * (e & 4);
-          b[e] = bias != nullptr && ne < g.N ? bf16_bits_to_f32(bias[ne]) : 0.0f;
-        }
-        if constexpr (T::INT) {
-          if (n < g.ntiles_w * 16) {
-            col[0] = *reinterpret_cast<const float4v*>(wscales + (int64_t)n * 4);
-            col[1] = *reinterpret_cast<const float4v*>(wscales + (int64_t)(n + 8) * 4);
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t w[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t h2[2];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const int e = 2 * x + y;  // register 8 j + e
-              float v = acc[mt][nt][8 * j + e];
-              if constexpr (T::INT) v = (float)(int)__float_as_uint(v) * (rsc[mt] * col[e / 4][e % 4]);
-              h2[y] = f32_to_bf16_bits(alpha * v + b[e]);
-            }
-            w[x] = h2[0] | (h2[1] << 16);
-          }
-          swap_halves(w[0], w[2]);
-          swap_halves(w[1], w[3]);
-          const int m = (mt * WM + wm) * 32 + (lane & 31), at = n0 + (wn * NT + nt) * 32 + 16 * j + 8 * kb;
-          if (m < tile.rows && at < (int)g.ld_out)
-            *reinterpret_cast<uint4v*>(d + (int64_t)m * g.ld_out + at) = uint4v{w[0], w[1], w[2], w[3]};
+        for (int e = 0; e < 16; ++e) {
+          const int n = nb + 8 * (e / 4) + 4 * kb + e % 4;
+          b[e] = n < g.N ? bf16_bits_to_f32(bias[n]) : 0.0f;
         }
       }
+      float4v col[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = nb + 8 * i + 4 * kb;
+        col[i] = float4v{1.f, 1.f, 1.f, 1.f};
+        if constexpr (T::INT) {
+          if (n < g.ntiles_w * 16) col[i] = *reinterpret_cast<const float4v*>(wscales + (int64_t)n * 4);
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float v[16];
+        float top = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float s = acc[mt][nt][e];
+          if constexpr (T::INT) s = (float)(int)__float_as_uint(s) * (rsc[mt] * col[e / 4][e % 4]);
+          v[e] = alpha * s + b[e];
+        }
+        if (!inside) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = nb + 8 * (e / 4) + 4 * kb + e % 4 < g.N ? v[e] : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) top = __builtin_fmaxf(top, __builtin_fabsf(v[e]));  // NaN is passed over
+        if (__any(top == __builtin_inff())) {  // the largest finite one
+          top = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float x = __builtin_fabsf(v[e]);
+            top = x < __builtin_inff() && x > top ? x : top;
+          }
+        }
+        uint32_t t0 = __float_as_uint(top), t1 = t0;
+        swap_halves(t0, t1);
+        int ex = (int)((t0 > t1 ? t0 : t1) >> 23) - 127;
+        ex = ex < -112 ? -112 : ex;
+        const float f = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+        uint32_t w[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const half2v h = __builtin_convertvector((float2v{v[2 * x] * f, v[2 * x + 1] * f}), half2v);
+          w[x] = __builtin_bit_cast(uint32_t, h);
+        }
+        const int m = (mt * WM + wm) * 32 + (lane & 31);
+        const bool live = m < tile.rows && nb < (int)g.ld_out;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          swap_halves(w[4 * j], w[4 * j + 2]);
+          swap_halves(w[4 * j + 1], w[4 * j + 3]);
+        }
+        if (live) {  // a row's two lanes write the one factor
+          uint16_t* const at = d + (int64_t)m * g.ld_out + nb + 8 * kb;
+          *reinterpret_cast<uint4v*>(at) = uint4v{w[0], w[1], w[2], w[3]};
+          *reinterpret_cast<uint4v*>(at + 16) = uint4v{w[4], w[5], w[6], w[7]};
+          scales[(int64_t)m * (g.ld_out / 32) + nb / 32] = __uint_as_float((uint32_t)(127 + ex - 14) << 23);
+        }
+      }
+    }
   }
 }
 

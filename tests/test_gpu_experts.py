@@ -89,7 +89,9 @@ def code_values(fmt, v, tol, scale):
 def reference(fmt, xh, wu, wd, weights, ids, act, bu, bd, res):
     """(y, tolerance) of tokens xh [T, H]. Counted: the products' sums (2^-12 of the sum of magnitudes for the
     FP8 and FP4 matrix instructions, 2^-20 for integers), the activation as in the linear layers' tests, the
-    codes of h (code_values), a bf16 rounding of each d and of y, float32 sums."""
+    codes of h (code_values), an fp16 rounding of each d, float32 sums, a bf16 rounding of y. d is divided by a
+    power of two before it, so that the largest of 32 columns lies in 2^14 .. 2^15: an fp16 rounding is off by
+    at most 2^-11 of the value, or by 2^-25 below 2^-14, which is 2^-39 of the largest."""
     rel = 2.0 ** -20 if fmt == "int8" else 2.0 ** -12
     E = wu.shape[0]
     y = np.zeros((xh.shape[0], wd.shape[1])) if res is None else res.copy()
@@ -111,7 +113,9 @@ def reference(fmt, xh, wu, wd, weights, ids, act, bu, bd, res):
         hq, off = code_values(fmt, h, eh, SH)
         d = hq @ wd[e].T + (0 if bd is None else bd[e])
         ed = off @ np.abs(wd[e]).T + rel * (np.abs(hq) + off) @ np.abs(wd[e]).T + 2.0 ** -22 * np.abs(d)
-        ed = ed * (1 + HALF_BF16) + HALF_BF16 * np.abs(d)
+        top = np.abs(d) + ed
+        top = np.pad(top, ((0, 0), (0, -top.shape[1] % 32))).reshape(top.shape[0], -1, 32).max(2)
+        ed = ed * (1 + 2.0 ** -11) + 2.0 ** -11 * np.abs(d) + 2.0 ** -39 * np.repeat(top, 32, 1)[:, :d.shape[1]]
         w = weights[t, j][:, None]
         np.add.at(y, t, w * d)
         np.add.at(tol, t, np.abs(w) * ed)
@@ -202,6 +206,34 @@ def test_tiles(fmt, T, k, E, H, I, Ho):
     # a token's result does not depend on where its pairs come to lie
     order = torch.from_numpy(rng.permutation(T)).to(DEV)
     assert torch.equal(layer(x[order].contiguous(), w[order].contiguous(), e[order].contiguous()), y[order])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("T", [4, 70])
+def test_rows_of_any_size_on_their_way(fmt, T):
+    """Outputs of very different sizes beside one another, and columns whose weights are not finite: the rows of
+    the second product keep 2^-11 of each or 2^-39 of the largest of 32, and infinities and NaN where they are."""
+    announce(f"experts rows {fmt} T={T}")
+    rng = np.random.default_rng(T)
+    E, H, I, Ho = 3, 128, 128, 176 if fmt != "fp8_block" else 256
+    layer = Layer(fmt, E, H, I, Ho=Ho)
+    x, x64 = bf16(rng.standard_normal((T, H)))
+    w, e, w64, ids = choice(rng, T, E, 2)
+    big = np.zeros(Ho)
+    big[5], big[40], big[41], big[75] = 3e38, np.inf, np.nan, -np.inf
+    big[64:80] += 1e-39
+    big[96:112] = 2.0 ** np.arange(-100, -52, 3)
+    layer.bd, layer.bd64 = bf16(np.tile(big, (E, 1)))
+    y = f64(layer(x, w, e))
+    with np.errstate(invalid="ignore"):
+        ref, _ = layer.reference(x64, w64, ids)
+    odd = [40, 41, 75]
+    assert np.isposinf(y[:, 40]).all() and np.isnan(y[:, 41]).all() and np.isneginf(y[:, 75]).all()
+    layer.bd64 = np.where(np.isfinite(layer.bd64), layer.bd64, 0.0)
+    ref, tol = layer.reference(x64, w64, ids)
+    keep = [n for n in range(Ho) if n not in odd]
+    d = np.abs(y - ref)[:, keep]
+    assert (d <= tol[:, keep]).all(), np.argwhere(d > tol[:, keep])[:4]
 
 
 FEW = [(1, 1, 1, 32, 32, 16), (1, 64, 64, 96, 160, 33), (1, 5, 9, 640, 544, 130), (2, 3, 40, 1120, 96, 77),
