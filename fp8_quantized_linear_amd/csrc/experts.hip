@@ -3,9 +3,9 @@
 // layers and INT8.
 //
 //   prepare   pairs (token, place) counted and placed by expert; x quantized, by token
-//   product   up: rows gathered by the sorted order, activation, float32
-//   quantize  the inner activation, from float32
-//   product   down: bf16 rows in sorted order
+//   product   up: rows gathered by the sorted order, activation, quantized or float32
+//   quantize  the inner activation, from float32 (where the first product did not)
+//   product   down: rows in sorted order, fp16 with a factor for 32 columns (few rows: float32)
 //   combine   y_t = residual_t + the k rows of token t times their weights, float32
 //
 // A product's workgroup computes one tile of one expert: rows of its range of the
@@ -758,7 +758,11 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
 // 16 x 128 while an expert has few rows, else the tile of least time: rounds of the card's
 // workgroups times (chunks * tc + f) us, with six tenths of a tile an expert for its last
 // rows. tc is measured, full tiles on the whole card; past four rounds workgroups start
-// as others end. Whole calls with 16-row tiles against 64-row ones, us: at 4 rows an expert
+// as others end. f is fitted to 46 products (each tile forced, 24 to 4096 tokens, 4 to 128
+// experts): the tile it picks costs a call 0.9% over the best of the three on average.
+// (4 experts of FP8, 495 tokens, 5376, 288 inner: 64-row tiles for both 46.6 us, 128-row
+// tiles 53.2; 60 of MXFP4, 152 tokens, 672, 448 inner: 28.4 and 30.0, 256 rows 33.9.)
+// Whole calls with 16-row tiles against 64-row ones, us: at 4 rows an expert
 // MXFP8 (64 experts, 4096, 1024 inner) 164 and 162, at 8 164 and 158, at 16 178 and 160;
 // block FP8 (32, 4096, 2048) 148 and 148, 155 and 153, 166 and 154; MXFP4 (128, 4096, 1280)
 // 211 and 209, 219 and 211, 236 and 208; FP8 (8, 4096, 14336) 257 and 279, 261 and 257, 287
@@ -770,8 +774,8 @@ static ProductPlan plan_product(int fmt, int64_t pairs, int64_t E, int64_t N, in
     double tc[3], f;  // MXFP4, block FP8, the others
   };
   static constexpr Tile tiles[] = {{1, 4, 2, 2, 3, 2, {1.00, 1.00, 1.40}, 5.0},
-                                   {1, 4, 4, 2, 4, 1, {0.85, 1.45, 1.35}, 5.0},
-                                   {2, 2, 4, 4, 4, 1, {1.04, 1.92, 1.60}, 8.0}};
+                                   {1, 4, 4, 2, 4, 1, {0.85, 1.45, 1.35}, 7.5},
+                                   {2, 2, 4, 4, 4, 1, {1.04, 1.92, 1.60}, 11.0}};
   const bool block = fmt == SC_FP8_BLOCK;
   const int64_t KC = round_up(K, 128) / 128;
   ProductPlan p{};

@@ -722,7 +722,8 @@ typedef struct {
  * The feed forward of each token's experts, formats MXFP4, MXFP8, FP8, block FP8
  * and INT8:
  *   h = act(alpha_up * (x_q @ Wu_e^T) + bu_e)      float32, e = experts[t][j]
- *   d = alpha_down * (h_q @ Wd_e^T) + bd_e         float32 in calls of a few tokens, else bf16
+ *   d = alpha_down * (h_q @ Wd_e^T) + bd_e         float32, or with many rows an expert fp16
+ *                                                  times a power of two for 32 columns
  *   y[t] = bf16(residual[t] + sum_j weights[t][j] * d), the sum in float32
  * with x quantized as fql_linear_<format> quantizes its input, and the float32 h
  * likewise. A place whose expert is outside 0 .. E - 1 adds nothing; the same expert

@@ -188,7 +188,8 @@ def test_experts(fmt, T, k, E, H, I):
 
 # (T, k, E, H, I, Ho) at which the products take tiles of 64, 128 and 256 rows, each of the formats
 TILES = [(1500, 4, 16, 384, 256, 256), (6000, 2, 3, 384, 384, 640), (3000, 2, 8, 384, 640, 640),
-         (800, 2, 32, 384, 256, 2176), (3000, 2, 4, 384, 384, 256)]
+         (800, 2, 32, 384, 256, 2176), (3000, 2, 4, 384, 384, 256), (300, 2, 3, 6784, 128, 256),
+         (150, 2, 3, 256, 8192, 384)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
