@@ -715,22 +715,38 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void experts_tile_kernel
   // expert's last rows cost what they are (in steps of 32 WM)
   const int row_tiles = (tile.rows + 31) / 32;
   const int used = (row_tiles - wm + WM - 1) / WM;
-  auto iteration = [&](int i, int slot, int q, int h, bool first_of_four) {
-    wait_vmcnt<L * (ST - 2)>();
+  // A row's 64 bytes of a stage are half a cache line. Where the ring is even, the activation
+  // loads of stages 2 c and 2 c + 1 go out together, both halves of a tile's lines one after
+  // the other, when both slots are free: a stage apart the second half came from L2 again.
+  constexpr bool PAIRS = ST % 2 == 0;
+  constexpr int LA = TA / Cfg::NW, LB = L - LA;
+  auto iteration = [&](int i, int slot, int q, int h, bool odd, bool first_of_four) {
+    // loads that may be on their way when stage i + 1 has to be there: those issued after its own
+    if constexpr (!PAIRS) wait_vmcnt<L * (ST - 2)>();
+    else if (odd) wait_vmcnt<LB + (ST - 2) / 2 * LB + (ST - 4) / 2 * (2 * LA + LB)>();
+    else wait_vmcnt<(ST - 2) * L>();
     stage_barrier();
     const int next_slot = (slot + 1) % ST;
     if (first_of_four) loads.four_scales((i / PER + 4 < (int)g.KC ? i / PER + 4 : 0), ((i / FOUR) + 1) & 1);
-    int rc = i + ST;
+    int rc = i + ST, rb = rc - 1;
     rc = rc < stages ? rc : stages - 1;
+    rb = rb < stages ? rb : stages - 1;
     const uint32_t bv = loads.b_voff(rc);
+    auto load = [&](int j) {  // j-th load of the iteration
+      if (!PAIRS) loads.stage(slot, rc, bv, j);
+      else if (!odd) loads.stage(slot, rc, bv, LA + j);
+      else if (j < 2 * LA) loads.stage(j % 2 ? slot : (slot + ST - 1) % ST, j % 2 ? rc : rb, bv, j / 2);
+      else loads.stage(slot, rc, bv, j - LA);
+    };
+    const int n = !PAIRS ? L : odd ? 2 * LA + LB : LB;
     const int ni = i + 1;
     read_scales(ni / PER, PER == 2 ? (h ^ 1) : 0, q ^ 1);
     read_scales2(ni / PER, q ^ 1);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-      for (int j = 0; j < L; ++j)
-        if ((j * MT) / L == mt) loads.stage(slot, rc, bv, j);
+      for (int j = 0; j < 2 * LA + LB; ++j)
+        if (j < n && (j * MT) / n == mt) load(j);
       if (mt < used) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) mfma(q, mt, nt, h);
@@ -746,7 +762,7 @@ __global__ __launch_bounds__(256, MT * NT >= 8 ? 1 : 2) void experts_tile_kernel
   for (int i0 = 0; i0 < stages; i0 += U) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i0 + u < stages) iteration(i0 + u, u % ST, u % 2, PER == 2 ? u % 2 : 0, (i0 + u) % FOUR == 0);
+      if (i0 + u < stages) iteration(i0 + u, u % ST, u % 2, PER == 2 ? u % 2 : 0, u % 2 != 0, (i0 + u) % FOUR == 0);
   }
   wait_vmcnt<0>();  // no LDS load may still be in flight when the ring is used again
   __syncthreads();
