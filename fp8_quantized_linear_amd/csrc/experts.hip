@@ -758,11 +758,10 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
 // 16 x 128 while an expert has few rows, else the tile of least time: rounds of the card's
 // workgroups times (chunks * tc + f) us, with six tenths of a tile an expert for its last
 // rows. tc is measured, full tiles on the whole card; past four rounds workgroups start
-// as others end. f is fitted to 46 products (each tile forced, 24 to 4096 tokens, 4 to 128
+// as others end. f is fitted to 50 products (each tile forced, 24 to 4096 tokens, 4 to 128
 // experts): the tile it picks costs a call 0.9% over the best of the three on average.
-// (4 experts of FP8, 495 tokens, 5376, 288 inner: 64-row tiles for both 46.6 us, 128-row
-// tiles 53.2; 60 of MXFP4, 152 tokens, 672, 448 inner: 28.4 and 30.0, 256 rows 33.9.)
-// Whole calls with 16-row tiles against 64-row ones, us: at 4 rows an expert
+// (4 experts of FP8, 495 tokens, 5376, 288 inner: 64-row tiles 43.6 us, 128-row 53.2; 60 of
+// MXFP4, 152 tokens, 672, 448 inner, down: 28.4 and 30.0, 256 rows 33.9.) Whole calls with 16-row tiles against 64-row ones, us: at 4 rows an expert
 // MXFP8 (64 experts, 4096, 1024 inner) 164 and 162, at 8 164 and 158, at 16 178 and 160;
 // block FP8 (32, 4096, 2048) 148 and 148, 155 and 153, 166 and 154; MXFP4 (128, 4096, 1280)
 // 211 and 209, 219 and 211, 236 and 208; FP8 (8, 4096, 14336) 257 and 279, 261 and 257, 287
