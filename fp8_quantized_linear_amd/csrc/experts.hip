@@ -541,8 +541,9 @@ __global__ __launch_bounds__(64 * WM * WN) void experts_product_kernel(const Pro
 
 // y_t = bf16(residual_t + sum_j w_tj d_row(t, j)), eight columns a thread, the sum in
 // float32 in the order of the places. HALF: d's rows are fp16 with a factor for every 32
-// columns (finish_tile), else float32; ldd columns either way, a multiple of 32.
-template <bool HALF>
+// columns (finish_tile), else float32; ldd columns either way, a multiple of 32. The rows
+// of U places are loaded together.
+template <bool HALF, int U>
 __global__ __launch_bounds__(256) void experts_combine_kernel(const uint8_t* __restrict__ d,
                                                               const float* __restrict__ scales, int64_t ldd, int64_t T,
                                                               int64_t N, const float* __restrict__ weights,
@@ -571,27 +572,43 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(const uint8_t* __r
       for (int j = 0; j < 8; ++j) sum[j] = n + j < N ? bf16_bits_to_f32(r[j]) : 0.0f;
     }
   }
-  for (int p = 0; p < k; ++p) {
-    const int row = pair_row[t * k + p];
-    if (row < 0) continue;
-    const float w = weights[t * k + p];
-    float v[8];
-    if constexpr (HALF) {
-      const float f = scales[(int64_t)row * (ldd / 32) + n / 32];
-      const uint4v u = *reinterpret_cast<const uint4v*>(d + ((int64_t)row * ldd + n) * 2);
+  for (int p0 = 0; p0 < k; p0 += U) {
+    int row[U];
+    float w[U], f[U];
+    uint4v q[U][HALF ? 1 : 2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const half2v h = __builtin_bit_cast(half2v, (uint32_t)u[j]);
-        v[2 * j] = (float)h.x * f;
-        v[2 * j + 1] = (float)h.y * f;
-      }
-    } else {
-      const float4v* const f = reinterpret_cast<const float4v*>(d + ((int64_t)row * ldd + n) * 4);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = f[j / 4][j % 4];  // columns past N: whatever is there, not stored
+    for (int j = 0; j < U; ++j) {  // past the last place: it again, dropped below
+      const int64_t at = t * k + (p0 + j < k ? p0 + j : k - 1);
+      row[j] = pair_row[at];
+      w[j] = weights[at];
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum[j] = __builtin_fmaf(w, v[j], sum[j]);
+    for (int j = 0; j < U; ++j) {
+      const int64_t r = row[j] < 0 ? 0 : row[j];  // (row 0 for a place without an expert: dropped)
+      f[j] = 1.0f;
+      if constexpr (HALF) f[j] = scales[r * (ldd / 32) + n / 32];
+#pragma unroll
+      for (int i = 0; i < (HALF ? 1 : 2); ++i)  // columns past N: whatever is there, not stored
+        q[j][i] = *reinterpret_cast<const uint4v*>(d + (r * ldd + n) * (HALF ? 2 : 4) + 16 * i);
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (p0 + j >= k || row[j] < 0) continue;
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (HALF) {
+          const half2v h = __builtin_bit_cast(half2v, (uint32_t)q[j][0][i]);
+          v[2 * i] = (float)h.x * f[j];
+          v[2 * i + 1] = (float)h.y * f[j];
+        } else {
+          v[i] = __uint_as_float(q[j][0][i]);
+          v[4 + i] = __uint_as_float(q[j][1][i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] = __builtin_fmaf(w[j], v[i], sum[i]);
+    }
   }
   uint16_t* const out = y + t * ldy + n;
   if (whole) {
@@ -743,7 +760,8 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
     auto whole = [](const void* ptr, int64_t ld) { return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && ld % 8 == 0; };
     const bool vec = whole(a.y, a.ldy) && (r == nullptr || whole(a.residual, a.ldr));
     const int64_t items = T * ((a.down.N + 7) / 8);
-    const auto combine = p.down.large ? experts_combine_kernel<true> : experts_combine_kernel<false>;
+    const auto combine = p.down.large ? (a.k > 2 ? experts_combine_kernel<true, 4> : experts_combine_kernel<true, 2>)
+                                      : (a.k > 2 ? experts_combine_kernel<false, 4> : experts_combine_kernel<false, 2>);
     combine<<<(unsigned)((items + 255) / 256), 256, 0, st>>>(d, ds, round_up(a.down.N, 32), T, a.down.N, a.weights + t0 * a.k,
                                                              m[0].pair_row, a.k, r, a.ldr, y, a.ldy, vec);
     e = hipGetLastError();
