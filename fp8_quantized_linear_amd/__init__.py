@@ -423,12 +423,21 @@ def packed_nvfp4_bytes(N, K):
     return n.value
 
 
+def _check_pack(codes, *scales):
+    """What every packer asks of its tensors: the kernel takes their addresses as they come."""
+    _require_cuda(codes, "codes")
+    for t in scales:
+        _require_cuda(t, "scales")
+        if t.device != codes.device:
+            raise FQLError("scales must be on the codes' device")
+    if not all(t.is_contiguous() for t in (codes, *scales)):
+        raise FQLError("codes and scales must be contiguous")
+
+
 def pack_weight_nvfp4(codes, scales, out=None):
     """Re-lay canonical NVFP4 weight (codes [N, K/2], scales [N, K/16]) for the GEMM."""
-    _require_cuda(codes, "codes")
+    _check_pack(codes, scales)
     N, K = codes.shape[0], codes.shape[1] * 2
-    if not (codes.is_contiguous() and scales.is_contiguous()):
-        raise FQLError("codes and scales must be contiguous")
     if tuple(scales.shape) != (N, K // 16):
         raise FQLError("scales must be [N, K/16]")
     nbytes = packed_nvfp4_bytes(N, K)
@@ -869,11 +878,9 @@ def packed_mxfp4_bytes(N, K):
 
 
 def _pack_sc(fmt, codes, scales, out):
-    _require_cuda(codes, "codes")
+    _check_pack(codes, *(() if fmt == "fp8" else (scales,)))  # (per-tensor FP8's one scale is not packed)
     N = codes.shape[0]
     K = codes.shape[1] * (2 if fmt == "mxfp4" else 1)
-    if not codes.is_contiguous() or (scales is not None and not scales.is_contiguous()):
-        raise FQLError("codes and scales must be contiguous")
     if fmt in ("mxfp4", "mxfp8") and tuple(scales.shape) != (N, K // 32):
         raise FQLError("scales must be [N, K/32]")
     if fmt == "fp8_block" and (tuple(scales.shape) != (N // 128, K // 128) or scales.dtype != torch.float32):
