@@ -434,15 +434,22 @@ def _check_pack(codes, *scales):
         raise FQLError("codes and scales must be contiguous")
 
 
+def _packed_storage(nbytes, codes, out):
+    """The bytes that a packer writes: `out`, or new ones."""
+    if out is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+    if not isinstance(out, torch.Tensor) or out.device != codes.device or not out.is_contiguous():
+        raise FQLError("out must be a contiguous tensor on the codes' device")
+    return out
+
+
 def pack_weight_nvfp4(codes, scales, out=None):
     """Re-lay canonical NVFP4 weight (codes [N, K/2], scales [N, K/16]) for the GEMM."""
     _check_pack(codes, scales)
     N, K = codes.shape[0], codes.shape[1] * 2
     if tuple(scales.shape) != (N, K // 16):
         raise FQLError("scales must be [N, K/16]")
-    nbytes = packed_nvfp4_bytes(N, K)
-    if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+    out = _packed_storage(packed_nvfp4_bytes(N, K), codes, out)
     _check(lib().fql_pack_weight_nvfp4(_ptr(codes), _ptr(scales), N, K, _ptr(out), out.numel(),
                                        _stream(codes.device)))
     return out
@@ -887,9 +894,7 @@ def _pack_sc(fmt, codes, scales, out):
         raise FQLError("scales must be float32 [N/128, K/128]")
     if fmt == "int8" and (codes.dtype != torch.int8 or tuple(scales.shape) != (N,) or scales.dtype != torch.float32):
         raise FQLError("codes must be int8 [N, K] and scales float32 [N]")
-    nbytes = _size_query(f"fql_packed_{fmt}_bytes", N, K)
-    if out is None:
-        out = torch.empty(nbytes, dtype=torch.uint8, device=codes.device)
+    out = _packed_storage(_size_query(f"fql_packed_{fmt}_bytes", N, K), codes, out)
     if fmt == "fp8":
         _check(_fn("fql_pack_weight_fp8")(_ptr(codes), N, K, _ptr(out), out.numel(),
                                           _stream(codes.device)))

@@ -116,3 +116,19 @@ def test_scales_of_another_device_are_refused(fmt, where, calls):
         with pytest.raises(fql.FQLError, match="scales must be"):
             call()
     assert calls == []
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_storage_of_another_device_or_with_gaps_is_refused(fmt, calls):
+    """The packing kernel would write through an address that is not its device's, or over the gaps of a view."""
+    codes, scales = operands(fmt)
+    n = storage(fmt).numel()
+    for out in (on(torch.Tensor, storage(fmt)), storage(fmt, Gpu1), on(Gpu0, torch.zeros(2 * n, dtype=torch.uint8))[::2]):
+        with pytest.raises(fql.FQLError, match="out must be"):
+            pack(fmt, codes, scales, out)
+    with pytest.raises(fql.FQLError, match="out must be"):
+        weight(fmt, Gpu1).repack_(codes, scales)
+    if fmt != "nvfp4":
+        with pytest.raises(fql.FQLError, match="out must be"):
+            experts(fmt, Gpu1).repack_(0, codes, 0.25 if fmt == "fp8" else scales)
+    assert calls == []
