@@ -423,9 +423,22 @@ def packed_nvfp4_bytes(N, K):
     return n.value
 
 
-def _check_pack(codes, *scales):
-    """What every packer asks of its tensors: the kernel takes their addresses as they come."""
+_BYTES = (torch.uint8, torch.int8)  # codes held as plain bytes
+_CODES = {"nvfp4": _BYTES + (torch.float4_e2m1fn_x2,), "mxfp4": _BYTES + (torch.float4_e2m1fn_x2,),
+          "mxfp8": _BYTES + (torch.float8_e4m3fn,), "fp8": _BYTES + (torch.float8_e4m3fn,),
+          "fp8_block": _BYTES + (torch.float8_e4m3fn,), "int8": (torch.int8,)}
+
+
+def _check_codes(fmt, codes):
     _require_cuda(codes, "codes")
+    if codes.dtype not in _CODES[fmt]:
+        names = ", ".join(str(t).removeprefix("torch.") for t in _CODES[fmt])
+        raise FQLError(f"codes must be {names} ({fmt}), not {codes.dtype}")
+
+
+def _check_pack(fmt, codes, *scales):
+    """What every packer asks of its tensors: the kernel takes their addresses as they come."""
+    _check_codes(fmt, codes)
     for t in scales:
         _require_cuda(t, "scales")
         if t.device != codes.device:
@@ -445,7 +458,7 @@ def _packed_storage(nbytes, codes, out):
 
 def pack_weight_nvfp4(codes, scales, out=None):
     """Re-lay canonical NVFP4 weight (codes [N, K/2], scales [N, K/16]) for the GEMM."""
-    _check_pack(codes, scales)
+    _check_pack("nvfp4", codes, scales)
     N, K = codes.shape[0], codes.shape[1] * 2
     if tuple(scales.shape) != (N, K // 16):
         raise FQLError("scales must be [N, K/16]")
@@ -885,7 +898,7 @@ def packed_mxfp4_bytes(N, K):
 
 
 def _pack_sc(fmt, codes, scales, out):
-    _check_pack(codes, *(() if fmt == "fp8" else (scales,)))  # (per-tensor FP8's one scale is not packed)
+    _check_pack(fmt, codes, *(() if fmt == "fp8" else (scales,)))  # (per-tensor FP8's one scale is not packed)
     N = codes.shape[0]
     K = codes.shape[1] * (2 if fmt == "mxfp4" else 1)
     if fmt in ("mxfp4", "mxfp8") and tuple(scales.shape) != (N, K // 32):

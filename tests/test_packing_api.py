@@ -132,3 +132,23 @@ def test_storage_of_another_device_or_with_gaps_is_refused(fmt, calls):
         with pytest.raises(fql.FQLError, match="out must be"):
             experts(fmt, Gpu1).repack_(0, codes, 0.25 if fmt == "fp8" else scales)
     assert calls == []
+
+
+@pytest.mark.parametrize("fmt", ("nvfp4", "mxfp4", "mxfp8", "fp8", "fp8_block"))
+def test_codes_of_wider_types_are_refused(fmt, calls):
+    """Their first bytes would be packed as codes."""
+    codes, scales = operands(fmt)
+    for dtype in (torch.bfloat16, torch.float32, torch.int32, torch.float8_e5m2, torch.float8_e4m3fnuz):
+        wide = codes.to(dtype)
+        bad = [lambda: pack(fmt, wide, scales, storage(fmt)), lambda: weight(fmt).repack_(wide, scales)]
+        if fmt != "nvfp4":
+            bad.append(lambda: experts(fmt).repack_(0, wide, 0.25 if fmt == "fp8" else scales))
+            bad.append(lambda: fql.ExpertWeight.from_codes(fmt, torch.stack([wide] * 2), torch.stack([codes] * 2)))
+        for call in bad:
+            with pytest.raises(fql.FQLError, match="codes must be"):
+                call()
+    assert calls == []
+    bytes_ = [torch.uint8, torch.int8] + ([torch.float8_e4m3fn] if "fp8" in fmt else [])
+    for dtype in bytes_:
+        pack(fmt, codes.view(dtype), scales, storage(fmt))
+    assert len(calls) == len(bytes_)
