@@ -428,19 +428,23 @@ _CODES = {"nvfp4": _BYTES + (torch.float4_e2m1fn_x2,), "mxfp4": _BYTES + (torch.
           "mxfp8": _BYTES + (torch.float8_e4m3fn,), "fp8": _BYTES + (torch.float8_e4m3fn,),
           "fp8_block": _BYTES + (torch.float8_e4m3fn,), "int8": (torch.int8,)}
 
+_SCALES = {"nvfp4": _BYTES + (torch.float8_e4m3fn,), "mxfp4": _BYTES + (torch.float8_e8m0fnu,),
+           "mxfp8": _BYTES + (torch.float8_e8m0fnu,), "fp8_block": (torch.float32,),
+           "int8": (torch.float32,)}
 
-def _check_codes(fmt, codes):
-    _require_cuda(codes, "codes")
-    if codes.dtype not in _CODES[fmt]:
-        names = ", ".join(str(t).removeprefix("torch.") for t in _CODES[fmt])
-        raise FQLError(f"codes must be {names} ({fmt}), not {codes.dtype}")
+
+def _one_of(t, name, types, fmt):
+    _require_cuda(t, name)
+    if t.dtype not in types:
+        names = ", ".join(str(d).removeprefix("torch.") for d in types)
+        raise FQLError(f"{name} must be {names} ({fmt}), not {t.dtype}")
 
 
 def _check_pack(fmt, codes, *scales):
     """What every packer asks of its tensors: the kernel takes their addresses as they come."""
-    _check_codes(fmt, codes)
+    _one_of(codes, "codes", _CODES[fmt], fmt)
     for t in scales:
-        _require_cuda(t, "scales")
+        _one_of(t, "scales", _SCALES[fmt], fmt)
         if t.device != codes.device:
             raise FQLError("scales must be on the codes' device")
     if not all(t.is_contiguous() for t in (codes, *scales)):
@@ -903,10 +907,10 @@ def _pack_sc(fmt, codes, scales, out):
     K = codes.shape[1] * (2 if fmt == "mxfp4" else 1)
     if fmt in ("mxfp4", "mxfp8") and tuple(scales.shape) != (N, K // 32):
         raise FQLError("scales must be [N, K/32]")
-    if fmt == "fp8_block" and (tuple(scales.shape) != (N // 128, K // 128) or scales.dtype != torch.float32):
+    if fmt == "fp8_block" and tuple(scales.shape) != (N // 128, K // 128):
         raise FQLError("scales must be float32 [N/128, K/128]")
-    if fmt == "int8" and (codes.dtype != torch.int8 or tuple(scales.shape) != (N,) or scales.dtype != torch.float32):
-        raise FQLError("codes must be int8 [N, K] and scales float32 [N]")
+    if fmt == "int8" and tuple(scales.shape) != (N,):
+        raise FQLError("scales must be float32 [N]")
     out = _packed_storage(_size_query(f"fql_packed_{fmt}_bytes", N, K), codes, out)
     if fmt == "fp8":
         _check(_fn("fql_pack_weight_fp8")(_ptr(codes), N, K, _ptr(out), out.numel(),

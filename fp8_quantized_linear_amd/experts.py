@@ -22,8 +22,8 @@ import struct
 
 import torch
 
-from . import (FP8BlockWeight, FP8Weight, FQLError, INT8Weight, MXFP4Weight, MXFP8Weight, _check, _check_codes, _pack_sc,
-               _rows_view, _size_query, fp8_output_scale, fp8_scale_from_amax, lib)
+from . import (FP8BlockWeight, FP8Weight, FQLError, INT8Weight, MXFP4Weight, MXFP8Weight, _CODES, _SCALES, _check,
+               _one_of, _pack_sc, _rows_view, _size_query, fp8_output_scale, fp8_scale_from_amax, lib)
 from . import quant_fp8_block_weight, quant_fp8_weight, quant_int8_weight, quant_mxfp4_weight, quant_mxfp8_weight
 from .serving import (ACTIVATIONS, FORMATS, _bf16, _cuda, _f32, _format, _i32, _new, _query, _rows, _same_device, _stream,
                       _u8, _within, _workspace)
@@ -117,7 +117,9 @@ class ExpertWeight:
         _format(fmt)
         if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dim() != 3 or codes.shape[0] < 1:
             raise FQLError("codes must be a CUDA (HIP) tensor [E, N, K]")
-        _check_codes(fmt, codes)
+        _one_of(codes, "codes", _CODES[fmt], fmt)
+        if fmt != "fp8":
+            _one_of(scales, "scales", _SCALES[fmt], fmt)
         E, N, K = codes.shape
         K *= 2 if fmt == "mxfp4" else 1
         if not isinstance(scales, torch.Tensor) or scales.shape[:1] != (E,) or scales.device != codes.device:

@@ -152,3 +152,23 @@ def test_codes_of_wider_types_are_refused(fmt, calls):
     for dtype in bytes_:
         pack(fmt, codes.view(dtype), scales, storage(fmt))
     assert len(calls) == len(bytes_)
+
+
+@pytest.mark.parametrize("fmt", ("nvfp4", "mxfp4", "mxfp8"))
+def test_one_byte_scales_of_another_type_are_refused(fmt, calls):
+    """A checkpoint's scales as float32, of the right shape, would be packed byte by byte."""
+    codes, scales = operands(fmt)
+    own = torch.float8_e4m3fn if fmt == "nvfp4" else torch.float8_e8m0fnu
+    other = torch.float8_e8m0fnu if fmt == "nvfp4" else torch.float8_e4m3fn
+    for wide in (scales.to(torch.float32), scales.to(torch.bfloat16), scales.to(torch.int32), scales.view(other)):
+        bad = [lambda: pack(fmt, codes, wide, storage(fmt)), lambda: weight(fmt).repack_(codes, wide)]
+        if fmt != "nvfp4":
+            bad.append(lambda: experts(fmt).repack_(0, codes, wide))
+            bad.append(lambda: fql.ExpertWeight.from_codes(fmt, torch.stack([codes] * 2), torch.stack([wide] * 2)))
+        for call in bad:
+            with pytest.raises(fql.FQLError, match="scales must be"):
+                call()
+    assert calls == []
+    for dtype in (torch.uint8, own):
+        pack(fmt, codes, scales.view(dtype), storage(fmt))
+    assert len(calls) == 2
