@@ -443,6 +443,8 @@ def _one_of(t, name, types, fmt):
 def _check_pack(fmt, codes, *scales):
     """What every packer asks of its tensors: the kernel takes their addresses as they come."""
     _one_of(codes, "codes", _CODES[fmt], fmt)
+    if codes.dim() != 2:
+        raise FQLError("codes must have two dimensions")
     for t in scales:
         _one_of(t, "scales", _SCALES[fmt], fmt)
         if t.device != codes.device:

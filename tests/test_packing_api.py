@@ -172,3 +172,15 @@ def test_one_byte_scales_of_another_type_are_refused(fmt, calls):
     for dtype in (torch.uint8, own):
         pack(fmt, codes, scales.view(dtype), storage(fmt))
     assert len(calls) == 2
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_codes_that_are_no_matrix_are_refused(fmt, calls):
+    """The codes of several experts, or one row's, are no [N, K] weight."""
+    codes, scales = operands(fmt)
+    for bad in (torch.stack([codes, codes]), codes[0]):
+        with pytest.raises(fql.FQLError, match="codes must have two dimensions"):
+            pack(fmt, bad, scales, storage(fmt))
+        with pytest.raises(fql.FQLError, match="codes must"):
+            weight(fmt).repack_(bad, scales)
+    assert calls == []
