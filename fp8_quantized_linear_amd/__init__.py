@@ -462,6 +462,14 @@ def _packed_storage(nbytes, codes, out):
     return out
 
 
+def _check_repack(fmt, w, codes):
+    """The storage's layout goes by the weight's shape: new codes have the same."""
+    _require_cuda(codes, "codes")
+    per = 2 if fmt in ("nvfp4", "mxfp4") else 1
+    if tuple(codes.shape) != (w.N, w.K // per):
+        raise FQLError(f"codes must be [{w.N}, {w.K // per}] as the weight's, not {list(codes.shape)}")
+
+
 def pack_weight_nvfp4(codes, scales, out=None):
     """Re-lay canonical NVFP4 weight (codes [N, K/2], scales [N, K/16]) for the GEMM."""
     _check_pack("nvfp4", codes, scales)
@@ -536,6 +544,7 @@ class NVFP4Weight:
         Weights with a transform or a dynamic input scale pass g_w to the
         library by value and reject a changed scale.
         """
+        _check_repack("nvfp4", self, codes)
         pack_weight_nvfp4(codes, scales, out=self.packed)
         if weight_global_scale is not None and float(weight_global_scale) != self.weight_global_scale:
             if self.transform is not None or self.dynamic_input_scale:
@@ -957,6 +966,7 @@ class _ScWeight:
 
     def repack_(self, codes, scales=None):
         """Re-pack new canonical weights into the same storage (address kept)."""
+        _check_repack(self.fmt, self, codes)
         _pack_sc(self.fmt, codes, scales, self.packed)
         return self
 
@@ -1018,6 +1028,7 @@ class FP8Weight(_ScWeight):
     def repack_(self, codes, scales=None, weight_scale=None):
         """Re-pack new FP8 weight codes into the same storage; a new weight_scale
         updates alpha and alpha_dev (in stream order)."""
+        _check_repack(self.fmt, self, codes)
         _pack_sc(self.fmt, codes, scales, self.packed)
         if weight_scale is not None:
             self.weight_scale = _c_f32(float(weight_scale)).value

@@ -184,3 +184,16 @@ def test_codes_that_are_no_matrix_are_refused(fmt, calls):
         with pytest.raises(fql.FQLError, match="codes must"):
             weight(fmt).repack_(bad, scales)
     assert calls == []
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_repacking_another_shape_is_refused(fmt, calls):
+    """A smaller weight fits the storage, whose layout goes by the old shape."""
+    codes, scales = operands(fmt)
+    half = codes[:N // 2].contiguous(), None if scales is None else scales[:(scales.shape[0]) // 2].contiguous()
+    narrow = codes[:, :codes.shape[1] // 2].contiguous(), (
+        None if scales is None else scales if fmt == "int8" else scales[:, :scales.shape[1] // 2].contiguous())
+    for bad in (half, narrow):
+        with pytest.raises(fql.FQLError, match="codes must be"):
+            weight(fmt).repack_(*bad)
+    assert calls == []
