@@ -772,6 +772,10 @@ hipError_t launch_t(const ExpertsPlan& p, const ExpertsArgs& a, uint8_t* workspa
 
 }  // namespace
 
+// From how many rows an expert on a product takes the large tiles (why: plan_product).
+static int64_t large_rows(int fmt) { return fmt == SC_INT8 ? 20 : 8; }
+constexpr int64_t kTokenMax = 6;  // tokens of a call whose pairs stay for themselves, at most (plan_experts)
+
 // The tile of one product, N columns of a K-deep product, `pairs` rows over E experts:
 // 16 x 128 while an expert has few rows, else the tile of least time: rounds of the card's
 // workgroups times (chunks * tc + f) us, with six tenths of a tile an expert for its last
@@ -796,7 +800,7 @@ static ProductPlan plan_product(int fmt, int64_t pairs, int64_t E, int64_t N, in
   const bool block = fmt == SC_FP8_BLOCK;
   const int64_t KC = round_up(K, 128) / 128;
   ProductPlan p{};
-  if (pairs / E >= (fmt == SC_INT8 ? 20 : 8)) {
+  if (pairs / E >= large_rows(fmt)) {
     double best = 0.0;
     for (const Tile& t : tiles) {
       const int64_t R = 32 * t.wm * t.mtw;
@@ -836,10 +840,12 @@ ExpertsPlan plan_experts(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, in
   // 1 token 17 us (sorted 32), 4 tokens 37 (52), 8 tokens 63 (69), 12 tokens 89 (80); 8
   // experts, 2 a token (FP8, 4096, 14336): 1 token 64 (93), 2 tokens 118 (127), 3 tokens
   // 170 (159); 128 experts, 8 a token (MXFP4, 4096, 1280): 6 tokens 82 (84), 8 tokens 105 (100).
-  p.token = T == 1 || (T <= 6 && p.tokens == T && 4 * p.pairs < 3 * E);
+  p.token = T == 1 || (T <= kTokenMax && p.tokens == T && 4 * p.pairs < 3 * E);
   p.h_quantized = !p.token && p.up.large && fmt != SC_INT8;
   p.counter_bytes = 64 * 1024;
-  p.meta_bytes = round_up(meta_bytes(p.pairs, p.up.max_tiles, p.down.max_tiles), 256);
+  // (the tiles of the smallest form, so that more tokens never take fewer bytes)
+  const int64_t tiles = std::min(p.pairs, p.pairs / (p.up.large ? 64 : 16) + std::min(E, p.pairs));
+  p.meta_bytes = round_up(meta_bytes(p.pairs, tiles, tiles), 256);
   p.xcode_bytes = round_up(p.tokens * xr.ld_codes, 256);
   p.xscale_bytes = round_up(p.tokens * xr.ld_scales, 256);
   p.h_bytes = p.h_quantized ? 0 : round_up(p.pairs * 4 * round_up(I, 4), 256);
@@ -850,6 +856,17 @@ ExpertsPlan plan_experts(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, in
   p.total_bytes = p.counter_bytes + p.meta_bytes + p.xcode_bytes + p.xscale_bytes + p.h_bytes + p.hcode_bytes +
                   p.hscale_bytes + p.d_bytes;
   return p;
+}
+
+// Larger tiles keep h as codes and d in 16 bits, so the call of the most tokens need not be
+// the one of the most bytes: the largest calls of each of the three ways are looked at.
+int64_t experts_workspace(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, int64_t N, int64_t I, int64_t Ho) {
+  auto bytes = [&](int64_t t) { return plan_experts(fmt, t, k, E, H, N, I, Ho).total_bytes; };
+  int64_t most = bytes(T);
+  for (int64_t t = 1; t <= std::min(T, kTokenMax); ++t) most = std::max(most, bytes(t));
+  const int64_t small = (large_rows(fmt) * E - 1) / k;  // the most tokens on 16-row tiles
+  if (small >= 1) most = std::max(most, bytes(std::min(T, small)));
+  return most;
 }
 
 std::string describe_experts(const ExpertsPlan& p) {

@@ -1494,7 +1494,7 @@ int fql_experts_workspace_bytes(int format, int64_t T, int k, int64_t E, int64_t
     int64_t I = 0;
     fql::ExpertsPlan plan;
     if (int r = check_experts(format, T, k, E, H, N, Ho, activation, &I, &plan)) return r;
-    *bytes = (size_t)plan.total_bytes;
+    *bytes = (size_t)fql::experts_workspace(plan.fmt, std::max<int64_t>(T, 1), k, E, H, N, I, Ho);
     return ok();
   });
 }

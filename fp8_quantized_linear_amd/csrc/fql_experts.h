@@ -68,6 +68,8 @@ struct ExpertsPlan {
 };
 // N: output columns of the first product (before the activation), I: its activation's, Ho: of the second.
 ExpertsPlan plan_experts(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, int64_t N, int64_t I, int64_t Ho);
+// Workspace bytes of a call of T tokens or of any number below.
+int64_t experts_workspace(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, int64_t N, int64_t I, int64_t Ho);
 std::string describe_experts(const ExpertsPlan& p);
 
 struct ExpertWeights {

@@ -736,7 +736,7 @@ typedef struct {
  *   residual  [T][ldr] bf16, Ho columns, or NULL.
  *   y         [T][ldy]; may be residual or (Ho = H) x itself: same pointer and stride.
  *   workspace 256-byte aligned, at least fql_experts_workspace_bytes of the same
- *             shapes; one workspace per stream at a time. Its first 64 KiB are left
+ *             shapes (which serves fewer tokens too); one workspace per stream at a time. Its first 64 KiB are left
  *             alone (a linear call's workspace serves).
  * Dimensions are at most 2^18, T at most 2^24. T = 0 does nothing. Nothing is read
  * back to the host.

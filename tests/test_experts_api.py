@@ -160,3 +160,17 @@ def test_the_gpu_tests_reach_every_tile():
             for tile in ("16x128", "64x256", "128x256", "256x256"):
                 assert any(f"tiles={tile}" in p for p in of), (fmt, product, tile)
         assert any("token" in p for p in plans)
+
+
+@pytest.mark.parametrize("fmt", (MXFP4, MXFP8, FP8, BLOCK, INT8))
+@pytest.mark.parametrize("k,E,H,N,Ho", [(8, 64, 4096, 2048, 4096), (2, 8, 4096, 28672, 4096), (4, 32, 2048, 2816, 2048),
+                                        (1, 1, 128, 256, 128), (64, 1024, 256, 512, 384), (8, 128, 128, 256, 16384)])
+def test_a_workspace_of_the_largest_batch_serves_every_smaller_one(fmt, k, E, H, N, Ho):
+    n = ctypes.c_size_t()
+    sizes = []
+    batches = sorted({*range(1, 700), *(int(1.07 ** i) for i in range(246)), *(E * r // k + d for r in (8, 20)
+                     for d in (-1, 0, 1)), 1 << 24})
+    for T in (t for t in batches if 0 < t <= 1 << 24):
+        assert fql.lib().fql_experts_workspace_bytes(fmt, T, k, E, H, N, Ho, 5, ctypes.byref(n)) == 0
+        sizes.append((n.value, T))
+    assert sizes == sorted(sizes), next((a, b) for a, b in zip(sizes, sizes[1:]) if a > b)
