@@ -493,7 +493,7 @@ __global__ __launch_bounds__(64 * WM * WN) void experts_product_kernel(const Pro
         const float col = n < g.ntiles_w * 16 ? reinterpret_cast<const float*>(wscales)[n] : 0.0f;
         const int4v s = __builtin_bit_cast(int4v, acc[mt][nt]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[mt][nt][i] = (float)s[i] * (row[i] * col);
+        for (int i = 0; i < 4; ++i) acc[mt][nt][i] = int8_value(s[i], row[i], col);
       }
     }
   }

@@ -261,7 +261,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float s = acc[mt][nt][4 * i + e];
-            if constexpr (T::INT) s = (float)(int)__float_as_uint(s) * (rsc[mt] * col[e]);
+            if constexpr (T::INT) s = int8_value((int)__float_as_uint(s), rsc[mt], col[e]);
             v[e] = alpha * s + b[e];
           }
           put(mt * 32 + (lane & 31), c, v);
@@ -299,8 +299,8 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
           for (int e = 0; e < 4; ++e) {
             float a = acc[mt][nt][4 * i + e], u = acc[mt][nt][4 * i + e + 8];
             if constexpr (T::INT) {
-              a = (float)(int)__float_as_uint(a) * (rsc[mt] * cg[e]);
-              u = (float)(int)__float_as_uint(u) * (rsc[mt] * cu[e]);
+              a = int8_value((int)__float_as_uint(a), rsc[mt], cg[e]);
+              u = int8_value((int)__float_as_uint(u), rsc[mt], cu[e]);
             }
             const float z = alpha * a + bg[e];
             acc[mt][nt][4 * i + e] = z_sigmoid(z, z) * (alpha * u + bu[e]);
@@ -510,7 +510,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& g, const Meta& me
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float s = acc[mt][nt][e];
-          if constexpr (T::INT) s = (float)(int)__float_as_uint(s) * (rsc[mt] * col[e / 4][e % 4]);
+          if constexpr (T::INT) s = int8_value((int)__float_as_uint(s), rsc[mt], col[e / 4][e % 4]);
           v[e] = alpha * s + b[e];
         }
         if (!inside) {

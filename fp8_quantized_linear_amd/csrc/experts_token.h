@@ -191,7 +191,7 @@ __device__ __forceinline__ void row_product(const X* __restrict__ row, int64_t K
 // The lane's column's sum as float32 (INT8: times the scales).
 template <int F>
 __device__ __forceinline__ float finished(float s, float row, const uint8_t* wscales, int n) {
-  if constexpr (F == SC_INT8) return (float)(int)__float_as_uint(s) * (row * reinterpret_cast<const float*>(wscales)[n]);
+  if constexpr (F == SC_INT8) return int8_value((int)__float_as_uint(s), row, reinterpret_cast<const float*>(wscales)[n]);
   else return s;
 }
 

@@ -72,8 +72,8 @@ __device__ __forceinline__ float4v mfma_int8(const int8v& a, const int8v& b, con
 // Four rows' sums of one column as float32 (rounded above 2^24) times the scales.
 __device__ __forceinline__ float4v int8_scaled(const float4v& acc, const float4v& row, float col) {
   const int4v s = __builtin_bit_cast(int4v, acc);
-  return float4v{(float)s[0] * (row[0] * col), (float)s[1] * (row[1] * col), (float)s[2] * (row[2] * col),
-                 (float)s[3] * (row[3] * col)};
+  return float4v{int8_value(s[0], row[0], col), int8_value(s[1], row[1], col), int8_value(s[2], row[2], col),
+                 int8_value(s[3], row[3], col)};
 }
 
 // The sum of two fragments of one format.

@@ -492,8 +492,10 @@ int fql_linear_fp8_block(const void* x, int64_t M, int64_t K, int64_t ldx, const
  * to even (s = 0: q = 0). A row that holds a NaN or an infinity gets scale NaN,
  * which makes its outputs NaN; its codes say nothing. Codes [rows][K], 8-byte
  * aligned; scales float [rows]. A weight's codes may be any int8, -128 included.
- * The sum over K is exact in 32-bit integers (K <= 131072); where a launch plan
- * splits K, the ranges' sums are scaled and joined in float32.
+ * The sum over K is exact in 32-bit integers (K <= 131072); it is multiplied by the
+ * channel's scale and then the row's in float32, and stays in range where the result does
+ * for channel scales of 2^-126 .. 2^97 (0 and any row scale included). Where a launch plan
+ * splits K, the ranges' scaled sums are joined in float32.
  * ------------------------------------------------------------------------- */
 int fql_quant_int8(const void* x, int64_t M, int64_t K, int64_t ldx, int8_t* codes, float* scales,
                    void* stream);

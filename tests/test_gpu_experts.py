@@ -502,6 +502,46 @@ def test_decoder_feed_forward(fmt, T):
         assert torch.equal(gy, eager)
 
 
+@pytest.mark.parametrize("T", [1, 19, 40, 6000])
+def test_int8_scales_of_any_size_beside_one_another(T):
+    """A row's scale times a channel's below or above float32's range where the product with the sum is not:
+    single tokens, and tiles of every kind, in both products."""
+    H, I, Ho = 1024, 2048, 64
+    announce(f"experts int8 scales T={T} {fql.experts_fused_plan('int8', T, 1, 1, H, I, Ho, 'none')}")
+
+    def pack(codes, scale):
+        sw = torch.full((1, codes.shape[0]), 1.4 * 2.0 ** scale, dtype=torch.float32)
+        return fql.ExpertWeight.from_codes("int8", torch.from_numpy(codes[None].astype(np.int8)).to(DEV), sw.to(DEV))
+
+    rng = np.random.default_rng(T)
+    uc = rng.integers(90, 128, (I, H))
+    dc = rng.integers(90, 128, (Ho, I))
+    dc[3::4] = 0
+    w, e = torch.ones((T, 1), device=DEV), torch.zeros((T, 1), dtype=torch.int32, device=DEV)
+    q = rng.integers(64, 128, (T, H))
+    q[:, 0] = 127
+    for a, b, c in ((-98, -48, 30), (-40, -60, -67), (121, 8, -60), (100, -20, 60), (0, 0, 0)):
+        x, x64 = bf16(np.ldexp(q.astype(np.float64), a))
+        assert np.array_equal(x64, np.ldexp(q.astype(np.float64), a))
+        y = f64(fql.experts_fused(x, pack(uc, b), pack(dc, c), w, e, activation="none"))
+        s = float(np.float32(1.4))
+        h = np.ldexp(q.astype(np.float64) @ uc.T * s, a + b)
+        past = (h > 3.4e38).any(1)
+        assert not past.any() or past.all()
+        # counted: h's roundings (2^-22) move its scale by as much, and rare codes by a step, of I * 64 steps a sum
+        # and more; an fp16 rounding of a row (2^-11); y's own rounding
+        hq, hs = O.quant_int8(np.minimum(h, 3.4e38).astype(np.float32))
+        want = np.ldexp(hq.astype(np.float64) @ dc.T * (hs.astype(np.float64)[:, None] * s), c)
+        if past.all():
+            assert np.isnan(y).all()  # an inner activation beyond float32: the row's scale is NaN
+            continue
+        assert (y[:, 3::4] == 0).all(), (a, b, c)
+        over = want > 3.41e38
+        assert over[:, 0].all() == over.any() == (c == 60) and np.isposinf(y[over]).all()
+        y, want = np.where(over, 0.0, y), np.where(over, 0.0, want)
+        assert (np.abs(y - want) <= (HALF_BF16 + 2.0 ** -11 + 2.0 ** -16) * want).all(), (a, b, c)
+
+
 def parts_of(plan):
     return int(plan.rsplit("tokens=", 1)[1])
 

@@ -271,3 +271,54 @@ def test_warmup_takes_int8_layers():
     announce("int8 warmup")
     g, _ = weight(np.random.default_rng(1).standard_normal((64, 128)))
     assert fql.warmup([g, g], [1, 40]) == 2
+
+
+def check_relative(y, want, what):
+    """`want` is what the exact sums of integers times the scales come to, all normal numbers of bf16, zeros or
+    beyond its range. Counted: the sum's conversion and the scales' products a float32 rounding each (2^-24), the
+    join of up to 16 ranges of K, whose terms all have one sign or cancel exactly (2^-20), one bf16 rounding."""
+    y = f64(y)
+    top = 3.3895313892515355e38
+    past = np.abs(want) > top * (1 + 2.0 ** -9)
+    assert np.array_equal(np.isinf(y), past), what
+    assert (np.sign(y) == np.sign(want)).all(), what
+    d = np.abs(np.where(past, 0.0, y) - np.where(past, 0.0, want))
+    assert (d <= (HALF_BF16 + 2.0 ** -20) * np.where(past, 0.0, np.abs(want))).all(), (what, float(np.nanmax(d)))
+
+
+# (row's scale 2^a, channel's scale 1.4 * 2^b): their product alone is below or above float32's range, or the
+# sum times the row's scale is, while what comes of all three is a normal number
+APART = [(-98, -51), (-75, -74), (-110, -30), (121, 8), (121, -30), (100, 40), (60, -60), (0, 0)]
+
+
+@pytest.mark.parametrize("M", [1, 20, 70, 300])
+def test_scales_of_any_size_beside_one_another(M):
+    K, N = 4096, 64
+    announce(f"int8 scales of any size M={M} {fql.linear_sc_plan('int8', M, N, K)}")
+    rng = np.random.default_rng(M)
+    codes = rng.integers(90, 128, (N, K))
+    codes[3::4, 1::2] = -codes[3::4, 0::2]  # with equal neighbours in x these columns' sums are 0 in every range of K
+    q = np.repeat(rng.integers(64, 127, (M, K // 2)), 2, axis=1)
+    q[:, :2] = 127
+    sums = q.astype(np.float64) @ codes.T
+    wc = torch.from_numpy(codes.astype(np.int8)).to(DEV)
+    for a, b in APART:
+        x, x64 = bf16(np.ldexp(q.astype(np.float64), a))
+        assert np.array_equal(x64, np.ldexp(q.astype(np.float64), a))
+        sw = np.full(N, np.ldexp(np.float32(1.4), b), dtype=np.float32)
+        g = fql.INT8Weight(fql.pack_weight_int8(wc, torch.from_numpy(sw).to(DEV)), N, K)
+        with np.errstate(over="ignore"):
+            want = np.ldexp(sums, a) * sw.astype(np.float64)
+        check_relative(fql.linear_int8(x, g), want, ("plain", a, b))
+        check_relative(fql.linear_fused(x, g, activation="relu"), want, ("fused", a, b))
+        check_relative(fql.linear_fused(fql.quant_operand(x, "int8"), g, activation="relu"), want, ("operand", a, b))
+        # gated, with ups of their own size: silu(z) is z where z is large, z / 2 where it is small
+        if a + b > -40:
+            continue
+        up = sw.reshape(-1, 32).copy()
+        up[:, 16:] = np.ldexp(np.float32(1.0), -a - 20)
+        g = fql.INT8Weight(fql.pack_weight_int8(wc, torch.from_numpy(up.reshape(-1)).to(DEV)), N, K)
+        z, u = (np.ldexp(v, a).reshape(M, -1, 16) for v in np.split(sums.reshape(M, -1, 32), 2, axis=2))
+        want = (z * float(sw[0]) / 2 * u * 2.0 ** (-a - 20)).reshape(M, -1)
+        y = f64(fql.linear_fused(x, g, activation="swiglu"))
+        assert (np.abs(y - want) <= (HALF_BF16 + 2.0 ** -17) * np.abs(want)).all(), ("gated", a, b)
