@@ -299,6 +299,17 @@ def _rows_view(x, name):
     return x2, ld
 
 
+def _out_rows(out, M, N):
+    """(2-D view [M, N], row stride) of a linear call's output."""
+    _require_cuda(out, "out")
+    if out.dtype != torch.bfloat16:
+        raise FQLError("out must be a bfloat16 tensor")
+    y2, ldy = _rows_view(out, "out")
+    if tuple(y2.shape) != (M, N):
+        raise FQLError(f"out must hold {M} rows of {N} columns, not {tuple(out.shape)}")
+    return y2, ldy
+
+
 # ---------------------------------------------------------------------------
 # availability
 # ---------------------------------------------------------------------------
@@ -657,7 +668,9 @@ def linear_nvfp4(x, weight, alpha=None, bias=None, out=None, workspace=None):
             raise FQLError("bias must be a contiguous bf16 tensor of N elements")
     if out is None:
         out = torch.empty(tuple(x.shape[:-1]) + (N,), dtype=torch.bfloat16, device=x.device)
-    y2, ldy = _rows_view(out, "out")
+        y2, ldy = _rows_view(out, "out")
+    else:
+        y2, ldy = _out_rows(out, M, N)
     need = linear_workspace_bytes(M, N, K)
     if workspace is None:
         workspace = _workspace(x.device, need)
@@ -705,7 +718,7 @@ def linear_nvfp4_noalloc(x, weight, out, alpha=None, bias=None):
         _require_cuda(bias, "bias")
         if bias.dtype != torch.bfloat16 or bias.numel() != weight.N or not bias.is_contiguous():
             raise FQLError("bias must be a contiguous bf16 tensor of N elements")
-    y2, ldy = _rows_view(out, "out")
+    y2, ldy = _out_rows(out, M, weight.N)
     a = weight.alpha if alpha is None else alpha
     _check(lib().fql_linear_nvfp4_noalloc(_ptr(x2), M, K, ld, weight.input_global_scale,
                                           weight.hadamard_block, _ptr(weight.packed), weight.N,
@@ -731,7 +744,7 @@ def linear_nvfp4_gemm(M, weight, workspace, alpha, x_aligned=True, bias=None, ou
     N = weight.N
     if out is None:
         out = torch.empty((int(M), N), dtype=torch.bfloat16, device=workspace.device)
-    y2, ldy = _rows_view(out, "out")
+    y2, ldy = _out_rows(out, int(M), N)
     _check(lib().fql_linear_nvfp4_gemm(int(M), weight.K, int(bool(x_aligned)), _ptr(weight.packed), N,
                                        float(alpha), _ptr(bias), _ptr(y2), ldy, _ptr(workspace),
                                        workspace.numel(), _stream(workspace.device)))
@@ -1080,7 +1093,9 @@ def _linear_sc(fmt, x, weight, alpha, bias, out, workspace):
             raise FQLError("bias must be a contiguous bf16 tensor of N elements")
     if out is None:
         out = torch.empty(tuple(x.shape[:-1]) + (N,), dtype=torch.bfloat16, device=x.device)
-    y2, ldy = _rows_view(out, "out")
+        y2, ldy = _rows_view(out, "out")
+    else:
+        y2, ldy = _out_rows(out, M, N)
     if workspace is None:
         workspace = _workspace(x.device, linear_sc_workspace_bytes(fmt, M, N, K))
     st = _stream(x.device)
