@@ -299,6 +299,14 @@ def _rows_view(x, name):
     return x2, ld
 
 
+def _same_gpu(x, **tensors):
+    """Every tensor of a linear call on x's device: its kernels take their addresses as they come."""
+    index = x.get_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != index:
+            raise FQLError(f"{name} must be on x's device")
+
+
 def _out_rows(out, M, N):
     """(2-D view [M, N], row stride) of a linear call's output."""
     _require_cuda(out, "out")
@@ -671,10 +679,11 @@ def linear_nvfp4(x, weight, alpha=None, bias=None, out=None, workspace=None):
         y2, ldy = _rows_view(out, "out")
     else:
         y2, ldy = _out_rows(out, M, N)
+    T = getattr(weight, "transform", None)
+    _same_gpu(x, weight=weight.packed, bias=bias, out=out, workspace=workspace, alpha_dev=alpha_dev, transform=T)
     need = linear_workspace_bytes(M, N, K)
     if workspace is None:
         workspace = _workspace(x.device, need)
-    T = getattr(weight, "transform", None)
     if getattr(weight, "dynamic_input_scale", False):
         b = T.shape[0] if T is not None else weight.hadamard_block
         _check(lib().fql_linear_nvfp4_dynamic(_ptr(x2), M, K, ld, _ptr(T), b, _ptr(weight.packed), N,
@@ -719,6 +728,7 @@ def linear_nvfp4_noalloc(x, weight, out, alpha=None, bias=None):
         if bias.dtype != torch.bfloat16 or bias.numel() != weight.N or not bias.is_contiguous():
             raise FQLError("bias must be a contiguous bf16 tensor of N elements")
     y2, ldy = _out_rows(out, M, weight.N)
+    _same_gpu(x, weight=weight.packed, bias=bias, out=out)
     a = weight.alpha if alpha is None else alpha
     _check(lib().fql_linear_nvfp4_noalloc(_ptr(x2), M, K, ld, weight.input_global_scale,
                                           weight.hadamard_block, _ptr(weight.packed), weight.N,
@@ -1096,6 +1106,8 @@ def _linear_sc(fmt, x, weight, alpha, bias, out, workspace):
         y2, ldy = _rows_view(out, "out")
     else:
         y2, ldy = _out_rows(out, M, N)
+    _same_gpu(x, weight=weight.packed, bias=bias, out=out, workspace=workspace,
+              alpha_dev=weight.alpha_dev if fmt == "fp8" and alpha is None else None)
     if workspace is None:
         workspace = _workspace(x.device, linear_sc_workspace_bytes(fmt, M, N, K))
     st = _stream(x.device)

@@ -18,7 +18,7 @@ def bf16(*shape, kind=Gpu0):
 
 
 def u8(n, kind=Gpu0):
-    return on(kind, torch.zeros(n, dtype=torch.uint8))
+    return on(kind, torch.empty(n, dtype=torch.uint8))
 
 
 def weight(fmt, kind=Gpu0, alpha_kind=Gpu0):
@@ -64,3 +64,26 @@ def test_outputs_of_another_shape_or_type_are_refused(fmt, calls):
     for out in (bf16(2, 3, N), bf16(M, N), bf16(M, N + 5)[:, :N]):
         assert LINEAR[fmt](x, weight(fmt), out=out, workspace=ws) is out
     assert len(calls) == 3
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_tensors_of_another_device_are_refused(fmt, calls):
+    """The kernel would use an address that is the host's or another GPU's."""
+    x, out, ws = bf16(M, K), bf16(M, N), u8(1 << 20)
+    good = dict(weight=weight(fmt), out=out, workspace=ws, bias=bf16(N))
+    for kind in (torch.Tensor, Gpu1):
+        bad = [("weight", weight(fmt, kind=kind)), ("out", bf16(M, N, kind=kind)), ("workspace", u8(1 << 20, kind)),
+               ("bias", bf16(N, kind=kind))]
+        for name, t in bad:
+            with pytest.raises(fql.FQLError, match=f"{name} must be"):
+                LINEAR[fmt](x, **{**good, name: t})
+        if fmt in ("nvfp4", "fp8"):
+            with pytest.raises(fql.FQLError, match="alpha_dev must be"):
+                LINEAR[fmt](x, **{**good, "weight": weight(fmt, alpha_kind=kind)})
+        if fmt == "nvfp4":
+            for name, t in bad:
+                if name != "workspace":
+                    with pytest.raises(fql.FQLError, match=f"{name} must be"):
+                        fql.linear_nvfp4_noalloc(x, **{**{k: v for k, v in good.items() if k != "workspace"}, name: t})
+    assert calls == []
+    assert LINEAR[fmt](x, **good) is out and len(calls) == 1

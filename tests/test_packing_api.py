@@ -21,7 +21,7 @@ class Gpu1(Gpu0):
     index = 1
 
 
-N, K = 256, 512
+N, K = 128, 128  # (small: torch starts no threads, which other tests' forked workers would inherit halfway)
 
 
 def on(kind, t):
@@ -39,7 +39,7 @@ def operands(fmt, kind=Gpu0):
 
 
 def storage(fmt, kind=Gpu0):
-    return on(kind, torch.zeros(fql._size_query(f"fql_packed_{fmt}_bytes", N, K), dtype=torch.uint8))
+    return on(kind, torch.empty(fql._size_query(f"fql_packed_{fmt}_bytes", N, K), dtype=torch.uint8))
 
 
 def pack(fmt, codes, scales, out):
@@ -62,7 +62,7 @@ def weight(fmt, kind=Gpu0):
 def experts(fmt, kind=Gpu0):
     size = -(-storage(fmt).numel() // 256) * 256
     args = dict(input_scale=0.5, alpha=on(kind, torch.zeros(2))) if fmt == "fp8" else {}
-    return fql.ExpertWeight(fmt, on(kind, torch.zeros((2, size), dtype=torch.uint8)), N, K, **args)
+    return fql.ExpertWeight(fmt, on(kind, torch.empty((2, size), dtype=torch.uint8)), N, K, **args)
 
 
 @pytest.fixture
@@ -123,7 +123,7 @@ def test_storage_of_another_device_or_with_gaps_is_refused(fmt, calls):
     """The packing kernel would write through an address that is not its device's, or over the gaps of a view."""
     codes, scales = operands(fmt)
     n = storage(fmt).numel()
-    for out in (on(torch.Tensor, storage(fmt)), storage(fmt, Gpu1), on(Gpu0, torch.zeros(2 * n, dtype=torch.uint8))[::2]):
+    for out in (on(torch.Tensor, storage(fmt)), storage(fmt, Gpu1), on(Gpu0, torch.empty(2 * n, dtype=torch.uint8))[::2]):
         with pytest.raises(fql.FQLError, match="out must be"):
             pack(fmt, codes, scales, out)
     with pytest.raises(fql.FQLError, match="out must be"):
