@@ -783,12 +783,22 @@ constexpr int64_t kTokenMax = 6;  // tokens of a call whose pairs stay for thems
 // as others end. f is fitted to 50 products (each tile forced, 24 to 4096 tokens, 4 to 128
 // experts): the tile it picks costs a call 0.9% over the best of the three on average.
 // (4 experts of FP8, 495 tokens, 5376, 288 inner: 64-row tiles 43.6 us, 128-row 53.2; 60 of
-// MXFP4, 152 tokens, 672, 448 inner, down: 28.4 and 30.0, 256 rows 33.9.) Whole calls with 16-row tiles against 64-row ones, us: at 4 rows an expert
-// MXFP8 (64 experts, 4096, 1024 inner) 164 and 162, at 8 164 and 158, at 16 178 and 160;
-// block FP8 (32, 4096, 2048) 148 and 148, 155 and 153, 166 and 154; MXFP4 (128, 4096, 1280)
-// 211 and 209, 219 and 211, 236 and 208; FP8 (8, 4096, 14336) 257 and 279, 261 and 257, 287
-// and 263; INT8 (32, 2048, 1408; quantizes h on its own either way) 66 and 79, 68 and 80,
-// 74 and 81, at 20 rows 80 and 78.
+// MXFP4, 152 tokens, 672, 448 inner, down: 28.4 and 30.0, 256 rows 33.9.)
+// Whole calls on 16-row tiles and on the larger ones, us, at 4, 8 and 16 rows an expert:
+//   MXFP8      64 experts, 4096, 1024 inner   158, 151   166, 154   182, 157
+//              32, 2048, 2048                  89, 85     92, 85    102, 87
+//   block FP8  32, 4096, 2048                 152, 149   158, 151   170, 153
+//              64, 2048, 1024                  88, 88     92, 90    101, 91
+//   MXFP4      128, 4096, 1280                201, 195   210, 198   244, 206
+//              32, 2048, 2048                  50, 48     50, 48     56, 48
+//   FP8        8, 4096, 14336                 245, 256   250, 257   290, 260
+//              32, 2048, 1408                  60, 60     61, 60     69, 61
+// and INT8, which quantizes h in a launch of its own either way, at 8, 16, 20 and 24 rows:
+//              32, 2048, 1408                  61, 65     72, 68     74, 69     75, 70
+//              8, 4096, 7168                  138, 147   157, 150   163, 152   170, 155
+//              64, 2048, 1024                  96, 98    102, 101   112, 103   118, 105
+// So the limit of 8 costs few large FP8 experts 3% at 8 rows and the others up to 5% below it;
+// INT8's of 20 costs 1 to 5% between 13 and 19 rows.
 static ProductPlan plan_product(int fmt, int64_t pairs, int64_t E, int64_t N, int64_t K) {
   struct Tile {
     int wm, wn, mtw, ntw, st, resident;
@@ -830,16 +840,25 @@ ExpertsPlan plan_experts(int fmt, int64_t T, int64_t k, int64_t E, int64_t H, in
   p.fmt = fmt;
   const ExpertRows xr = expert_rows(fmt, H), hr = expert_rows(fmt, I);
   // a pass's activations lie within 32-bit offsets and 1 GiB of workspace
-  const int64_t per_token = xr.ld_codes + xr.ld_scales + k * (hr.ld_codes + hr.ld_scales + 4 * round_up(I, 4) + 4 * round_up(Ho, 32));
+  const int64_t per_pair = hr.ld_codes + hr.ld_scales + 4 * round_up(I, 4) + 4 * round_up(Ho, 32);
+  const int64_t per_token = xr.ld_codes + xr.ld_scales + k * per_pair;
   p.tokens = std::max<int64_t>(1, std::min<int64_t>(T, ((int64_t)1 << 30) / per_token));
   p.pairs = p.tokens * k;
   p.up = plan_product(fmt, p.pairs, E, N, H);
   p.down = plan_product(fmt, p.pairs, E, Ho, I);
-  // A few tokens, every pair for itself: two launches for five, but an expert that several
-  // tokens choose is read for each. 64 experts, 8 a token (block FP8, 2048, 1024 inner):
-  // 1 token 17 us (sorted 32), 4 tokens 37 (52), 8 tokens 63 (69), 12 tokens 89 (80); 8
-  // experts, 2 a token (FP8, 4096, 14336): 1 token 64 (93), 2 tokens 118 (127), 3 tokens
-  // 170 (159); 128 experts, 8 a token (MXFP4, 4096, 1280): 6 tokens 82 (84), 8 tokens 105 (100).
+  // A few tokens, every pair for itself: two launches for four or five, but an expert that
+  // several tokens choose is read for each. A call each way, us (each pair, sorted):
+  //   64 experts, 8 a token, 2048, 1024 inner   1 token   4 tokens   6 tokens   8 tokens
+  //     block FP8                               16, 28    35, 48     48, 57     61, 64
+  //     MXFP8                                   16, 28    37, 47     52, 60     64, 64
+  //     INT8                                    17, 28    38, 49     52, 60     67, 68
+  //     MXFP4                                   14, 24    23, 34     30, 40     38, 42
+  //   64, 6 a token, 4096, 1024 (MXFP8)         20, 33    56, 68     80, 83    103, 100
+  //   128, 8 a token, 4096, 1280 (MXFP4)        20, 31    56, 61     78, 76    102, 97
+  //   32, 4 a token, 2048, 1408 (INT8)          16, 25    29, 37     40, 44     48, 49
+  //   8, 2 a token, 4096, 14336 (FP8)           63, 94     (2 tokens) 119, 132  (3) 167, 150
+  // 4 pairs < 3 experts keeps the last line's 3 tokens out, and the 6 tokens of the first lines
+  // too, where each pair for itself would be 9 to 25% faster.
   p.token = T == 1 || (T <= kTokenMax && p.tokens == T && 4 * p.pairs < 3 * E);
   p.h_quantized = !p.token && p.up.large && fmt != SC_INT8;
   p.counter_bytes = 64 * 1024;

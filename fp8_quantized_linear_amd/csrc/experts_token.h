@@ -4,8 +4,9 @@
 // registers in the packed order, which is the matrix instruction's; all 16 rows of the
 // instruction are the pair's one row. Bound by the weights and the chain of a launch, the
 // loads and the join: one token of 8 in 64 experts (2048, 1024 inner, block FP8, 50 MB of
-// weights) takes 14.6 us (up 8.2, down 7.0 alone, 3.5 TB/s together) where the sorted way
-// takes five launches and 27 us.
+// weights) takes 15.5 us a call where the sorted way takes 27.9; traced up 7.9 and down 6.8,
+// 3.4 TB/s together (FP8 7.7 and 6.7, MXFP8 8.1 and 7.2, MXFP4 5.8 and 6.4, INT8, whose waves
+// read the whole row for its scale, 9.1 and 7.4).
 #pragma once
 
 #include "experts_tile.h"
@@ -108,7 +109,7 @@ __device__ __forceinline__ float row_scale(const X* __restrict__ row, int64_t K)
 // column (lane % 16) of each tile, every row of the instruction being the one. Four
 // chunks are in flight together, the row's before the weights': it is quantized, by all
 // lanes once, while the weights come (each lane loading and quantizing its operand
-// for itself took 20.6 us instead of 14.6 for the token above). No branch but the loop, so
+// for itself took 6 us more for the token above). No branch but the loop, so
 // that nothing is loaded late. codes: 512 bytes of LDS of the wave's own.
 template <int F, int NT, typename X>
 __device__ __forceinline__ void row_product(const X* __restrict__ row, int64_t K, float r, const uint8_t* __restrict__ wcodes,

@@ -13,6 +13,12 @@
 // the product y are float64, y is rounded to float32 once and quantized from that.
 // A row with a value that is not a number or not finite has scale NaN: integers
 // cannot hold it, and the outputs of the row's product become NaN.
+//
+// Bound by memory, and for rows into an operand by its 16-byte pieces: 4096 x 4096 into the
+// operand 12.3 us (50 MB, 4.1 TB/s; the FP8 quantizers, which take 16 rows a wave in the
+// operand's order, 9.5), into plain codes 10.5 traced; the norm with a residual into the
+// operand 8192 x 5120 89 us (294 MB, 3.3 TB/s; block FP8's 64, the bytes alone 59), 4096 x 4096
+// 30 (block FP8's 27, the bytes 24).
 #include "fql_device.h"
 #include "fql_serving.h"
 #include "sc_quant.h"

@@ -22,8 +22,8 @@ import struct
 
 import torch
 
-from . import (FP8BlockWeight, FP8Weight, FQLError, INT8Weight, MXFP4Weight, MXFP8Weight, _CODES, _SCALES, _check,
-               _one_of, _pack_sc, _rows_view, _size_query, fp8_output_scale, fp8_scale_from_amax, lib)
+from . import (FQLError, _CODES, _SCALES, _check, _one_of, _pack_sc, _rows_view, _size_query, fp8_output_scale,
+               fp8_scale_from_amax, lib)
 from . import quant_fp8_block_weight, quant_fp8_weight, quant_int8_weight, quant_mxfp4_weight, quant_mxfp8_weight
 from .serving import (ACTIVATIONS, FORMATS, _bf16, _cuda, _f32, _format, _i32, _new, _query, _rows, _same_device, _stream,
                       _u8, _within, _workspace)
@@ -76,7 +76,6 @@ def route_experts(logits, top_k, score="softmax", bias=None, groups=1, top_group
 # experts
 # ---------------------------------------------------------------------------
 
-_WEIGHTS = {"mxfp4": MXFP4Weight, "mxfp8": MXFP8Weight, "fp8": FP8Weight, "fp8_block": FP8BlockWeight, "int8": INT8Weight}
 _QUANT = {"mxfp4": quant_mxfp4_weight, "mxfp8": quant_mxfp8_weight, "fp8_block": quant_fp8_block_weight,
           "int8": quant_int8_weight}
 

@@ -6,8 +6,9 @@ INT8     per row: s = fl32(max |v| / 127), r = fl32(1 / s) (0 when s = 0, the la
          finite float32 when it overflows), q = rint(fl32(v r)), ties to even; a row
          with a value that is not finite has scale NaN.
 Route    an expert is available where its logit is neither NaN nor -inf (+inf counts
-         as the largest finite float32), and can be chosen where its bias is neither, either. s = softmax over the available experts or the
-         sigmoid. c = s + bias, without a bias the logit. Groups of neighbours: a
+         as the largest finite float32), and can be chosen where its bias is neither,
+         either. s = softmax over the available experts or the sigmoid. c = s + bias,
+         without a bias the logit. Groups of neighbours: a
          group's score is the sum of its two largest c (s without a bias) over available
          experts, a lone one counting alone; only the best `top_groups` groups that have
          an available expert take part. The k largest c, ties to the lowest index;
@@ -20,8 +21,6 @@ Experts  u = x_q Wu_e^T + bu_e, h = fl32(act(u)), d = h_q Wd_e^T + bd_e,
 import math
 
 import numpy as np
-
-from . import serving as S
 
 MAX32 = np.float32(3.4028234663852886e38)
 
@@ -76,7 +75,3 @@ def route(logits, k, score="softmax", bias=None, groups=1, top_groups=1, renorma
             v = v / v.sum() if v.sum() > 0 else 0 * v
         w[t, :len(chosen)], ids[t, :len(chosen)] = v * scale, chosen
     return w, ids
-
-
-def activation(z, act):
-    return S.activation(z, act)
